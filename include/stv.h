@@ -94,6 +94,9 @@ enum stv_dev_status {
   STV_DEV_BAD_ROW = 4,    /* row_seq outside [0, n_seqs) or row_pos negative */
   STV_DEV_BAD_COMMIT = 8, /* n_commit outside [1, T] or path not a root path */
   STV_DEV_TIMEOUT = 16,   /* a bounded wait inside a kernel gave up; outputs are invalid */
+  STV_DEV_BAD_SAMPLE = 32, /* stv_sample: a row without a finite logit, a NaN or +inf logit, a bad parameter */
+  STV_DEV_NO_PAGES = 64,  /* page calls: fewer free pages than the call needs */
+  STV_DEV_BAD_SEQ = 128,  /* page calls: a sequence outside the pool, named twice, or in the wrong state */
 };
 
 enum stv_path { STV_PATH_EXACT = 0, STV_PATH_INT8 = 1 };
@@ -461,6 +464,188 @@ int stv_lookup_workspace_bytes(int n_seqs, size_t* bytes);
 int stv_lookup_draft(const stv_history* hist, int n_seqs, int min_len, int max_len, int k, int32_t* n_prop,
                      int32_t* prop, int32_t* match_len, int64_t* match_pos, void* workspace, size_t ws_bytes,
                      stv_stream_t stream);
+
+/* ======================================================================== */
+/* Around the round: rotary positions before the append, sampling before    */
+/* the acceptance, and the pages of the caches.                             */
+/* ======================================================================== */
+
+/* Element types of stv_rope's rows and stv_sample's logits. */
+enum stv_dtype { STV_F32 = 0, STV_F16 = 1, STV_BF16 = 2 };
+
+/*
+ * Rotary positions with several axes (the pages leave out what precedes the
+ * append; a vision-language target gives every token a position in time, in
+ * height and in width, text tokens the same one on each axis, and a tree
+ * node its context plus its depth).
+ *
+ * The first rotary_dim channels of a head make h = rotary_dim / 2 pairs, pair
+ * i being channels (i, i + h).  Its frequency is f_i = theta^(-2 i /
+ * rotary_dim), its axis a(i): sections[0] pairs of axis 0, then sections[1]
+ * of axis 1 and so on (interleaved 0); or axis i % n_axes where that axis a
+ * is not 0 and i < n_axes * sections[a], else axis 0 (interleaved 1).  With
+ * phi = pos[a(i)][row] * f_i:
+ *     out[i]     = x[i] cos(phi) - x[i + h] sin(phi)
+ *     out[i + h] = x[i + h] cos(phi) + x[i] sin(phi)
+ * and channels from rotary_dim on are copied.  inverse turns by -phi: the
+ * gradient of the call, and what takes a position back out of a row.
+ * Products are formed in fp32 and rounded once; phi is exact to 2^-31 of a
+ * turn for every int32 position, negative ones among them.
+ */
+typedef struct {
+  int32_t rotary_dim;  /* even, 2 .. head_dim */
+  int32_t n_axes;      /* 1 .. 4 */
+  int32_t sections[4]; /* pairs of each axis, >= 0, rotary_dim / 2 in all */
+  int32_t interleaved; /* 0: whole sections in turn; 1: the axes dealt pair by pair */
+  double theta;        /* >= 1 */
+} stv_rope_spec;
+
+/* Rows of heads: element (r, c, x) at data[r * row_stride + c * head_stride +
+ * x], strides in elements; heads and rows do not overlap one another
+ * (head_stride >= head_dim, and row_stride >= the heads' extent). */
+typedef struct {
+  void* data; /* device */
+  int64_t row_stride, head_stride;
+  int32_t heads;
+} stv_rows;
+
+/*
+ *  dtype:    enum stv_dtype, of all four views.   head_dim: 2 .. 512, even.
+ *  pos:      device int32 [n_axes][n_rows].
+ *  q, q_out: input and output views of the same number of heads; k, k_out
+ *            likewise; either pair may be NULL.  An output may be its own
+ *            input (the same data and strides: in place, channels from
+ *            rotary_dim on are then not touched), or lie in other columns of
+ *            the same rows; any other overlap is STV_ERR_INVALID_ARG.
+ * n_rows = 0 enqueues nothing.
+ */
+int stv_rope(const stv_rope_spec* spec, int dtype, int head_dim, const int32_t* pos, int n_rows, const stv_rows* q,
+             const stv_rows* q_out, const stv_rows* k, const stv_rows* k_out, int inverse, stv_stream_t stream);
+
+/*
+ * Sampling from the target's logits ("elpis-lossless" README, "Lossless":
+ * its own acceptance takes the argmax; here the target's token at every tree
+ * node is drawn from the filtered distribution, from given random numbers).
+ * The ids take target_argmax's place in stv_tree_accept: a child is accepted
+ * iff it is the token drawn at its parent, so what the round commits is
+ * distributed as the target's own sampling, whatever proposed the drafts.
+ *
+ * Row r with logits x[0 .. vocab), T = temperature, in the order of x
+ * descending, among equals the lower index first; tokens of -inf are masked
+ * and take no part.  w = exp((x - max x) / T).  Kept are
+ *   the first top_k tokens (all, when top_k < 1);
+ *   of those the shortest head whose w add up to at least top_p times theirs
+ *   (all, when top_p >= 1; one token at least);
+ *   of those the ones with w >= min_p.
+ * The row's token is the first, in that order, whose running sum of kept w
+ * exceeds u times the whole.  T = 0 takes the first token.
+ *
+ * Sums of w are exact sums of 64-bit integers, w having a relative error
+ * below 2^-29 down to 2^-45 of the largest: the result does not depend on the
+ * order in which threads add, and differs from the exact one only where u
+ * falls that close to a border between two tokens.
+ *
+ *  logits:   device, dtype (enum stv_dtype), row r at logits + r * row_stride
+ *            elements; row_stride >= vocab (any alignment of the type).
+ *  temperature, top_k, top_p, min_p: device fp32 / int32 / fp32 / fp32
+ *            [ceil(n_rows / rows_per_param)], entry r / rows_per_param for
+ *            row r (a tree's T rows share their request's); NULL for 1, 0,
+ *            1 and 0.  T = 0 or in [2^-100, 2^60], top_p >= 0, min_p in
+ *            [0, 1].
+ *  u:        device fp32 [n_rows], in [0, 1).
+ *  ids:      device int32 [n_rows].
+ *  logprob:  device fp32 [n_rows] or NULL: ln of the token's share of the
+ *            kept mass.
+ * A row with no finite logit, a NaN or +inf logit, or a bad T, top_p, min_p
+ * or u gets id -1 and logprob -inf, and STV_DEV_BAD_SAMPLE is reported; the
+ * other rows are not affected.  1 <= vocab <= 524,288 (else
+ * STV_ERR_SHAPE_UNSUPPORTED); n_rows = 0 enqueues nothing.
+ */
+int stv_sample(const void* logits, int dtype, int64_t row_stride, int n_rows, int vocab, const float* temperature,
+               const int32_t* top_k, const float* top_p, const float* min_p, int rows_per_param, const float* u,
+               int32_t* ids, float* logprob, int32_t* dev_status, stv_stream_t stream);
+
+/*
+ * The pages of the caches.  The layers' pools share one numbering (a page
+ * number is the same page of every layer), and a page pool keeps the books on
+ * the device, where the calls below change them in stream order without the
+ * host: they can be captured into a graph.
+ *  refs:   device int32 [n_pages]: table entries (of any sequence) that hold
+ *          the page; 0 = free.  A caller may count holders of its own.
+ *  tables: device int32 [max_seqs][table_stride]: the sequences' page tables
+ *          (row s is stv_seq.page_table of sequence s); -1 past counts[s].
+ *  counts: device int32 [max_seqs]: pages that each sequence holds.
+ * An empty pool is refs = 0, tables = -1, counts = 0.  New pages are always
+ * the lowest free ones, so results do not depend on timing.  Every call but
+ * stv_page_compact is all or nothing: when anything that it reads is wrong
+ * (STV_DEV_BAD_SEQ, STV_DEV_BAD_PAGE) or pages are short (STV_DEV_NO_PAGES),
+ * it changes nothing.  1 <= n_pages <= 262,144, 1 <= max_seqs <= 4,096 (else
+ * STV_ERR_SHAPE_UNSUPPORTED); calls on one pool must not overlap.
+ */
+typedef struct {
+  int32_t* refs;
+  int32_t* tables;
+  int32_t* counts;
+  int32_t n_pages, max_seqs, table_stride;
+} stv_page_pool;
+
+/* Workspace of stv_page_fork, stv_page_compact and stv_page_copy (a list of
+ * page copies); no need to clear it.  Calls that overlap on the GPU, graphs
+ * among them, need one each. */
+int stv_page_workspace_bytes(const stv_page_pool* pool, size_t* bytes);
+
+/*
+ * Gives each of the n sequences pages for ctx[s] + extra tokens (a round's
+ * tree rows, a prompt), in the order of the list; a sequence that holds
+ * enough keeps what it has.
+ *  seqs: device int32 [n], distinct.   ctx: device int32 [max_seqs].
+ */
+int stv_page_reserve(const stv_page_pool* pool, const int32_t* seqs, int n, const int32_t* ctx, int extra,
+                     int32_t* dev_status, stv_stream_t stream);
+
+/*
+ * Forks: dst[i] becomes a copy of src[i]'s first ctx tokens.  Full pages are
+ * shared (refs + 1; nothing ever writes them, rows go to positions >= ctx);
+ * a last page of fewer than 256 tokens is copied, in every layer, to a new
+ * page.  ctx[dst[i]] = ctx[src[i]].  Pages that src holds past ctx stay its
+ * own.
+ *  src, dst: device int32 [n]; a source may be named many times; the dst are
+ *            distinct, hold no pages and are no source of the call.
+ *  layers:   host array; every pool has at least pool->n_pages pages.
+ */
+int stv_page_fork(const stv_shape* shape, const stv_layer_cache* layers, int n_layers, const stv_page_pool* pool,
+                  const int32_t* src, const int32_t* dst, int n, int32_t* ctx, void* workspace, size_t ws_bytes,
+                  int32_t* dev_status, stv_stream_t stream);
+
+/* The sequences (device int32 [n], distinct) give up their pages: refs - 1
+ * each, table entries -1, counts 0.  A sequence without pages may be named. */
+int stv_page_free(const stv_page_pool* pool, const int32_t* seqs, int n, int32_t* dev_status, stv_stream_t stream);
+
+/*
+ * Moves the live pages (refs > 0) to the front of every layer's pool: with
+ * n_live of them, the i-th live page from n_live on (in page order) goes to
+ * the i-th free page before n_live; the others stay.  Tables and refs follow.
+ *  map:    device int32 [n_pages], written: where each page went (itself
+ *          when it stayed), -1 for a page that was free.
+ *  n_live: device int32 [1], written.
+ * A table entry outside the pool, or of a free page, is left as it is
+ * (STV_DEV_BAD_PAGE); so are the entries of a sequence whose count is not
+ * within its table (STV_DEV_BAD_SEQ).
+ */
+int stv_page_compact(const stv_shape* shape, const stv_layer_cache* layers, int n_layers, const stv_page_pool* pool,
+                     int32_t* map, int32_t* n_live, void* workspace, size_t ws_bytes, int32_t* dev_status,
+                     stv_stream_t stream);
+
+/*
+ * Copies page src[i] to page dst[i] in every layer; no books are kept.  The
+ * dst are distinct and no dst is a source (STV_DEV_BAD_PAGE, and nothing is
+ * copied); a source may be named many times.
+ *  src, dst: device int32 [n], n <= n_pages, each in [0, n_pages).
+ *  workspace: of a pool of n_pages pages.
+ */
+int stv_page_copy(const stv_shape* shape, const stv_layer_cache* layers, int n_layers, int n_pages,
+                  const int32_t* src, const int32_t* dst, int n, void* workspace, size_t ws_bytes,
+                  int32_t* dev_status, stv_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -27,6 +27,9 @@ STV_DEV_BAD_TREE = 2
 STV_DEV_BAD_ROW = 4
 STV_DEV_BAD_COMMIT = 8
 STV_DEV_TIMEOUT = 16
+STV_DEV_BAD_SAMPLE = 32
+STV_DEV_NO_PAGES = 64
+STV_DEV_BAD_SEQ = 128
 
 STV_KV_BY_GROUP = 0  # group 32: the 3-bit cache; group 256: the int4 per-token-head cache
 STV_KV_K4V2 = 2      # the K 4 / V 2-bit cache (group 32)
@@ -49,7 +52,9 @@ EXPORTS = (
     "stv_verify_attn", "stv_split_combine", "stv_tree_accept", "stv_kv_commit", "stv_int8_qk_dots",
     "stv_verify_attn_no_alloc", "stv_append_verify_attn", "stv_lookup_workspace_bytes", "stv_lookup_draft",
     "stv_prefill_workspace_bytes", "stv_prefill_attn", "stv_verify_attn_timeout_test",
-    "stv_prefill_attn_timeout_test", "stv_append_verify_combine",
+    "stv_prefill_attn_timeout_test", "stv_append_verify_combine", "stv_rope", "stv_sample",
+    "stv_page_workspace_bytes", "stv_page_reserve", "stv_page_fork", "stv_page_free", "stv_page_compact",
+    "stv_page_copy",
 )
 
 
@@ -74,6 +79,21 @@ class stv_history(ctypes.Structure):
 
 class stv_seq(ctypes.Structure):
     _fields_ = [("page_table", ctypes.c_void_p), ("n_pages", ctypes.c_int32), ("ctx", ctypes.c_int32)]
+
+
+class stv_rope_spec(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int32), ("n_axes", ctypes.c_int32), ("sections", ctypes.c_int32 * 4),
+                ("interleaved", ctypes.c_int32), ("theta", ctypes.c_double)]
+
+
+class stv_rows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("row_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("heads", ctypes.c_int32)]
+
+
+class stv_page_pool(ctypes.Structure):
+    _fields_ = [("refs", ctypes.c_void_p), ("tables", ctypes.c_void_p), ("counts", ctypes.c_void_p),
+                ("n_pages", ctypes.c_int32), ("max_seqs", ctypes.c_int32), ("table_stride", ctypes.c_int32)]
 
 
 _lib = None
@@ -123,6 +143,22 @@ def load() -> ctypes.CDLL:
         lib.stv_verify_attn_no_alloc.argtypes = [P, P, P, I, P, P, I, I, P, P, P]
         lib.stv_verify_attn_timeout_test.restype = I
         lib.stv_verify_attn_timeout_test.argtypes = [P, P, P, I, P, P, I, I, P, ctypes.c_size_t, P, P]
+        lib.stv_rope.restype = I
+        lib.stv_rope.argtypes = [P, I, I, P, I, P, P, P, P, I, P]
+        lib.stv_sample.restype = I
+        lib.stv_sample.argtypes = [P, I, I64, I, I, P, P, P, P, I, P, P, P, P, P]
+        lib.stv_page_workspace_bytes.restype = I
+        lib.stv_page_workspace_bytes.argtypes = [P, P]
+        lib.stv_page_reserve.restype = I
+        lib.stv_page_reserve.argtypes = [P, P, I, P, I, P, P]
+        lib.stv_page_fork.restype = I
+        lib.stv_page_fork.argtypes = [P, P, I, P, P, P, I, P, P, ctypes.c_size_t, P, P]
+        lib.stv_page_free.restype = I
+        lib.stv_page_free.argtypes = [P, P, I, P, P]
+        lib.stv_page_compact.restype = I
+        lib.stv_page_compact.argtypes = [P, P, I, P, P, P, P, ctypes.c_size_t, P, P]
+        lib.stv_page_copy.restype = I
+        lib.stv_page_copy.argtypes = [P, P, I, I, P, P, I, P, ctypes.c_size_t, P, P]
         _lib = lib
     return _lib
 
@@ -438,3 +474,215 @@ def stv_prefill_attn_timeout_test(shape, layer: LayerCache, seq, q, n_tokens: in
         ctypes.byref(shape), ctypes.byref(lc), arr, _ptr(q, torch.float16, "q"), int(n_tokens), int(path),
         _ptr(workspace, name="workspace"), workspace.numel() * workspace.element_size(),
         _ptr(o, torch.float16, "o"), _ptr(dev_status, torch.int32, "dev_status"), _stream(stream)))
+
+
+# --------------------------------------------------------------------------
+# around the round: rotary positions, sampling, the pages of the caches
+# --------------------------------------------------------------------------
+
+_DTYPES = None
+
+
+def _dtype_code(dtype, name):
+    global _DTYPES
+    if _DTYPES is None:
+        import torch
+
+        _DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}  # enum stv_dtype
+    try:
+        return _DTYPES[dtype]
+    except KeyError:
+        raise TypeError(f"{name} must be fp32, fp16 or bf16, got {dtype}") from None
+
+
+def _vec(t, dtype, n, name):
+    """A contiguous CUDA vector of n entries."""
+    p = _ptr(t, dtype, name)
+    if t is not None and t.numel() != n:
+        raise ValueError(f"{name} must have {n} entries, got {t.numel()}")
+    return p
+
+
+def _same_device(first, *tensors):
+    """The call's tensors lie on one device, the current one (the kernels are
+    launched there)."""
+    import torch
+
+    dev = first.get_device()
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"tensors on cuda:{dev}, but the current device is cuda:{torch.cuda.current_device()}")
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("tensors on different devices")
+
+
+def make_rope(rotary_dim: int, sections, theta: float = 10000.0, interleaved: bool = False) -> stv_rope_spec:
+    """Rotary positions over rotary_dim channels with len(sections) axes,
+    sections[a] channel pairs each (include/stv.h)."""
+    if not 1 <= len(sections) <= 4:
+        raise ValueError(f"1 to 4 axes, got {len(sections)}")
+    sec = (ctypes.c_int32 * 4)(*[int(n) for n in sections])
+    return stv_rope_spec(int(rotary_dim), len(sections), sec, int(interleaved), float(theta))
+
+
+def _rows(t, n_rows, head_dim, dtype, name):
+    if t.device.type != "cuda" or t.dim() != 3 or t.shape[0] != n_rows or t.shape[2] != head_dim:
+        raise ValueError(f"{name} must be a CUDA tensor [{n_rows}][heads][{head_dim}]")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    row, head, last = t.stride()
+    if last != 1 and head_dim > 1:
+        raise ValueError(f"{name} must have adjacent channels")
+    return stv_rows(t.data_ptr(), row, max(head, head_dim) if t.shape[1] == 1 else head, t.shape[1])
+
+
+def stv_rope(spec: stv_rope_spec, pos, q, q_out, k=None, k_out=None, inverse: bool = False, stream=None):
+    """Rotary positions with several axes: q, k [n_rows][heads][head_dim]
+    (fp32, fp16 or bf16; any row and head strides) turned by pos, int32
+    [n_axes][n_rows], into q_out, k_out (the input itself: in place).  q or k
+    may be None.  inverse: the gradient, by the opposite angles."""
+    import torch
+
+    first = q if q is not None else k
+    if first is None or (q is None) != (q_out is None) or (k is None) != (k_out is None):
+        raise ValueError("q with q_out, k with k_out, or both pairs")
+    n, _, hd = first.shape
+    if tuple(pos.shape) != (spec.n_axes, n):
+        raise ValueError(f"pos must be [{spec.n_axes}][{n}], got {tuple(pos.shape)}")
+    _same_device(first, pos, q, q_out, k, k_out)
+    views = [None if t is None else _rows(t, n, hd, first.dtype, name)
+             for t, name in ((q, "q"), (q_out, "q_out"), (k, "k"), (k_out, "k_out"))]
+    _check("stv_rope", load().stv_rope(
+        ctypes.byref(spec), _dtype_code(first.dtype, "q"), hd, _ptr(pos, torch.int32, "pos"), n,
+        *[None if v is None else ctypes.byref(v) for v in views], int(bool(inverse)), _stream(stream)))
+
+
+def stv_sample(logits, u, ids, logprob=None, temperature=None, top_k=None, top_p=None, min_p=None,
+               rows_per_param: int = 1, dev_status=None, stream=None):
+    """One token per row of logits [n_rows][vocab] (fp32, fp16 or bf16, rows
+    any distance apart), drawn with u [n_rows] in [0, 1) from the row's
+    distribution under temperature, top_k, top_p and min_p, one entry of each
+    for rows_per_param rows (None: 1, all, 1, 0); ids int32 [n_rows], logprob
+    fp32 [n_rows] or None (include/stv.h)."""
+    import torch
+
+    if logits.device.type != "cuda" or logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError("logits must be a CUDA tensor [n_rows][vocab] with adjacent columns")
+    n, vocab = logits.shape
+    rpp = int(rows_per_param)
+    if rpp < 1:
+        raise ValueError(f"rows_per_param must be at least 1, got {rpp}")
+    m = -(-n // rpp)
+    _same_device(logits, u, ids, logprob, temperature, top_k, top_p, min_p, dev_status)
+    f32, i32 = torch.float32, torch.int32
+    _check("stv_sample", load().stv_sample(
+        logits.data_ptr(), _dtype_code(logits.dtype, "logits"), logits.stride(0) if n > 1 else vocab, n, vocab,
+        _vec(temperature, f32, m, "temperature"), _vec(top_k, i32, m, "top_k"), _vec(top_p, f32, m, "top_p"),
+        _vec(min_p, f32, m, "min_p"), rpp, _vec(u, f32, n, "u"), _vec(ids, i32, n, "ids"),
+        _vec(logprob, f32, n, "logprob"), _ptr(dev_status, i32, "dev_status"), _stream(stream)))
+
+
+class PagePool:
+    """The books of a page pool (include/stv.h): refs int32 [n_pages], tables
+    int32 [max_seqs][table_stride], counts int32 [max_seqs], on the device."""
+
+    def __init__(self, refs, tables, counts):
+        import torch
+
+        if tables.dim() != 2 or refs.dim() != 1:
+            raise ValueError("refs must be [n_pages], tables [max_seqs][table_stride]")
+        _same_device(refs, tables, counts)
+        self.refs, self.tables, self.counts = refs, tables, counts
+        self._c = stv_page_pool(_ptr(refs, torch.int32, "refs").value, _ptr(tables, torch.int32, "tables").value,
+                                _vec(counts, torch.int32, tables.shape[0], "counts").value, refs.numel(),
+                                tables.shape[0], tables.shape[1])
+
+    @classmethod
+    def empty(cls, n_pages: int, max_seqs: int, table_stride: int, device="cuda"):
+        """All pages free, no sequence holding any."""
+        import torch
+
+        z = lambda *shape: torch.zeros(shape, dtype=torch.int32, device=device)
+        return cls(z(n_pages), torch.full((max_seqs, table_stride), -1, dtype=torch.int32, device=device), z(max_seqs))
+
+    def c(self) -> stv_page_pool:
+        return self._c
+
+    def seq(self, s: int, n_pages: int, ctx: int) -> Seq:
+        """Sequence s as the round's calls take it: the first n_pages of its
+        table, ctx cached tokens."""
+        return Seq(self.tables[s, :n_pages], ctx)
+
+
+def _layer_array(layers):
+    arr = (stv_layer_cache * len(layers))()
+    for i, l in enumerate(layers):
+        arr[i] = l.c()
+    return arr
+
+
+def stv_page_workspace_bytes(pool: PagePool) -> int:
+    out = ctypes.c_size_t()
+    _check("stv_page_workspace_bytes", load().stv_page_workspace_bytes(ctypes.byref(pool.c()), ctypes.byref(out)))
+    return out.value
+
+
+def stv_page_reserve(pool: PagePool, seqs, ctx, extra: int, dev_status=None, stream=None):
+    """Pages for ctx[s] + extra tokens for every sequence of the list (int32
+    CUDA tensor); ctx int32 [max_seqs] on the device."""
+    import torch
+
+    _same_device(pool.refs, seqs, ctx, dev_status)
+    _check("stv_page_reserve", load().stv_page_reserve(
+        ctypes.byref(pool.c()), _ptr(seqs, torch.int32, "seqs"), seqs.numel(),
+        _vec(ctx, torch.int32, pool.c().max_seqs, "ctx"), int(extra), _ptr(dev_status, torch.int32, "dev_status"),
+        _stream(stream)))
+
+
+def stv_page_free(pool: PagePool, seqs, dev_status=None, stream=None):
+    """The listed sequences give up their pages."""
+    import torch
+
+    _same_device(pool.refs, seqs, dev_status)
+    _check("stv_page_free", load().stv_page_free(
+        ctypes.byref(pool.c()), _ptr(seqs, torch.int32, "seqs"), seqs.numel(),
+        _ptr(dev_status, torch.int32, "dev_status"), _stream(stream)))
+
+
+def stv_page_fork(shape, layers, pool: PagePool, src, dst, ctx, workspace, dev_status=None, stream=None):
+    """Sequence dst[i] becomes a copy of src[i]'s first ctx tokens: full pages
+    shared, the last partial page copied in every layer; ctx[dst] is set."""
+    import torch
+
+    _same_device(pool.refs, src, dst, ctx, workspace, dev_status)
+    _check("stv_page_fork", load().stv_page_fork(
+        ctypes.byref(shape), _layer_array(layers), len(layers), ctypes.byref(pool.c()),
+        _ptr(src, torch.int32, "src"), _vec(dst, torch.int32, src.numel(), "dst"), src.numel(),
+        _vec(ctx, torch.int32, pool.c().max_seqs, "ctx"), _ptr(workspace, name="workspace"),
+        workspace.numel() * workspace.element_size(), _ptr(dev_status, torch.int32, "dev_status"), _stream(stream)))
+
+
+def stv_page_compact(shape, layers, pool: PagePool, page_map, n_live, workspace, dev_status=None, stream=None):
+    """Live pages move to the front of every layer's pool, tables and refs
+    with them; page_map int32 [n_pages] and n_live int32 [1] are written."""
+    import torch
+
+    _same_device(pool.refs, page_map, n_live, workspace, dev_status)
+    _check("stv_page_compact", load().stv_page_compact(
+        ctypes.byref(shape), _layer_array(layers), len(layers), ctypes.byref(pool.c()),
+        _vec(page_map, torch.int32, pool.c().n_pages, "page_map"), _vec(n_live, torch.int32, 1, "n_live"),
+        _ptr(workspace, name="workspace"), workspace.numel() * workspace.element_size(),
+        _ptr(dev_status, torch.int32, "dev_status"), _stream(stream)))
+
+
+def stv_page_copy(shape, layers, src, dst, workspace, dev_status=None, stream=None):
+    """Page src[i] to page dst[i] in every layer (int32 CUDA tensors); the
+    workspace is one of a pool of as many pages as the smallest layer's."""
+    import torch
+
+    _same_device(workspace, src, dst, dev_status)
+    _check("stv_page_copy", load().stv_page_copy(
+        ctypes.byref(shape), _layer_array(layers), len(layers), min(l.n_pages for l in layers),
+        _ptr(src, torch.int32, "src"), _vec(dst, torch.int32, src.numel(), "dst"), src.numel(),
+        _ptr(workspace, name="workspace"), workspace.numel() * workspace.element_size(),
+        _ptr(dev_status, torch.int32, "dev_status"), _stream(stream)))

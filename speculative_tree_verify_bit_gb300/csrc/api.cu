@@ -9,7 +9,7 @@
 
 namespace stv {
 
-static int check_shape(const stv_shape* sh, int t_nodes, ShapeInfo* out) {
+int check_shape(const stv_shape* sh, int t_nodes, ShapeInfo* out) {
   if (!sh) return STV_ERR_INVALID_ARG;
   if (sh->head_dim != kHeadDim || sh->page_tokens != kPageTok) return STV_ERR_SHAPE_UNSUPPORTED;
   if (sh->group != kGroup && sh->group != kGroupI4) return STV_ERR_SHAPE_UNSUPPORTED;
@@ -32,7 +32,7 @@ static int check_shape(const stv_shape* sh, int t_nodes, ShapeInfo* out) {
   return STV_OK;
 }
 
-static int check_layer(const stv_layer_cache* l, const ShapeInfo& sh) {
+int check_layer(const stv_layer_cache* l, const ShapeInfo& sh) {
   if (!l || !l->pool || l->n_pages < 1) return STV_ERR_INVALID_ARG;
   if (l->page_bytes != (int64_t)sh.hkv * (sh.fmt == kFmtInt4 ? kI4HeadBytes : kHeadBytes)) return STV_ERR_SHAPE_UNSUPPORTED;
   return STV_OK;
@@ -50,7 +50,7 @@ static int check_seqs(const stv_seq* seqs, int n_seqs, int need_keys) {
   return STV_OK;
 }
 
-static int device_sm_count(int* n) {
+int device_sm_count(int* n) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return STV_ERR_CUDA;
   if (cudaDeviceGetAttribute(n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return STV_ERR_CUDA;

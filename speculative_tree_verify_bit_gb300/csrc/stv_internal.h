@@ -252,6 +252,9 @@ cudaError_t launch_pdl_coop(void (*kernel)(KArgs...), int grid, int block, size_
 }
 
 // ---- host helpers (api.cu) ----
+int check_shape(const stv_shape* sh, int t_nodes, ShapeInfo* out);  // t_nodes < 0: no round
+int check_layer(const stv_layer_cache* l, const ShapeInfo& sh);
+int device_sm_count(int* n);
 int make_plan(const ShapeInfo& sh, const stv_seq* seqs, int n_seqs, int sm_count, Plan* plan, bool balance);
 WsLayout ws_layout(const ShapeInfo& sh, int n_seqs, const Plan& plan);
 
