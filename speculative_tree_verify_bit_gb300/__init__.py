@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libstv.so")
@@ -480,40 +481,63 @@ def stv_prefill_attn_timeout_test(shape, layer: LayerCache, seq, q, n_tokens: in
 # around the round: rotary positions, sampling, the pages of the caches
 # --------------------------------------------------------------------------
 
-_DTYPES = None
+# These calls take a few microseconds on the GPU, so the marshalling is kept
+# short: raw pointers and packed structs, torch imported once.
+_torch = None
+_ROWS = struct.Struct("@Pqqi4x")  # stv_rows
+_DTYPES = {}
+
+
+def _t():
+    global _torch
+    if _torch is None:
+        import torch
+
+        _DTYPES.update({torch.float32: 0, torch.float16: 1, torch.bfloat16: 2})  # enum stv_dtype
+        _torch = torch
+    return _torch
+
+
+def _device_of(t, name):
+    """The CUDA device of the call, which is the current one (the kernels are
+    launched there)."""
+    torch = _t()
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    dev, cur = t.get_device(), torch.cuda.current_device()
+    if dev != cur:
+        raise ValueError(f"{name} is on cuda:{dev}, but the current device is cuda:{cur}")
+    return dev
+
+
+def _raw(t, dtype, dev, name, n=None):
+    """Address of a contiguous tensor of the call's device (None: no tensor),
+    of n entries where n is given."""
+    if t is None:
+        return None
+    if not isinstance(t, _torch.Tensor) or t.get_device() != dev:
+        raise (TypeError if not isinstance(t, _torch.Tensor) or not t.is_cuda else ValueError)(
+            f"{name} must be a CUDA tensor on cuda:{dev}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if n is not None and t.numel() != n:
+        raise ValueError(f"{name} must have {n} entries, got {t.numel()}")
+    return t.data_ptr()
+
+
+def _raw_stream(stream, dev):
+    if stream is None:
+        return _torch._C._cuda_getCurrentRawStream(dev)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _dtype_code(dtype, name):
-    global _DTYPES
-    if _DTYPES is None:
-        import torch
-
-        _DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}  # enum stv_dtype
     try:
         return _DTYPES[dtype]
     except KeyError:
         raise TypeError(f"{name} must be fp32, fp16 or bf16, got {dtype}") from None
-
-
-def _vec(t, dtype, n, name):
-    """A contiguous CUDA vector of n entries."""
-    p = _ptr(t, dtype, name)
-    if t is not None and t.numel() != n:
-        raise ValueError(f"{name} must have {n} entries, got {t.numel()}")
-    return p
-
-
-def _same_device(first, *tensors):
-    """The call's tensors lie on one device, the current one (the kernels are
-    launched there)."""
-    import torch
-
-    dev = first.get_device()
-    if dev != torch.cuda.current_device():
-        raise ValueError(f"tensors on cuda:{dev}, but the current device is cuda:{torch.cuda.current_device()}")
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError("tensors on different devices")
 
 
 def make_rope(rotary_dim: int, sections, theta: float = 10000.0, interleaved: bool = False) -> stv_rope_spec:
@@ -525,15 +549,22 @@ def make_rope(rotary_dim: int, sections, theta: float = 10000.0, interleaved: bo
     return stv_rope_spec(int(rotary_dim), len(sections), sec, int(interleaved), float(theta))
 
 
-def _rows(t, n_rows, head_dim, dtype, name):
-    if t.device.type != "cuda" or t.dim() != 3 or t.shape[0] != n_rows or t.shape[2] != head_dim:
-        raise ValueError(f"{name} must be a CUDA tensor [{n_rows}][heads][{head_dim}]")
+def _rows(t, n_rows, head_dim, dtype, dev, name):
+    if t is None:
+        return None
+    if not isinstance(t, _torch.Tensor) or t.get_device() != dev:
+        raise (TypeError if not isinstance(t, _torch.Tensor) or not t.is_cuda else ValueError)(
+            f"{name} must be a CUDA tensor on cuda:{dev}")
+    shape = t.shape
+    if len(shape) != 3 or shape[0] != n_rows or shape[2] != head_dim:
+        raise ValueError(f"{name} must be [{n_rows}][heads][{head_dim}], got {list(shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     row, head, last = t.stride()
     if last != 1 and head_dim > 1:
         raise ValueError(f"{name} must have adjacent channels")
-    return stv_rows(t.data_ptr(), row, max(head, head_dim) if t.shape[1] == 1 else head, t.shape[1])
+    heads = shape[1]
+    return _ROWS.pack(t.data_ptr(), row, head if heads > 1 or head >= head_dim else head_dim, heads)
 
 
 def stv_rope(spec: stv_rope_spec, pos, q, q_out, k=None, k_out=None, inverse: bool = False, stream=None):
@@ -541,20 +572,23 @@ def stv_rope(spec: stv_rope_spec, pos, q, q_out, k=None, k_out=None, inverse: bo
     (fp32, fp16 or bf16; any row and head strides) turned by pos, int32
     [n_axes][n_rows], into q_out, k_out (the input itself: in place).  q or k
     may be None.  inverse: the gradient, by the opposite angles."""
-    import torch
-
+    torch = _t()
     first = q if q is not None else k
     if first is None or (q is None) != (q_out is None) or (k is None) != (k_out is None):
         raise ValueError("q with q_out, k with k_out, or both pairs")
+    dev = _device_of(first, "q")
+    if first.dim() != 3:
+        raise ValueError("q and k must be [n_rows][heads][head_dim]")
     n, _, hd = first.shape
+    dt = first.dtype
     if tuple(pos.shape) != (spec.n_axes, n):
-        raise ValueError(f"pos must be [{spec.n_axes}][{n}], got {tuple(pos.shape)}")
-    _same_device(first, pos, q, q_out, k, k_out)
-    views = [None if t is None else _rows(t, n, hd, first.dtype, name)
-             for t, name in ((q, "q"), (q_out, "q_out"), (k, "k"), (k_out, "k_out"))]
-    _check("stv_rope", load().stv_rope(
-        ctypes.byref(spec), _dtype_code(first.dtype, "q"), hd, _ptr(pos, torch.int32, "pos"), n,
-        *[None if v is None else ctypes.byref(v) for v in views], int(bool(inverse)), _stream(stream)))
+        raise ValueError(f"pos must be [{spec.n_axes}][{n}], got {list(pos.shape)}")
+    rc = load().stv_rope(
+        ctypes.byref(spec), _dtype_code(dt, "q"), hd, _raw(pos, torch.int32, dev, "pos"), n,
+        _rows(q, n, hd, dt, dev, "q"), _rows(q_out, n, hd, dt, dev, "q_out"), _rows(k, n, hd, dt, dev, "k"),
+        _rows(k_out, n, hd, dt, dev, "k_out"), 1 if inverse else 0, _raw_stream(stream, dev))
+    if rc:
+        raise StvError("stv_rope", rc)
 
 
 def stv_sample(logits, u, ids, logprob=None, temperature=None, top_k=None, top_p=None, min_p=None,
@@ -564,44 +598,46 @@ def stv_sample(logits, u, ids, logprob=None, temperature=None, top_k=None, top_p
     distribution under temperature, top_k, top_p and min_p, one entry of each
     for rows_per_param rows (None: 1, all, 1, 0); ids int32 [n_rows], logprob
     fp32 [n_rows] or None (include/stv.h)."""
-    import torch
-
-    if logits.device.type != "cuda" or logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
-        raise ValueError("logits must be a CUDA tensor [n_rows][vocab] with adjacent columns")
+    torch = _t()
+    dev = _device_of(logits, "logits")
+    if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError("logits must be [n_rows][vocab] with adjacent columns")
     n, vocab = logits.shape
     rpp = int(rows_per_param)
     if rpp < 1:
         raise ValueError(f"rows_per_param must be at least 1, got {rpp}")
     m = -(-n // rpp)
-    _same_device(logits, u, ids, logprob, temperature, top_k, top_p, min_p, dev_status)
     f32, i32 = torch.float32, torch.int32
-    _check("stv_sample", load().stv_sample(
+    rc = load().stv_sample(
         logits.data_ptr(), _dtype_code(logits.dtype, "logits"), logits.stride(0) if n > 1 else vocab, n, vocab,
-        _vec(temperature, f32, m, "temperature"), _vec(top_k, i32, m, "top_k"), _vec(top_p, f32, m, "top_p"),
-        _vec(min_p, f32, m, "min_p"), rpp, _vec(u, f32, n, "u"), _vec(ids, i32, n, "ids"),
-        _vec(logprob, f32, n, "logprob"), _ptr(dev_status, i32, "dev_status"), _stream(stream)))
+        _raw(temperature, f32, dev, "temperature", m), _raw(top_k, i32, dev, "top_k", m),
+        _raw(top_p, f32, dev, "top_p", m), _raw(min_p, f32, dev, "min_p", m), rpp, _raw(u, f32, dev, "u", n),
+        _raw(ids, i32, dev, "ids", n), _raw(logprob, f32, dev, "logprob", n),
+        _raw(dev_status, i32, dev, "dev_status"), _raw_stream(stream, dev))
+    if rc:
+        raise StvError("stv_sample", rc)
 
 
 class PagePool:
     """The books of a page pool (include/stv.h): refs int32 [n_pages], tables
-    int32 [max_seqs][table_stride], counts int32 [max_seqs], on the device."""
+    int32 [max_seqs][table_stride], counts int32 [max_seqs], on the device.
+    The pool holds the tensors; give it others only by making another pool."""
 
     def __init__(self, refs, tables, counts):
-        import torch
-
+        i32 = _t().int32
         if tables.dim() != 2 or refs.dim() != 1:
             raise ValueError("refs must be [n_pages], tables [max_seqs][table_stride]")
-        _same_device(refs, tables, counts)
+        self._dev = dev = _device_of(refs, "refs")
         self.refs, self.tables, self.counts = refs, tables, counts
-        self._c = stv_page_pool(_ptr(refs, torch.int32, "refs").value, _ptr(tables, torch.int32, "tables").value,
-                                _vec(counts, torch.int32, tables.shape[0], "counts").value, refs.numel(),
-                                tables.shape[0], tables.shape[1])
+        m, stride = tables.shape
+        self._c = stv_page_pool(_raw(refs, i32, dev, "refs"), _raw(tables, i32, dev, "tables"),
+                                _raw(counts, i32, dev, "counts", m), refs.numel(), m, stride)
+        self._ref = ctypes.byref(self._c)
 
     @classmethod
     def empty(cls, n_pages: int, max_seqs: int, table_stride: int, device="cuda"):
         """All pages free, no sequence holding any."""
-        import torch
-
+        torch = _t()
         z = lambda *shape: torch.zeros(shape, dtype=torch.int32, device=device)
         return cls(z(n_pages), torch.full((max_seqs, table_stride), -1, dtype=torch.int32, device=device), z(max_seqs))
 
@@ -613,76 +649,85 @@ class PagePool:
         table, ctx cached tokens."""
         return Seq(self.tables[s, :n_pages], ctx)
 
+    def _on_current(self):
+        cur = _t().cuda.current_device()
+        if cur != self._dev:
+            raise ValueError(f"the pool is on cuda:{self._dev}, but the current device is cuda:{cur}")
+        return self._dev
 
-def _layer_array(layers):
-    arr = (stv_layer_cache * len(layers))()
-    for i, l in enumerate(layers):
-        arr[i] = l.c()
-    return arr
+
+def _layer_array(layers, dev):
+    """The layers' stv_layer_cache array, packed."""
+    flat = []
+    for l in layers:
+        if l.pool.get_device() != dev or not l.pool.is_contiguous():
+            raise ValueError(f"the layers' pools must be contiguous CUDA tensors on cuda:{dev}")
+        flat += (l.pool.data_ptr(), l.page_bytes, l.n_pages)
+    return struct.pack("@" + "Pqi4x" * len(layers), *flat)
 
 
 def stv_page_workspace_bytes(pool: PagePool) -> int:
     out = ctypes.c_size_t()
-    _check("stv_page_workspace_bytes", load().stv_page_workspace_bytes(ctypes.byref(pool.c()), ctypes.byref(out)))
+    _check("stv_page_workspace_bytes", load().stv_page_workspace_bytes(pool._ref, ctypes.byref(out)))
     return out.value
 
 
 def stv_page_reserve(pool: PagePool, seqs, ctx, extra: int, dev_status=None, stream=None):
     """Pages for ctx[s] + extra tokens for every sequence of the list (int32
     CUDA tensor); ctx int32 [max_seqs] on the device."""
-    import torch
-
-    _same_device(pool.refs, seqs, ctx, dev_status)
-    _check("stv_page_reserve", load().stv_page_reserve(
-        ctypes.byref(pool.c()), _ptr(seqs, torch.int32, "seqs"), seqs.numel(),
-        _vec(ctx, torch.int32, pool.c().max_seqs, "ctx"), int(extra), _ptr(dev_status, torch.int32, "dev_status"),
-        _stream(stream)))
+    dev, i32 = pool._on_current(), _torch.int32
+    rc = load().stv_page_reserve(
+        pool._ref, _raw(seqs, i32, dev, "seqs"), seqs.numel(), _raw(ctx, i32, dev, "ctx", pool._c.max_seqs),
+        int(extra), _raw(dev_status, i32, dev, "dev_status"), _raw_stream(stream, dev))
+    if rc:
+        raise StvError("stv_page_reserve", rc)
 
 
 def stv_page_free(pool: PagePool, seqs, dev_status=None, stream=None):
     """The listed sequences give up their pages."""
-    import torch
-
-    _same_device(pool.refs, seqs, dev_status)
-    _check("stv_page_free", load().stv_page_free(
-        ctypes.byref(pool.c()), _ptr(seqs, torch.int32, "seqs"), seqs.numel(),
-        _ptr(dev_status, torch.int32, "dev_status"), _stream(stream)))
+    dev, i32 = pool._on_current(), _torch.int32
+    rc = load().stv_page_free(pool._ref, _raw(seqs, i32, dev, "seqs"), seqs.numel(),
+                              _raw(dev_status, i32, dev, "dev_status"), _raw_stream(stream, dev))
+    if rc:
+        raise StvError("stv_page_free", rc)
 
 
 def stv_page_fork(shape, layers, pool: PagePool, src, dst, ctx, workspace, dev_status=None, stream=None):
     """Sequence dst[i] becomes a copy of src[i]'s first ctx tokens: full pages
     shared, the last partial page copied in every layer; ctx[dst] is set."""
-    import torch
-
-    _same_device(pool.refs, src, dst, ctx, workspace, dev_status)
-    _check("stv_page_fork", load().stv_page_fork(
-        ctypes.byref(shape), _layer_array(layers), len(layers), ctypes.byref(pool.c()),
-        _ptr(src, torch.int32, "src"), _vec(dst, torch.int32, src.numel(), "dst"), src.numel(),
-        _vec(ctx, torch.int32, pool.c().max_seqs, "ctx"), _ptr(workspace, name="workspace"),
-        workspace.numel() * workspace.element_size(), _ptr(dev_status, torch.int32, "dev_status"), _stream(stream)))
+    dev, i32 = pool._on_current(), _torch.int32
+    n = src.numel()
+    rc = load().stv_page_fork(
+        ctypes.byref(shape), _layer_array(layers, dev), len(layers), pool._ref, _raw(src, i32, dev, "src"),
+        _raw(dst, i32, dev, "dst", n), n, _raw(ctx, i32, dev, "ctx", pool._c.max_seqs),
+        _raw(workspace, None, dev, "workspace"), workspace.nbytes, _raw(dev_status, i32, dev, "dev_status"),
+        _raw_stream(stream, dev))
+    if rc:
+        raise StvError("stv_page_fork", rc)
 
 
 def stv_page_compact(shape, layers, pool: PagePool, page_map, n_live, workspace, dev_status=None, stream=None):
     """Live pages move to the front of every layer's pool, tables and refs
     with them; page_map int32 [n_pages] and n_live int32 [1] are written."""
-    import torch
-
-    _same_device(pool.refs, page_map, n_live, workspace, dev_status)
-    _check("stv_page_compact", load().stv_page_compact(
-        ctypes.byref(shape), _layer_array(layers), len(layers), ctypes.byref(pool.c()),
-        _vec(page_map, torch.int32, pool.c().n_pages, "page_map"), _vec(n_live, torch.int32, 1, "n_live"),
-        _ptr(workspace, name="workspace"), workspace.numel() * workspace.element_size(),
-        _ptr(dev_status, torch.int32, "dev_status"), _stream(stream)))
+    dev, i32 = pool._on_current(), _torch.int32
+    rc = load().stv_page_compact(
+        ctypes.byref(shape), _layer_array(layers, dev), len(layers), pool._ref,
+        _raw(page_map, i32, dev, "page_map", pool._c.n_pages), _raw(n_live, i32, dev, "n_live", 1),
+        _raw(workspace, None, dev, "workspace"), workspace.nbytes, _raw(dev_status, i32, dev, "dev_status"),
+        _raw_stream(stream, dev))
+    if rc:
+        raise StvError("stv_page_compact", rc)
 
 
 def stv_page_copy(shape, layers, src, dst, workspace, dev_status=None, stream=None):
     """Page src[i] to page dst[i] in every layer (int32 CUDA tensors); the
     workspace is one of a pool of as many pages as the smallest layer's."""
-    import torch
-
-    _same_device(workspace, src, dst, dev_status)
-    _check("stv_page_copy", load().stv_page_copy(
-        ctypes.byref(shape), _layer_array(layers), len(layers), min(l.n_pages for l in layers),
-        _ptr(src, torch.int32, "src"), _vec(dst, torch.int32, src.numel(), "dst"), src.numel(),
-        _ptr(workspace, name="workspace"), workspace.numel() * workspace.element_size(),
-        _ptr(dev_status, torch.int32, "dev_status"), _stream(stream)))
+    i32 = _t().int32
+    dev = _device_of(workspace, "workspace")
+    n = src.numel()
+    rc = load().stv_page_copy(
+        ctypes.byref(shape), _layer_array(layers, dev), len(layers), min(l.n_pages for l in layers),
+        _raw(src, i32, dev, "src"), _raw(dst, i32, dev, "dst", n), n, _raw(workspace, None, dev, "workspace"),
+        workspace.nbytes, _raw(dev_status, i32, dev, "dev_status"), _raw_stream(stream, dev))
+    if rc:
+        raise StvError("stv_page_copy", rc)

@@ -137,6 +137,23 @@ cudaError_t launch_rope(RopeParams& p, bool copy_rest, cudaStream_t s) {
   return launch_pdl(rope_kernel<T, VE, 1>, (int)grid, kThreads, 0, s, p);
 }
 
+// Every pair's frequency in turns per position, 2^64 a turn.  The last ones
+// this thread made are kept: a model's layers ask for the same ones.
+const uint64_t* turns_of(double theta, int rotary_dim) {
+  static thread_local struct {
+    double theta;
+    int rotary_dim = 0;
+    uint64_t turn[kMaxPairs];
+  } memo;
+  if (memo.rotary_dim != rotary_dim || memo.theta != theta) {
+    for (int i = 0; i < rotary_dim / 2; ++i)
+      memo.turn[i] = (uint64_t)ldexp(pow(theta, -2.0 * i / rotary_dim) * 0.15915494309189533577, 64);
+    memo.theta = theta;
+    memo.rotary_dim = rotary_dim;
+  }
+  return memo.turn;
+}
+
 bool rows_ok(const stv_rows* v, int head_dim, int n_rows) {
   if (!v->data || v->heads < 1 || v->heads > 1 << 16 || v->head_stride < head_dim) return false;
   // an extent of at most 2^50 bytes, so that no offset below overflows
@@ -227,9 +244,8 @@ extern "C" int stv_rope(const stv_rope_spec* spec, int dtype, int head_dim, cons
       if (t < u && out[t] && out[u] && may_meet(out[t], out[u], head_dim, n_rows, es)) return STV_ERR_INVALID_ARG;
     }
 
+  memcpy(p.turn, turns_of(spec->theta, spec->rotary_dim), (size_t)half * sizeof(uint64_t));
   for (int i = 0; i < half; ++i) {
-    const double f = pow(spec->theta, -2.0 * i / spec->rotary_dim) * 0.15915494309189533577;  // turns per position
-    p.turn[i] = (uint64_t)ldexp(f, 64);
     int axis = 0;
     if (spec->interleaved) {
       axis = i % na;
