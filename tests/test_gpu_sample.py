@@ -28,6 +28,7 @@ def draw(logits, u, t=None, k=None, p=None, m=None, rpp=1, status=None):
 
 def check(logits, u, t=None, k=None, p=None, m=None, rpp=1):
     ids, lp = draw(logits, u, t, k, p, m, rpp)
+    lp = lp.astype(np.float64)  # the differences below in 64 bits
     x, us = logits.double().cpu().numpy(), u.cpu().numpy()
     at = lambda v, r, d: d if v is None else v[r // rpp]
     for r in range(len(us)):
