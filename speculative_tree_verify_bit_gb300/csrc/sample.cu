@@ -6,7 +6,7 @@
 // vocabulary is needed.  A cluster of CTAs shares a row, each CTA a stretch of
 // it, and sweeps it up to three times (the first time from HBM, then from L2):
 //   1. the maximum (a NaN shows in it);
-//      then one vector in kSample, counted by quarter octaves of w, tells how
+//      then some 8,192 tokens, counted by quarter octaves of w, tells how
 //      far down the order the cuts lie: x >= x_cut, the row's head;
 //   2. the mass of all tokens (unless top-k makes it unneeded), and of the
 //      head either the tokens themselves, when they are few, or their counts
@@ -43,10 +43,12 @@ constexpr int kBins = 2048;
 constexpr int kBinsPer = kBins / kThreads;
 constexpr int kList = 2048;      // tokens gathered around the cuts
 constexpr int kDirect = 1400;    // a head estimated at this many tokens is gathered at once
+constexpr float kLeastHead = 512.f;
 constexpr int kCoarse = 256;     // quarter octaves of the sample
 constexpr int kMaxVocab = 1 << 19;
 constexpr int kShift = 14;       // w < 2^45: 2^19 tokens stay below 2^64
 constexpr int kMaxCluster = 8;
+constexpr int kStages = 4;       // one being read, three on their way
 
 struct SampleParams {
   const void* x;
@@ -69,22 +71,49 @@ struct SampleParams {
 struct Decision {
   int done;
   int kb, pb1, pb2, mb, ub1, ub2;  // bins to gather; empty ranges where a cut is not made
+
+  __device__ bool wanted(int b) const {
+    return b == kb || (b >= pb1 && b <= pb2) || b == mb || (b >= ub1 && b <= ub2);
+  }
+};
+
+// A row's temperature and maximum as the weights need them.
+struct Scale {
+  float max;
+  float floor;  // below it w = 0 (62 octaves under the maximum)
+  float base;   // 0; the maximum where x / C would leave the integers of fp32: there
+                // x - max is exact for every x >= floor
+  float least;  // rint(x / C) of the floor, as kMagic + k: smaller ones count as it
+  float inv_c, c_hi, c_lo, inv_t;
+  int top;          // octave of the maximum
+  float cut;        // the head: x >= cut
+  float bin_scale;  // bins of the head, from the maximum down
+  float x_min;      // the least x that min_p keeps
 };
 
 struct Smem {
   u64 tot_mass[kBins];  // first CTA: the row's bins, then of each and all before
-  u64 mass[kBins];      // this CTA's bins; first CTA later: running mass over the list
+  u64 mass[kBins];      // this CTA's bins (low and high words apart); first CTA later:
+                        // running mass over the list
   u64 list[kList];      // (~key << 32) | index
   uint32_t tot_count[kBins];
   uint32_t count[kBins];  // this CTA's bins; first CTA later: a bin's first place in the list
+  uint4 ring[kStages][kThreads];  // vectors on their way in, a thread's own slots
+  u64 queue[kThreads / 32][64];   // a warp's tokens of the head, taken 32 at a time
   uint32_t coarse[kCoarse];
-  float coarse_est[kCoarse];
+  uint32_t coarse_all[kCoarse];
   uint32_t table[64];
   float table_f[64];
   u64 red[kThreads / 32];
-  u64 out, part;  // part: this CTA's share of the row's mass
-  float max;
-  int x_index;    // greedy: the maximum's first index in this CTA's stretch
+  u64 out;
+  double log_kept;  // ln of the kept mass, the largest w being 1
+  double inv_t, c, t_log_m;
+  // first CTA: what the CTAs of the cluster hand it
+  u64 part[kMaxCluster];      // their share of the row's mass
+  int n_lists[kMaxCluster];   // tokens that they gathered
+  int x_index[kMaxCluster];   // the maximum's first index in their stretch
+  float max[kMaxCluster];     // (every CTA's) the maxima of the stretches
+  Scale sc;
   int found[8];
   int n_list;
   Decision d;
@@ -113,29 +142,23 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
-// A row's temperature and maximum as the weights need them.
-struct Scale {
-  float max;
-  float floor;         // below it w = 0 (62 octaves under the maximum)
-  float base;          // 0; the maximum where x / C would leave the integers of fp32: there
-                       // x - max is exact for every x >= floor
-  float least;         // rint(x / C) of the floor, as kMagic + k: smaller ones count as it
-  float inv_c, c_hi, c_lo, inv_t;
-  int top;             // octave of the maximum
-  float cut;           // the head: x >= cut
-  float bin_scale;     // bins of the head, from the maximum down
-};
-
 constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: adding it rounds to an integer
 
-__device__ __forceinline__ Scale make_scale(float max, float temp) {
+// What does not depend on the maximum (one thread per CTA: fp64 runs at a 64th
+// of the fp32 rate).
+__device__ __forceinline__ void prepare_scale(Smem& s, float temp, float min_p) {
+  s.inv_t = 1.0 / (double)temp;
+  s.c = (double)temp * (0.69314718055994530942 / 64.0);
+  s.t_log_m = min_p > 0.f ? (double)temp * log((double)min_p) : 0.0;
+}
+__device__ __forceinline__ Scale make_scale(const Smem& s, float max, float min_p) {
   Scale sc;
-  const double c = (double)temp * (0.69314718055994530942 / 64.0);
+  const double c = s.c;
   sc.max = max;
   sc.c_hi = (float)c;
   sc.c_lo = (float)(c - (double)sc.c_hi);
-  sc.inv_c = (float)(1.0 / c);
-  sc.inv_t = (float)(1.0 / (double)temp);
+  sc.inv_c = (float)(s.inv_t * (64.0 / 0.69314718055994530942));
+  sc.inv_t = (float)s.inv_t;
   sc.floor = __double2float_rd((double)max - 62.0 * 64.0 * c);
   sc.base = fabsf(max) * sc.inv_c < 2097152.f ? 0.f : max;
   const float t = fmaf(max - sc.base, sc.inv_c, kMagic);
@@ -143,6 +166,7 @@ __device__ __forceinline__ Scale make_scale(float max, float temp) {
   sc.least = t - 62.f * 64.f;
   sc.cut = sc.floor;
   sc.bin_scale = 0.f;
+  sc.x_min = min_p > 0.f ? __double2float_ru((double)max + s.t_log_m) : -INFINITY;
   return sc;
 }
 
@@ -169,46 +193,178 @@ __device__ __forceinline__ int bin_of(float x, const Scale& sc) {
   return min(kBins - 1, __float2int_rd((sc.max - x) * sc.bin_scale));
 }
 
+// floor(f * m) for f in [0, 1); *exact tells whether nothing was cut off.
+__device__ __forceinline__ u64 share(float f, u64 m, bool* exact) {
+  const uint32_t b = __float_as_uint(f);
+  const int e = (int)(b >> 23);
+  const u64 frac = (b & 0x7fffffu) | (e ? 0x800000u : 0u);
+  const int sh = 150 - max(e, 1);  // f = frac * 2^-sh, sh in [24, 149]
+  const u64 lo = frac * m, hi = __umul64hi(frac, m);
+  if (sh >= 128) {
+    *exact = (lo | hi) == 0;
+    return 0;
+  }
+  if (sh >= 64) {
+    *exact = lo == 0 && (sh == 64 || (hi << (128 - sh)) == 0);
+    return sh == 64 ? hi : hi >> (sh - 64);
+  }
+  *exact = (lo << (64 - sh)) == 0;
+  return (lo >> sh) | (hi << (64 - sh));
+}
+// The least mass that is at least f * m (f below 1), and that exceeds it.
+__device__ __forceinline__ u64 at_least(float f, u64 m) {
+  bool exact;
+  const u64 t = share(f, m, &exact);
+  return exact ? t : t + 1;
+}
+__device__ __forceinline__ u64 above(float f, u64 m) {
+  bool exact;
+  return share(f, m, &exact) + 1;
+}
+
 __device__ __forceinline__ void set_cut(Scale& sc, float cut) {
   sc.cut = fminf(fmaxf(cut, sc.floor), sc.max);
   const float range = sc.max - sc.cut;
   sc.bin_scale = range > 0.f ? fminf((float)kBins / range, 3e38f) : 0.f;
 }
 
-// Calls f(x, index) for the tokens [lo, hi) of a row, a thread's own in
-// ascending order; of its 16-byte vectors only groups of 32 in `every`.
+__device__ __forceinline__ void copy_async(uint4* dst, const uint4* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
+               : "memory");
+}
+
+// Sweeps the tokens [lo, hi) of a row by whole warps: many(vector, its first
+// index, whether this lane has one) for the 16-byte vectors, one(value, index,
+// whether) for the ends that do not fill a vector (at most VE - 1 each, by the
+// first warp).  Vectors come in through the thread's own slots of the ring,
+// kStages - 1 ahead, without taking registers or barriers.
+template <typename T, typename Many, typename One>
+__device__ __forceinline__ void sweep_vectors(Smem& s, const T* row, int lo, int hi, Many&& many, One&& one) {
+  constexpr int VE = 16 / sizeof(T);
+  const int lane = threadIdx.x & 31;
+  const T* p = row + lo;
+  const int n = hi - lo;
+  const int head = min(n, (int)(((16 - ((uintptr_t)p & 15)) & 15) / sizeof(T)));
+  const int n_vec = (n - head) / VE;
+  const uint4* v = reinterpret_cast<const uint4*>(p + head);
+  uint4* ring = &s.ring[0][threadIdx.x];
+  int i = threadIdx.x;
+#pragma unroll
+  for (int a = 0; a < kStages - 1; ++a) {
+    if (i + a * kThreads < n_vec) copy_async(ring + a * kThreads, v + i + a * kThreads);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  int at = 0, put = (kStages - 1) * kThreads;
+#pragma unroll 1
+  for (; i - lane < n_vec; i += kThreads) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+    const bool in = i < n_vec;
+    const uint4 now = ring[at];
+    // the slot of the vector before, which has been used
+    const int next = i + (kStages - 1) * kThreads;
+    if (next < n_vec) copy_async(ring + put, v + next);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    put = at;
+    at = at == (kStages - 1) * kThreads ? 0 : at + kThreads;
+    many(now, lo + head + i * VE, in);
+  }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  const int rest = n - head - n_vec * VE;
+  if ((int)threadIdx.x < 32) {
+    const bool in = lane < head + rest;
+    const int j = lane < head ? lane : lane + n_vec * VE;
+    one(in ? to_f(p[j]) : -INFINITY, lo + j, in);
+  }
+}
+
+// Calls f(x, index) for the tokens [lo, hi) of a row.
 template <typename T, typename F>
-__device__ __forceinline__ void sweep(const T* row, int lo, int hi, F&& f, int every = 1) {
+__device__ __forceinline__ void sweep(Smem& s, const T* row, int lo, int hi, F&& f) {
+  sweep_vectors(
+      s, row, lo, hi,
+      [&](const uint4& q, int i, bool in) {
+        const T* e = reinterpret_cast<const T*>(&q);
+        if (in) {
+#pragma unroll
+          for (int k = 0; k < (int)(16 / sizeof(T)); ++k) f(to_f(e[k]), i + k);
+        }
+      },
+      [&](float x, int i, bool in) {
+        if (in) f(x, i);
+      });
+}
+
+// Calls each(x) for every token and f(entry, have) for the ones with x >= cut,
+// by whole warps: a warp collects such tokens in its queue and hands them over
+// 32 at a time, one per lane (have: whether the lane has one), so that what f
+// waits for is paid once for 32 of them.
+template <typename T, typename Each, typename F>
+__device__ __forceinline__ void sweep_head(Smem& s, const T* row, int lo, int hi, float cut, Each&& each, F&& f) {
+  const int lane = threadIdx.x & 31;
+  u64* queue = s.queue[threadIdx.x >> 5];
+  int waiting = 0;  // the same in every lane
+  auto put = [&](float x, int i, bool in) {
+    const unsigned m = __ballot_sync(0xffffffffu, in);
+    if (m) {
+      if (in) queue[waiting + __popc(m & ((1u << lane) - 1u))] = entry_of(x, i);
+      waiting += __popc(m);
+      if (waiting >= 32) {
+        __syncwarp();
+        f(queue[lane], true);
+        waiting -= 32;
+        const u64 e = queue[32 + lane];
+        __syncwarp();
+        if (lane < waiting) queue[lane] = e;
+        __syncwarp();
+      }
+    }
+  };
+  sweep_vectors(
+      s, row, lo, hi,
+      [&](const uint4& q, int i, bool in) {
+        constexpr int VE = 16 / sizeof(T);
+        const T* e = reinterpret_cast<const T*>(&q);
+        float m = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < VE; ++k) m = fmaxf(m, to_f(e[k]));
+        if (in) {
+#pragma unroll
+          for (int k = 0; k < VE; ++k) each(to_f(e[k]));
+        }
+        if (__any_sync(0xffffffffu, in && m >= cut)) {
+#pragma unroll
+          for (int k = 0; k < VE; ++k) put(to_f(e[k]), i + k, in && to_f(e[k]) >= cut);
+        }
+      },
+      [&](float x, int i, bool in) {
+        if (in) each(x);
+        put(x, i, in && x >= cut);
+      });
+  __syncwarp();
+  if (waiting) f(lane < waiting ? queue[lane] : 0ull, lane < waiting);
+  __syncwarp();
+}
+
+// Calls f(x) for one group of 32 vectors in `every` (and for no tokens outside
+// the vectors).
+template <typename T, typename F>
+__device__ __forceinline__ void sweep_sample(const T* row, int lo, int hi, int every, F&& f) {
   constexpr int VE = 16 / sizeof(T);
   const T* p = row + lo;
   const int n = hi - lo;
   const int head = min(n, (int)(((16 - ((uintptr_t)p & 15)) & 15) / sizeof(T)));
   const int n_vec = (n - head) / VE;
-  if ((int)threadIdx.x < head) f(to_f(p[threadIdx.x]), lo + (int)threadIdx.x);
   const uint4* v = reinterpret_cast<const uint4*>(p + head);
-  auto use = [&](const uint4& q, int i) {
-    const T* e = reinterpret_cast<const T*>(&q);
+#pragma unroll 1
+  for (int g = threadIdx.x >> 5; g * every * 32 < n_vec; g += kThreads / 32) {
+    const int i = g * every * 32 + (threadIdx.x & 31);
+    if (i < n_vec) {
+      const uint4 q = __ldg(v + i);
+      const T* e = reinterpret_cast<const T*>(&q);
 #pragma unroll
-    for (int k = 0; k < VE; ++k) f(to_f(e[k]), lo + head + i * VE + k);
-  };
-  if (every > 1) {
-    for (int g = threadIdx.x >> 5; g * every * 32 < n_vec; g += kThreads / 32) {
-      const int i = g * every * 32 + (threadIdx.x & 31);
-      if (i < n_vec) use(__ldg(v + i), i);
+      for (int k = 0; k < VE; ++k) f(to_f(e[k]));
     }
-    return;
   }
-  constexpr int kAhead = 4;  // loads in flight per thread
-  int i = threadIdx.x;
-  for (; i + (kAhead - 1) * kThreads < n_vec; i += kAhead * kThreads) {
-    uint4 q[kAhead];
-#pragma unroll
-    for (int a = 0; a < kAhead; ++a) q[a] = __ldg(v + i + a * kThreads);
-#pragma unroll
-    for (int a = 0; a < kAhead; ++a) use(q[a], i + a * kThreads);
-  }
-  for (; i < n_vec; i += kThreads) use(__ldg(v + i), i);
-  for (int j = head + n_vec * VE + threadIdx.x; j < n; j += kThreads) f(to_f(p[j]), lo + j);
 }
 
 template <typename Op>
@@ -289,24 +445,68 @@ __device__ __forceinline__ int first_bin(F&& past, int* slot) {
   return *slot;
 }
 
-// Sorts the first n entries of list (n <= kList) ascending.
-__device__ __forceinline__ void sort_list(u64* list, int n) {
-  int size = 2;
-  while (size < n) size <<= 1;
-  for (int i = n + threadIdx.x; i < size; i += kThreads) list[i] = ~0ull;
+// Sorts the first n entries of s.list (n <= kList) ascending, through s.mass:
+// a token's place is the number of tokens in the bins before its own (of 2,048
+// from `top` down, `scale` to a unit of x) and of smaller ones in it.  Few
+// tokens share a bin, unless they are equal.
+__device__ __forceinline__ void sort_list(Smem& s, int n, float top, float scale) {
+  constexpr int kPer = kList / kThreads;
+  if (n <= 1) return;
+#pragma unroll
+  for (int k = 0; k < kBinsPer; ++k) s.count[threadIdx.x + k * kThreads] = 0;
   __syncthreads();
-  for (int k = 2; k <= size; k <<= 1)
-    for (int j = k >> 1; j; j >>= 1) {
-      for (int t = threadIdx.x; t < size / 2; t += kThreads) {
-        const int i = 2 * t - (t & (j - 1)), l = i + j;
-        const u64 a = list[i], b = list[l];
-        if ((a > b) == ((i & k) == 0)) {
-          list[i] = b;
-          list[l] = a;
-        }
-      }
-      __syncthreads();
+  u64 e[kPer];
+  int bin[kPer];
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    const int i = threadIdx.x + k * kThreads;
+    if (i < n) {
+      e[k] = s.list[i];
+      bin[k] = min(kBins - 1, __float2int_rd((top - entry_x(e[k])) * scale));
+      atomicAdd(s.count + bin[k], 1u);
     }
+  }
+  __syncthreads();
+  // counts -> first places
+  uint32_t c[kBinsPer], sum = 0;
+#pragma unroll
+  for (int k = 0; k < kBinsPer; ++k) {
+    c[k] = s.count[kBinsPer * threadIdx.x + k];
+    sum += c[k];
+  }
+  uint32_t at = (uint32_t)block_scan(sum, s.red);
+#pragma unroll
+  for (int k = 0; k < kBinsPer; ++k) {
+    s.count[kBinsPer * threadIdx.x + k] = at;
+    at += c[k];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < kPer; ++k)
+    if ((int)threadIdx.x + k * kThreads < n) s.mass[atomicAdd(s.count + bin[k], 1u)] = e[k];
+  __syncthreads();
+  // s.count[b] is now the end of bin b
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    if ((int)threadIdx.x + k * kThreads < n) {
+      const int b0 = bin[k] ? (int)s.count[bin[k] - 1] : 0, b1 = (int)s.count[bin[k]];
+      int place = b0;
+      for (int j = b0; j < b1; ++j) place += s.mass[j] < e[k];
+      s.list[place] = e[k];
+    }
+  }
+  __syncthreads();
+}
+
+// The same, with the bins laid between the list's largest and smallest value.
+__device__ __forceinline__ void sort_list(Smem& s, int n) {
+  u64 lo = ~0ull, hi = 0;
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    lo = min(lo, s.list[i]);
+    hi = max(hi, s.list[i]);
+  }
+  const float top = entry_x(block_min(lo, s.red)), low = entry_x(block_max(hi, s.red));
+  sort_list(s, n, top, top > low ? fminf((float)kBins / (top - low), 3e38f) : 0.f);
 }
 
 // Running masses (inclusive) over the sorted list into s.mass.
@@ -328,32 +528,71 @@ __device__ __forceinline__ void sum_list(Smem& s, int n, const Scale& sc) {
   __syncthreads();
 }
 
-// Appends a token to this CTA's list; what does not fit is only counted.
+// Appends tokens to this CTA's list; what does not fit is only counted.
 __device__ __forceinline__ void append(Smem& s, float x, int i) {
   const int at = atomicAdd(&s.n_list, 1);
   if (at < kList) s.list[at] = entry_of(x, i);
 }
+__device__ __forceinline__ void append_warp(Smem& s, u64 entry, bool have) {
+  const unsigned m = __ballot_sync(0xffffffffu, have);
+  const int lane = threadIdx.x & 31;
+  int at = 0;
+  if (lane == 0 && m) at = atomicAdd(&s.n_list, __popc(m));
+  at = __shfl_sync(0xffffffffu, at, 0) + __popc(m & ((1u << lane) - 1u));
+  if (have && at < kList) s.list[at] = entry;
+}
 
-enum { kByCount, kMassAtLeast, kMassAbove };
+// ln of a mass, the largest w being 1.
+__device__ __forceinline__ double log_share(u64 mass, const Scale& sc, const Smem& s) {
+  return log((double)mass / (double)weigh(sc.max, sc, s.table, s.table_f));
+}
+
+// Adds one token of mass w to a bin.  The mass is kept as two words in
+// separate arrays (shared memory adds 32 bits at a time); join_bins makes it
+// one.
+__device__ __forceinline__ void add_to_bin(Smem& s, int b, u64 w) {
+  uint32_t* lo = reinterpret_cast<uint32_t*>(s.mass);
+  uint32_t* hi = lo + kBins;
+  atomicAdd(s.count + b, 1u);
+  const uint32_t wl = (uint32_t)w, old = atomicAdd(lo + b, wl);
+  const uint32_t wh = (uint32_t)(w >> 32) + (old + wl < old ? 1u : 0u);
+  if (wh) atomicAdd(hi + b, wh);
+}
+__device__ __forceinline__ u64 bin_mass(const Smem& s, int b) {
+  const uint32_t* lo = reinterpret_cast<const uint32_t*>(s.mass);
+  return ((u64)lo[kBins + b] << 32) | lo[b];
+}
+__device__ __forceinline__ void join_bins(Smem& s) {
+  u64 m[kBinsPer];
+#pragma unroll
+  for (int i = 0; i < kBinsPer; ++i) m[i] = bin_mass(s, threadIdx.x + i * kThreads);
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kBinsPer; ++i) s.mass[threadIdx.x + i * kThreads] = m[i];
+  __syncthreads();
+}
+__device__ __forceinline__ void clear_bins(Smem& s) {
+  for (int i = threadIdx.x; i < kBins; i += kThreads) {
+    s.count[i] = 0;
+    s.mass[i] = 0;
+  }
+}
 
 // The cut of the order inside bin `b` of the head (any number of tokens): the
-// first token whose rank (1, 2, ...) reaches `rank`, or whose running mass
-// reaches or exceeds `target`.  *mass: the running mass with it; *entry: the
+// first token whose rank (1, 2, ...) reaches `rank`, or, where rank is 0, whose
+// running mass reaches `target`.  *mass: the running mass with it; *entry: the
 // token.  One CTA does it, over the whole row, where too many tokens share the
 // cuts' bins to be gathered at once: the bin's keys are cut into 2,048 ranges
 // again and again until the cut's range is short, or a single value, whose
 // tokens are told apart by index.
 template <typename T>
 __device__ __noinline__ void find_in_bin(Smem& s, const T* row, int vocab, const Scale& sc, int b, uint32_t c_before,
-                                         u64 m_before, int mode, uint32_t rank, double target, u64* mass,
-                                         u64* entry) {
-  auto past = [&](uint32_t c, u64 m) {
-    return mode == kByCount ? c >= rank : (mode == kMassAtLeast ? (double)m >= target : (double)m > target);
-  };
+                                         u64 m_before, uint32_t rank, u64 target, u64* mass, u64* entry) {
+  auto past = [&](uint32_t c, u64 m) { return rank ? c >= rank : m >= target; };
   uint32_t lo = 0, hi = 0xffffffffu;
   for (;;) {
     uint32_t kmin = 0xffffffffu, kmax = 0, n = 0;
-    sweep(row, 0, vocab, [&](float x, int) {
+    sweep(s, row, 0, vocab, [&](float x, int) {
       const uint32_t k = key_of(x);
       if (x >= sc.cut && k >= lo && k <= hi && bin_of(x, sc) == b) {
         kmin = min(kmin, k);
@@ -365,24 +604,22 @@ __device__ __noinline__ void find_in_bin(Smem& s, const T* row, int vocab, const
     kmax = (uint32_t)block_max(kmax, s.red);
     n = (uint32_t)block_sum(n, s.red);
     if (kmin == kmax) {
+      // the t-th of n equal tokens, 1 <= t <= n
       const float x = of_key(kmin);
       const u64 w = weigh(x, sc, s.table, s.table_f);
-      // the t-th of n equal tokens (t >= 1): estimated, then set right
-      int64_t t;
-      if (mode == kByCount)
-        t = (int64_t)rank - c_before;
-      else
-        t = w ? (int64_t)((target - (double)m_before) / (double)w) : 1;
-      t = max((int64_t)1, min((int64_t)n, t));
-      while (t > 1 && past(c_before + (uint32_t)t - 1, m_before + (t - 1) * w)) --t;
-      while (t < (int64_t)n && !past(c_before + (uint32_t)t, m_before + t * w)) ++t;
+      u64 t = 1;
+      if (rank)
+        t = rank - c_before;
+      else if (w && target > m_before)
+        t = (target - m_before + w - 1) / w;
+      t = max(1ull, min((u64)n, t));
       *mass = m_before + t * w;
       // its index: each thread counts the equals of one stretch of the row
       const int per = (vocab + kThreads - 1) / kThreads;
       const int i0 = min(vocab, (int)threadIdx.x * per), i1 = min(vocab, i0 + per);
       int mine = 0;
       for (int i = i0; i < i1; ++i) mine += key_of(to_f(row[i])) == kmin;
-      int64_t left = t - (int64_t)block_scan(mine, s.red);
+      int64_t left = (int64_t)t - (int64_t)block_scan(mine, s.red);
       if (left >= 1 && left <= mine)
         for (int i = i0; i < i1; ++i)
           if (key_of(to_f(row[i])) == kmin && --left == 0) s.out = entry_of(x, i);
@@ -393,12 +630,12 @@ __device__ __noinline__ void find_in_bin(Smem& s, const T* row, int vocab, const
     if (n <= kList) {
       if (threadIdx.x == 0) s.n_list = 0;
       __syncthreads();
-      sweep(row, 0, vocab, [&](float x, int i) {
+      sweep(s, row, 0, vocab, [&](float x, int i) {
         const uint32_t k = key_of(x);
         if (x >= sc.cut && k >= lo && k <= hi && bin_of(x, sc) == b) append(s, x, i);
       });
       __syncthreads();
-      sort_list(s.list, (int)n);
+      sort_list(s, (int)n);
       sum_list(s, (int)n, sc);
       u64 best = n - 1;
       for (uint32_t i = threadIdx.x; i < n; i += kThreads)
@@ -411,20 +648,15 @@ __device__ __noinline__ void find_in_bin(Smem& s, const T* row, int vocab, const
     }
     // 2,048 ranges of the keys kmax .. kmin, descending
     const int shift = max(0, 32 - __clz(kmax - kmin) - 11);
-    for (int i = threadIdx.x; i < kBins; i += kThreads) {
-      s.mass[i] = 0;
-      s.count[i] = 0;
-    }
+    clear_bins(s);
     __syncthreads();
-    sweep(row, 0, vocab, [&](float x, int) {
+    sweep(s, row, 0, vocab, [&](float x, int) {
       const uint32_t k = key_of(x);
-      if (x >= sc.cut && k >= kmin && k <= kmax && bin_of(x, sc) == b) {
-        const uint32_t at = (kmax - k) >> shift;
-        atomicAdd(s.count + at, 1u);
-        atomicAdd(s.mass + at, weigh(x, sc, s.table, s.table_f));
-      }
+      if (x >= sc.cut && k >= kmin && k <= kmax && bin_of(x, sc) == b)
+        add_to_bin(s, (int)((kmax - k) >> shift), weigh(x, sc, s.table, s.table_f));
     });
     __syncthreads();
+    join_bins(s);
     accumulate_bins(s.count, s.mass, s.red);
     const int at = first_bin([&](int i) { return past(c_before + s.count[i], m_before + s.mass[i]); }, s.found);
     if (at > 0) {
@@ -464,22 +696,24 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   const float u = __ldg(p.u + r);
 
   // ---- 1. the maximum, and whether anything is wrong ----
+  if (tid == kThreads - 1) prepare_scale(s, temp, min_p);
   {
     float mx = -INFINITY;
-    sweep(row, lo_i, hi_i, [&](float x, int) { mx = max_nan(mx, x); });
+    sweep(s, row, lo_i, hi_i, [&](float x, int) { mx = max_nan(mx, x); });
 #pragma unroll
     for (int o = 16; o; o >>= 1) mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, o));
     float* red = reinterpret_cast<float*>(s.red);
     if ((tid & 31) == 0) red[tid >> 5] = mx;
     __syncthreads();
-    if (tid == 0) {
+    if (tid < c_size) {  // to every CTA of the cluster
+      mx = red[0];
       for (int w = 1; w < kThreads / 32; ++w) mx = max_nan(mx, red[w]);
-      s.max = mx;
+      cluster.map_shared_rank(&s, tid)->max[c_rank] = mx;
     }
   }
   cluster.sync();
-  float row_max = s0.max;
-  for (int c = 1; c < c_size; ++c) row_max = max_nan(row_max, cluster.map_shared_rank(&s, c)->max);
+  float row_max = s.max[0];
+  for (int c = 1; c < c_size; ++c) row_max = max_nan(row_max, s.max[c]);
   const bool bad = !(row_max > -INFINITY && row_max < INFINITY) ||
                    !(temp == 0.f || (temp >= 0x1p-100f && temp <= 0x1p60f)) || !(top_p >= 0.f) ||
                    !(min_p >= 0.f && min_p <= 1.f) || !(u >= 0.f && u < 1.f);
@@ -487,60 +721,64 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     // the maximum's first index
     if (!bad) {
       int first = p.vocab;
-      sweep(row, lo_i, hi_i, [&](float x, int i) {
-        if (x == row_max) first = min(first, i);
-      });
+      sweep_head(s, row, lo_i, hi_i, row_max, [](float) {},
+                 [&](u64 e, bool have) { first = have ? min(first, (int)(uint32_t)e) : first; });
       first = (int)block_min((u64)first, s.red);
-      if (tid == 0) s.x_index = first;
+      if (tid == 0) s0.x_index[c_rank] = first;
     }
-    cluster.sync();  // (also: no CTA ends while its maximum is read)
+    cluster.sync();
     if (c_rank == 0 && tid == 0) {
       int id = -1;
       if (!bad) {
-        id = s.x_index;
-        for (int c = 1; c < c_size; ++c) id = min(id, cluster.map_shared_rank(&s, c)->x_index);
+        id = s.x_index[0];
+        for (int c = 1; c < c_size; ++c) id = min(id, s.x_index[c]);
       }
       p.ids[r] = id;
       if (p.logprob) p.logprob[r] = bad ? -INFINITY : 0.f;
       if (bad) report(p.status, STV_DEV_BAD_SAMPLE);
     }
-    cluster.sync();
     return;
   }
-  Scale sc = make_scale(row_max, temp);
+  if (tid == 0) s.sc = make_scale(s, row_max, min_p);
+  __syncthreads();
+  Scale sc = s.sc;
+  const float x_min = sc.x_min;
   const bool want_k = top_k > 0 && top_k < p.vocab, has_p = top_p < 1.f, want_m = min_p > 0.f;
   const bool m_only = want_m && !want_k && !has_p;  // the head is what min_p keeps
   const bool need_all = !want_k && !m_only;         // the mass of every token
-  const float x_min = want_m ? __double2float_ru((double)sc.max + (double)temp * log((double)min_p)) : -INFINITY;
 
   // ---- the sample: how far down the cuts lie, and how many tokens that is ----
   bool direct;
   {
     const float per = 4.f / 64.f * sc.inv_c;  // quarter octaves per unit of x
-    sweep(
-        row, lo_i, hi_i,
-        [&](float x, int) {
-          const float y = (sc.max - x) * per;
-          if (y < (float)(kCoarse - 8)) atomicAdd(s.coarse + (int)y, 1u);
-        },
-        p.sample_every);
+    sweep_sample(row, lo_i, hi_i, p.sample_every, [&](float x) {
+      const float y = (sc.max - x) * per;
+      if (y < (float)(kCoarse - 8)) atomicAdd(s.coarse + (int)y, 1u);
+    });
     cluster.sync();
     const float f = (float)p.sample_every;
     if (tid < kCoarse) {
       uint32_t n = 0;
-      for (int c = 0; c < c_size; ++c) n += cluster.map_shared_rank(&s, c)->coarse[tid];
-      s.coarse_est[tid] = (float)n;
+#pragma unroll
+      for (int c = 0; c < kMaxCluster; ++c)
+        if (c < c_size) n += cluster.map_shared_rank(&s, c)->coarse[tid];
+      s.coarse_all[tid] = n;
     }
     __syncthreads();
-    if (tid < 32) {  // a warp: lane l holds eight bins, from the far end for the tail's mass
-      float cnt[8], wgt[8], c8 = 0.f, w8 = 0.f;
+    if (tid < 32) {  // a warp: lane l holds eight bins
+      float cnt[8], wgt[8], c8 = 0.f, w8 = 0.f, sure = 0.f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        cnt[i] = s.coarse_est[tid * 8 + i];
-        wgt[i] = f * cnt[i] * exp2f(-0.25f * (float)(tid * 8 + i));
+        cnt[i] = (float)s.coarse_all[tid * 8 + i];
+        const float w = exp2f(-0.25f * (float)(tid * 8 + i));
+        wgt[i] = f * cnt[i] * w;
         c8 += cnt[i];
         w8 += wgt[i];
+        // surely there: two deviations under the sample's count
+        sure += fmaxf(cnt[i], f * (cnt[i] - 2.f * sqrtf(cnt[i]))) * w;
       }
+#pragma unroll
+      for (int o = 16; o; o >>= 1) sure += __shfl_xor_sync(0xffffffffu, sure, o);
       float c_incl = c8, w_incl = w8;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -551,23 +789,26 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         }
       }
       const float w_all = __shfl_sync(0xffffffffu, w_incl, 31);
-      // enough: top_k tokens with four deviations of the sample's count; or a
-      // tail below the first bin of under 0.7 of what the cut leaves out (the
-      // maximum counts as 1, so tokens the sample missed err to this side)
+      // enough: top_k tokens with four deviations of the sample's count; what
+      // min_p keeps; or a tail of under 0.7 of what the cut leaves out of the
+      // mass that is surely there, the maximum's 1 with it, below a head of so
+      // many tokens that the sample knows what lies beneath
       const float k_need = (float)top_k / f;
       const float enough = p.sample_every > 1 ? k_need + 4.f * sqrtf(k_need) + 8.f : k_need;
       const float left = has_p ? 1.f - top_p : 1.f - u;
-      const float tail = 0.7f * left * (1.f + w_all);
+      const float tail = 0.7f * left * (1.f + sure);
       int b = kCoarse;
       float n_head = 0.f, c = c_incl - c8, w = w_incl - w8;
+#pragma unroll
       for (int i = 0; i < 8; ++i) {  // the bins up to this one are enough
         c += cnt[i];
         w += wgt[i];
         const int past = tid * 8 + i + 1;
-        if (m_only ? (float)past > (sc.max - x_min) * per : (want_k ? c >= enough : w_all - w <= tail)) {
+        const bool ok = m_only ? (float)past > (sc.max - x_min) * per
+                               : (want_k ? c >= enough : w_all - w <= tail && c * f >= kLeastHead);
+        if (ok && b == kCoarse) {
           b = past;
           n_head = c;
-          break;
         }
       }
       const unsigned any = __ballot_sync(0xffffffffu, b < kCoarse);
@@ -596,35 +837,28 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     }
     const bool complete = sc.cut <= sc.floor;
     // ---- 2. the mass of all, the head's tokens or bins ----
-    for (int i = tid; i < kBins && !direct; i += kThreads) {
-      s.count[i] = 0;
-      s.mass[i] = 0;
-    }
+    if (!direct) clear_bins(s);
     if (tid == 0) s.n_list = 0;
     __syncthreads();
-    u64 sum = 0;
     const bool all = need_all && round == 0;
-    sweep(row, lo_i, hi_i, [&](float x, int i) {
-      u64 w = 0;
-      if (all) {
-        w = weigh(x, sc, s.table, s.table_f);
-        sum += w;
+    auto take = [&](u64 e, bool have) {
+      if (direct) {
+        append_warp(s, e, have);
+      } else if (have) {
+        const float x = entry_x(e);
+        add_to_bin(s, bin_of(x, sc), weigh(x, sc, s.table, s.table_f));
       }
-      if (x >= sc.cut) {
-        if (direct) {
-          append(s, x, i);
-        } else {
-          if (!all) w = weigh(x, sc, s.table, s.table_f);
-          const int b = bin_of(x, sc);
-          atomicAdd(s.count + b, 1u);
-          atomicAdd(s.mass + b, w);
-        }
-      }
-    });
+    };
     if (all) {
+      u64 sum = 0;
+      sweep_head(s, row, lo_i, hi_i, sc.cut, [&](float x) { sum += weigh(x, sc, s.table, s.table_f); }, take);
       sum = block_sum(sum, s.red);
-      if (tid == 0) s.part = sum;
+      if (tid == 0) s0.part[c_rank] = sum;
+    } else {
+      sweep_head(s, row, lo_i, hi_i, sc.cut, [](float) {}, take);
+      __syncthreads();
     }
+    if (tid == 0) s0.n_lists[c_rank] = s.n_list;
     cluster.sync();
     if (!direct) {
       // each CTA adds up a share of the bins, for the first one
@@ -632,11 +866,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       for (int i = c_rank * per + tid; i < (c_rank + 1) * per; i += kThreads) {
         uint32_t c = 0;
         u64 m = 0;
-        for (int k = 0; k < c_size; ++k) {
-          const Smem* o = cluster.map_shared_rank(&s, k);
-          c += o->count[i];
-          m += o->mass[i];
-        }
+#pragma unroll
+        for (int k = 0; k < kMaxCluster; ++k)
+          if (k < c_size) {
+            const Smem* o = cluster.map_shared_rank(&s, k);
+            c += o->count[i];
+            m += bin_mass(*o, i);
+          }
         s0.tot_count[i] = c;
         s0.tot_mass[i] = m;
       }
@@ -646,15 +882,18 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     auto m_before = [&](int b) { return b ? s.tot_mass[b - 1] : 0ull; };
     // the tokens of every CTA's list in the first one's; false if they do not fit
     auto merge_lists = [&](int* n_out) {
-      int n = s.n_list;
-      bool fits = n <= kList;
-      for (int c = 1; c < c_size && fits; ++c) {
-        const Smem* o = cluster.map_shared_rank(&s, c);
-        const int m = o->n_list;
-        fits = n + m <= kList;
-        for (int i = tid; i < m && fits; i += kThreads) s.list[n + i] = o->list[i];
-        n += m;
+      int n = 0;
+      bool fits = true;
+      for (int c = 0; c < c_size; ++c) {
+        n += s.n_lists[c];
+        fits = fits && n <= kList;
       }
+      if (fits)
+        for (int i = s.n_lists[0] + tid; i < n; i += kThreads) {
+          int c = 1, j = i - s.n_lists[0];
+          while (j >= s.n_lists[c]) j -= s.n_lists[c++];
+          s.list[i] = cluster.map_shared_rank(&s, c)->list[j];
+        }
       __syncthreads();
       *n_out = n;
       return fits;
@@ -667,14 +906,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     d.pb1 = d.ub1 = 0;
     d.pb2 = d.ub2 = -1;
     if (c_rank == 0) {
-      if (all) {
-        total = s.part;
-        for (int c = 1; c < c_size; ++c) total += cluster.map_shared_rank(&s, c)->part;
-      }
+      if (all)
+        for (int c = 0; c < c_size; ++c) total += s.part[c];
       if (direct) {
         int n;
         if (merge_lists(&n) && n > 0) {
-          sort_list(s.list, n);
+          sort_list(s, n, sc.max, sc.bin_scale);
           sum_list(s, n, sc);
           const u64 head = s.mass[n - 1];
           bool ok = true;
@@ -683,27 +920,35 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
             has_k = false;
           }
           kept = has_k ? s.mass[top_k - 1] : (need_all ? total : head);
+          // the list is sorted: a cut is where a thread's entry is past it and the one before is not
           if (has_p) {
-            const double t = (double)top_p * (double)kept;
-            ok = ok && (double)head >= t;
-            u64 m = ~0ull;
+            const u64 t = at_least(top_p, kept);
+            ok = ok && head >= t;
+            if (tid == 0) s.out = kept;
+            __syncthreads();
             for (int i = tid; i < n; i += kThreads)
-              if ((double)s.mass[i] >= t) m = min(m, s.mass[i]);
-            kept = min(kept, block_min(m, s.red));
+              if (s.mass[i] >= t && (i == 0 || s.mass[i - 1] < t)) s.out = min(kept, s.mass[i]);
+            __syncthreads();
+            kept = s.out;
           }
           if (has_m) {
-            u64 w = 0;
+            if (tid == 0) s.part[0] = kept;
+            __syncthreads();
             for (int i = tid; i < n; i += kThreads)
-              if (entry_x(s.list[i]) >= x_min) w = max(w, s.mass[i]);
-            kept = min(kept, block_max(w, s.red));
+              if (entry_x(s.list[i]) >= x_min && (i == n - 1 || entry_x(s.list[i + 1]) < x_min))
+                s.part[0] = min(kept, s.mass[i]);
+            __syncthreads();
+            kept = s.part[0];
           }
-          const double t = (double)u * (double)kept;
-          ok = ok && (double)head > t;
-          u64 at = n - 1;
+          const u64 t = above(u, kept);
+          ok = ok && head >= t;
+          if (tid == 0) s.red[0] = s.list[n - 1];
+          __syncthreads();
           for (int i = tid; i < n; i += kThreads)
-            if ((double)s.mass[i] > t) at = min(at, (u64)i);
-          at = block_min(at, s.red);
-          token = s.list[at];
+            if (s.mass[i] >= t && (i == 0 || s.mass[i - 1] < t)) s.red[0] = s.list[i];
+          if (tid == kThreads - 1) s.log_kept = log_share(kept, sc, s);
+          __syncthreads();
+          token = s.red[0];
           d.done = ok;
         }
       } else {
@@ -716,6 +961,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
           has_k = false;
         }
         // a cut's mass lies between the mass before its first bin and with its last
+        auto reaches = [&](u64 t, int* slot) { return first_bin([&](int b) { return s.tot_mass[b] >= t; }, slot); };
         u64 lo = need_all ? total : head, hi = lo;
         if (has_k) {
           d.kb = first_bin([&](int b) { return s.tot_count[b] >= (uint32_t)top_k; }, s.found);
@@ -723,10 +969,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
           hi = s.tot_mass[d.kb];
         }
         if (has_p) {
-          const double t1 = (double)top_p * (double)lo, t2 = (double)top_p * (double)hi;
-          ok = ok && (double)head >= t2;
-          d.pb1 = first_bin([&](int b) { return (double)s.tot_mass[b] >= t1; }, s.found + 1);
-          d.pb2 = first_bin([&](int b) { return (double)s.tot_mass[b] >= t2; }, s.found + 2);
+          const u64 t = at_least(top_p, hi);
+          ok = ok && head >= t;
+          d.pb1 = reaches(at_least(top_p, lo), s.found + 1);
+          d.pb2 = has_k ? reaches(t, s.found + 2) : d.pb1;
           lo = min(lo, m_before(d.pb1));
           hi = min(hi, s.tot_mass[d.pb2]);
         }
@@ -735,44 +981,41 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
           lo = min(lo, m_before(d.mb));
           hi = min(hi, s.tot_mass[d.mb]);
         }
-        const double u1 = (double)u * (double)lo, u2 = (double)u * (double)hi;
-        ok = ok && (double)head > u2;
-        d.ub1 = first_bin([&](int b) { return (double)s.tot_mass[b] > u1; }, s.found + 3);
-        d.ub2 = first_bin([&](int b) { return (double)s.tot_mass[b] > u2; }, s.found + 4);
-        auto wanted = [&](int b) {
-          return b == d.kb || (b >= d.pb1 && b <= d.pb2) || b == d.mb || (b >= d.ub1 && b <= d.ub2);
-        };
+        const u64 t = above(u, hi);
+        ok = ok && head >= t;
+        d.ub1 = reaches(above(u, lo), s.found + 3);
+        d.ub2 = lo < hi ? reaches(t, s.found + 4) : d.ub1;
         uint32_t mine = 0;
         for (int b = kBinsPer * tid; b < kBinsPer * (tid + 1); ++b)
-          if (wanted(b)) mine += s.tot_count[b] - c_before(b);
+          if (d.wanted(b)) mine += s.tot_count[b] - c_before(b);
         const uint32_t n = (uint32_t)block_sum(mine, s.red);
-        if ((ok || round) && n > kList) {
+        d.done = ok || round ? 2 : 0;
+        if (d.done && n > kList) {
           // ---- one cut after the other, without the other CTAs ----
           kept = need_all ? total : head;
           if (has_k)
-            find_in_bin(s, row, p.vocab, sc, d.kb, c_before(d.kb), m_before(d.kb), kByCount, (uint32_t)top_k, 0.0,
-                        &kept, &token);
+            find_in_bin(s, row, p.vocab, sc, d.kb, c_before(d.kb), m_before(d.kb), (uint32_t)top_k, 0, &kept,
+                        &token);
           if (has_p) {
-            const double t = (double)top_p * (double)kept;
-            const int b = first_bin([&](int i) { return (double)s.tot_mass[i] >= t; }, s.found);
+            const u64 tp = at_least(top_p, kept);
+            const int b = reaches(tp, s.found);
             u64 m;
-            find_in_bin(s, row, p.vocab, sc, b, c_before(b), m_before(b), kMassAtLeast, 0, t, &m, &token);
+            find_in_bin(s, row, p.vocab, sc, b, c_before(b), m_before(b), 0, tp, &m, &token);
             kept = min(kept, m);
           }
           if (has_m) {
             u64 w = 0;
-            sweep(row, 0, p.vocab, [&](float x, int) {
+            sweep(s, row, 0, p.vocab, [&](float x, int) {
               if (x >= x_min) w += weigh(x, sc, s.table, s.table_f);
             });
             kept = min(kept, block_sum(w, s.red));
           }
-          const double t = (double)u * (double)kept;
-          const int b = first_bin([&](int i) { return (double)s.tot_mass[i] > t; }, s.found);
+          const u64 tu = above(u, kept);
+          const int b = reaches(tu, s.found);
           u64 m;
-          find_in_bin(s, row, p.vocab, sc, b, c_before(b), m_before(b), kMassAbove, 0, t, &m, &token);
+          find_in_bin(s, row, p.vocab, sc, b, c_before(b), m_before(b), 0, tu, &m, &token);
+          if (tid == 0) s.log_kept = log_share(kept, sc, s);
           d.done = 1;
-        } else {
-          d.done = ok || round ? 2 : 0;
         }
       }
       if (tid == 0) s.d = d;
@@ -783,21 +1026,22 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       cluster.sync();  // the decision is read before it is written again
       continue;
     }
-    if (d.done != 2) break;
+    if (d.done != 2) {
+      cluster.sync();  // the first CTA does not end while its decision is read
+      break;
+    }
     // ---- 3. the tokens of the cuts' bins ----
-    auto wanted = [&](int b) {
-      return b == d.kb || (b >= d.pb1 && b <= d.pb2) || b == d.mb || (b >= d.ub1 && b <= d.ub2);
-    };
     if (tid == 0) s.n_list = 0;
     __syncthreads();
-    sweep(row, lo_i, hi_i, [&](float x, int i) {
-      if (x >= sc.cut && wanted(bin_of(x, sc))) append(s, x, i);
-    });
+    sweep_head(s, row, lo_i, hi_i, sc.cut, [](float) {},
+               [&](u64 e, bool have) { append_warp(s, e, have && d.wanted(bin_of(entry_x(e), sc))); });
+    __syncthreads();
+    if (tid == 0) s0.n_lists[c_rank] = s.n_list;
     cluster.sync();
     if (c_rank == 0) {
       int n;
       merge_lists(&n);  // counted above: they fit
-      sort_list(s.list, n);
+      sort_list(s, n);
       sum_list(s, n, sc);
       for (int i = tid; i < n; i += kThreads) {
         const int b = bin_of(entry_x(s.list[i]), sc);
@@ -826,8 +1070,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       kept = need_all ? total : s.tot_mass[kBins - 1];
       if (d.kb >= 0) kept = least([&](int b, uint32_t rank, u64) { return b == d.kb && rank == (uint32_t)top_k; });
       if (has_p) {
-        const double t = (double)top_p * (double)kept;
-        kept = min(kept, least([&](int, uint32_t, u64 g) { return (double)g >= t; }));
+        const u64 t = at_least(top_p, kept);
+        kept = min(kept, least([&](int, uint32_t, u64 g) { return g >= t; }));
       }
       if (has_m) {
         u64 w = 0;
@@ -837,29 +1081,26 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         }
         kept = min(kept, m_before(d.mb) + block_sum(w, s.red));
       }
-      const double t = (double)u * (double)kept;
+      const u64 t = above(u, kept);
       u64 at = n - 1;
       for (int i = tid; i < n; i += kThreads) {
         int b;
         uint32_t rank;
         u64 g;
         place(i, &b, &rank, &g);
-        if ((double)g > t) at = min(at, (u64)i);
+        if (g >= t) at = min(at, (u64)i);
       }
+      if (tid == kThreads - 1) s.log_kept = log_share(kept, sc, s);
       at = block_min(at, s.red);
       token = s.list[at];
     }
+    cluster.sync();  // no CTA ends while the first one reads its list
     break;
   }
   if (c_rank == 0 && tid == 0) {
     p.ids[r] = (int32_t)(uint32_t)token;
-    if (p.logprob) {
-      // kept in units of the largest w
-      const double m = (double)kept / (double)weigh(sc.max, sc, s.table, s.table_f);
-      p.logprob[r] = (float)(((double)entry_x(token) - (double)sc.max) / (double)temp - log(m));
-    }
+    if (p.logprob) p.logprob[r] = (float)(((double)entry_x(token) - (double)sc.max) * s.inv_t - s.log_kept);
   }
-  cluster.sync();  // no CTA ends while the first one reads its list
 }
 
 template <typename T>
@@ -871,7 +1112,7 @@ cudaError_t launch_sample(SampleParams& p, cudaStream_t st) {
   while (c < kMaxCluster && (int64_t)p.n_rows * c * 2 <= 2 * sm && p.vocab / (2 * c) >= 2048) c *= 2;
   constexpr int VE = 16 / sizeof(T);
   p.stretch = ((p.vocab + c - 1) / c + VE - 1) / VE * VE;
-  p.sample_every = std::max(1, std::min(8, p.vocab / 16384));
+  p.sample_every = std::max(1, p.vocab / 8192);
   const size_t smem = sizeof(Smem);
   cudaError_t e = cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e == cudaSuccess) {
