@@ -7,15 +7,20 @@
 // fraction of half a turn, go to sincospif.  An fp32 product pos * f would be
 // off by up to 2^-7 rad at a position of 262,144.
 //
-// One thread turns the same VE channel pairs (one 16-byte load from each half
-// of the rotary channels) of kHeads heads of one row, so the VE sines and
-// cosines are computed once for kHeads heads and stay in registers; the
-// channels past rotary_dim are copied by threads of the same shape.  The call
-// reads and writes each element once: bound by HBM for prompts, by the launch
-// for a round's tree rows.
+// A CTA takes a few rows and some of their heads.  It computes each row's sines
+// and cosines once, into shared memory (a thread that turned its own channels
+// would compute them again for every head), while the loads of its first items
+// are on their way.  An item is two 16-byte loads and stores of one head: a
+// piece of the first half of the rotary channels and its partner in the
+// second, or two pieces past them to copy.
+//
+// The call reads and writes each element once: bound by HBM for prompts, by
+// the launch for a round's tree rows.
 #include <cuda_bf16.h>
 #include <math.h>
 #include <string.h>
+
+#include <algorithm>
 
 #include "stv_device.cuh"
 
@@ -23,7 +28,10 @@ namespace stv {
 namespace {
 
 constexpr int kMaxPairs = 256;
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;  // at least kMaxPairs
+constexpr int kShare = 8;  // items of a thread, for a prompt
+constexpr int kMaxRowsPer = 8;
+constexpr int kMaxHeadsPer = 64;
 
 struct RopeParams {
   uint64_t turn[kMaxPairs];  // frequency of each pair, 2^64 per turn
@@ -33,9 +41,11 @@ struct RopeParams {
   int64_t in_row[2], in_head[2], out_row[2], out_head[2];
   int heads[2];
   const int32_t* pos;
-  int n_rows, n_axes, head_groups;
+  int n_rows;
   int half, head_dim;
   int rot_items, items;  // per head: items that turn pairs, and those plus the ones that copy
+  int rows_per, heads_per, head_blocks;  // a CTA's rows and heads; CTAs per block of rows
+  uint32_t items_inv;                    // floor(2^32 / items) + 1 (see quotient)
   int negate;
 };
 
@@ -54,73 +64,95 @@ struct alignas(sizeof(T) * VE) Vec {
   T e[VE];
 };
 
-template <typename T, int VE, int kHeads>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeParams p) {
+// n / d for n * d < 2^32, with inv = floor(2^32 / d) + 1 (d > 1).
+__device__ __forceinline__ int quotient(int n, int d, uint32_t inv) {
+  return d == 1 ? n : (int)__umulhi((uint32_t)n, inv);
+}
+
+template <typename T, int VE>
+__global__ void __launch_bounds__(kThreads, 5) rope_kernel(const __grid_constant__ RopeParams p) {
   using V = Vec<T, VE>;
-  __shared__ uint64_t turn_s[kMaxPairs];
-  __shared__ uint8_t axis_s[kMaxPairs];
-  for (int i = threadIdx.x; i < p.half; i += kThreads) {
-    turn_s[i] = p.turn[i];
-    axis_s[i] = p.axis[i];
-  }
-  __syncthreads();
+  extern __shared__ __align__(16) float table[];  // [rows][half] cosines, then as many sines
   grid_dep_wait();
   grid_dep_launch();
-  const int64_t id = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  const int64_t unit = id / p.items;
-  const int j = (int)(id - unit * p.items);
-  const int row = (int)(unit / p.head_groups);
-  if (row >= p.n_rows) return;
-  const int h0 = (int)(unit - (int64_t)row * p.head_groups) * kHeads;
-  const int n_heads = p.heads[0] + p.heads[1];
+  const int hb = blockIdx.x % p.head_blocks;
+  const int row0 = (int)(blockIdx.x / p.head_blocks) * p.rows_per;
+  const int n_rows = min(p.rows_per, p.n_rows - row0);
+  const int h0 = hb * p.heads_per, n_heads = min(p.heads_per, p.heads[0] + p.heads[1] - h0);
+  const int n_items = n_rows * n_heads * p.items;
+  const uint32_t heads_inv = n_heads > 1 ? 0xffffffffu / n_heads + 1 : 0;
+  float* sines = table + p.rows_per * p.half;
 
-  const bool turns = j < p.rot_items;
-  // channels of the item: (c0, c1) = a pair of the two halves, or two pieces to copy
-  const int c0 = turns ? j * VE : 2 * p.half + (j - p.rot_items) * 2 * VE;
-  const int c1 = turns ? c0 + p.half : c0 + VE;
-  const bool has1 = c1 < p.head_dim;
-
-  V a[kHeads], b[kHeads];
-#pragma unroll
-  for (int i = 0; i < kHeads; ++i) {
-    const int h = h0 + i;
-    if (h < n_heads) {
-      const int t = h >= p.heads[0];
-      const T* src = static_cast<const T*>(p.in[t]) + row * p.in_row[t] + (h - (t ? p.heads[0] : 0)) * p.in_head[t];
-      a[i] = *reinterpret_cast<const V*>(src + c0);
-      if (has1) b[i] = *reinterpret_cast<const V*>(src + c1);
+  // an item: its row here, its two channels (c1 past the head: one piece only), its head's place
+  struct Item {
+    int row, c0, c1;
+    bool turns;
+  };
+  auto locate = [&](int e, Item* it, const T** src, T** dst) {
+    const int unit = quotient(e, p.items, p.items_inv), j = e - unit * p.items;
+    it->row = quotient(unit, n_heads, heads_inv);
+    const int h = h0 + unit - it->row * n_heads;
+    it->turns = j < p.rot_items;
+    it->c0 = it->turns ? j * VE : 2 * p.half + (j - p.rot_items) * 2 * VE;
+    it->c1 = it->turns ? it->c0 + p.half : it->c0 + VE;
+    const int t = h >= p.heads[0], hh = t ? h - p.heads[0] : h;
+    const int64_t r = row0 + it->row;
+    *src = static_cast<const T*>(p.in[t]) + r * p.in_row[t] + hh * p.in_head[t];
+    *dst = static_cast<T*>(p.out[t]) + r * p.out_row[t] + hh * p.out_head[t];
+  };
+  auto load = [&](int e, Item* it, T** dst, V* a, V* b) {
+    if (e < n_items) {
+      const T* src;
+      locate(e, it, &src, dst);
+      *a = *reinterpret_cast<const V*>(src + it->c0);
+      if (it->c1 < p.head_dim) *b = *reinterpret_cast<const V*>(src + it->c1);
     }
-  }
-  if (turns) {
-    float c[VE], s[VE];
-#pragma unroll
-    for (int e = 0; e < VE; ++e) {
-      const uint64_t f = turn_s[c0 + e];
-      const int32_t ps = __ldg(p.pos + (int64_t)axis_s[c0 + e] * p.n_rows + row);
-      const uint64_t ph = (uint64_t)((int64_t)ps) * f;  // modulo a turn
-      const float x = (float)(int32_t)(ph >> 32) * 4.656612873077393e-10f;  // half turns, [-1, 1]
-      sincospif(x, &s[e], &c[e]);
-      if (p.negate) s[e] = -s[e];
-    }
-#pragma unroll
-    for (int i = 0; i < kHeads; ++i) {
-#pragma unroll
-      for (int e = 0; e < VE; ++e) {
-        const float x = to_f(a[i].e[e]), y = to_f(b[i].e[e]);
-        a[i].e[e] = from_f<T>(x * c[e] - y * s[e]);
-        b[i].e[e] = from_f<T>(y * c[e] + x * s[e]);
+  };
+  V a, b;
+  Item it;
+  T* dst;
+  load(threadIdx.x, &it, &dst, &a, &b);
+  {
+    // the table: a thread keeps to one pair, whose parameters it reads once
+    const int rows_at_once = kThreads / p.half;
+    const int r0 = (int)threadIdx.x / p.half, pair = (int)threadIdx.x - r0 * p.half;
+    if (r0 < rows_at_once) {
+      const uint64_t turn = p.turn[pair];
+      const int32_t* pos = p.pos + (int64_t)p.axis[pair] * p.n_rows + row0;
+      for (int r = r0; r < n_rows; r += rows_at_once) {
+        const uint64_t ph = (uint64_t)((int64_t)__ldg(pos + r)) * turn;  // modulo a turn
+        const float x = (float)(int32_t)(ph >> 32) * 4.656612873077393e-10f;  // half turns, [-1, 1]
+        float sn, cs;
+        sincospif(x, &sn, &cs);
+        table[r * p.half + pair] = cs;
+        sines[r * p.half + pair] = p.negate ? -sn : sn;
       }
     }
+    __syncthreads();
   }
+#pragma unroll 1
+  for (int e = threadIdx.x; e < n_items; e += kThreads) {
+    // the next item's loads, ahead of this one's arithmetic and stores
+    V a1, b1;
+    Item it1;
+    T* dst1;
+    load(e + kThreads, &it1, &dst1, &a1, &b1);
+    if (it.turns) {
+      const Vec<float, VE>& c = *reinterpret_cast<const Vec<float, VE>*>(table + it.row * p.half + it.c0);
+      const Vec<float, VE>& s = *reinterpret_cast<const Vec<float, VE>*>(sines + it.row * p.half + it.c0);
 #pragma unroll
-  for (int i = 0; i < kHeads; ++i) {
-    const int h = h0 + i;
-    if (h < n_heads) {
-      const int t = h >= p.heads[0];
-      T* dst = static_cast<T*>(p.out[t]) + row * p.out_row[t] + (h - (t ? p.heads[0] : 0)) * p.out_head[t];
-      *reinterpret_cast<V*>(dst + c0) = a[i];
-      if (has1) *reinterpret_cast<V*>(dst + c1) = b[i];
+      for (int i = 0; i < VE; ++i) {
+        const float x = to_f(a.e[i]), y = to_f(b.e[i]);
+        a.e[i] = from_f<T>(x * c.e[i] - y * s.e[i]);
+        b.e[i] = from_f<T>(y * c.e[i] + x * s.e[i]);
+      }
     }
+    *reinterpret_cast<V*>(dst + it.c0) = a;
+    if (it.c1 < p.head_dim) *reinterpret_cast<V*>(dst + it.c1) = b;
+    a = a1;
+    b = b1;
+    it = it1;
+    dst = dst1;
   }
 }
 
@@ -129,12 +161,24 @@ cudaError_t launch_rope(RopeParams& p, bool copy_rest, cudaStream_t s) {
   const int rest = copy_rest ? p.head_dim - 2 * p.half : 0;
   p.rot_items = p.half / VE;
   p.items = p.rot_items + (rest / VE + 1) / 2;
+  int sm = 0;
+  if (device_sm_count(&sm) != STV_OK) return cudaErrorUnknown;
   const int n_heads = p.heads[0] + p.heads[1];
-  p.head_groups = n_heads;
-  const int64_t ids = (int64_t)p.n_rows * p.head_groups * p.items;
-  const int64_t grid = (ids + kThreads - 1) / kThreads;
+  const int64_t all = (int64_t)p.n_rows * n_heads * p.items;
+  // A CTA's share: kShare items per thread for a prompt; down to one where that
+  // leaves SMs idle.
+  const int64_t share = std::max<int64_t>(kThreads, std::min<int64_t>(all / (4 * sm), kShare * kThreads));
+  const int64_t row_items = (int64_t)n_heads * p.items;
+  p.rows_per = (int)std::max<int64_t>(1, std::min<int64_t>({share / row_items, kMaxRowsPer, p.n_rows}));
+  p.heads_per = (int)std::max<int64_t>(1, std::min<int64_t>({share / p.items, n_heads, kMaxHeadsPer}));
+  if (p.rows_per > 1) p.heads_per = std::min(n_heads, kMaxHeadsPer);
+  p.head_blocks = (n_heads + p.heads_per - 1) / p.heads_per;
+  p.heads_per = (n_heads + p.head_blocks - 1) / p.head_blocks;
+  p.items_inv = p.items > 1 ? (uint32_t)((1ull << 32) / p.items + 1) : 0;
+  const int64_t grid = (int64_t)((p.n_rows + p.rows_per - 1) / p.rows_per) * p.head_blocks;
   if (grid > 0x7fffffff) return cudaErrorInvalidValue;
-  return launch_pdl(rope_kernel<T, VE, 1>, (int)grid, kThreads, 0, s, p);
+  const size_t smem = (size_t)p.rows_per * p.half * 2 * sizeof(float);
+  return launch_pdl(rope_kernel<T, VE>, (int)grid, kThreads, smem, s, p);
 }
 
 // Every pair's frequency in turns per position, 2^64 a turn.  The last ones
@@ -257,7 +301,6 @@ extern "C" int stv_rope(const stv_rope_spec* spec, int dtype, int head_dim, cons
   }
   p.pos = pos;
   p.n_rows = n_rows;
-  p.n_axes = na;
   p.half = half;
   p.head_dim = head_dim;
   p.negate = inverse != 0;

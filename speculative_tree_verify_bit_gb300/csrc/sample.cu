@@ -6,7 +6,7 @@
 // vocabulary is needed.  A cluster of CTAs shares a row, each CTA a stretch of
 // it, and sweeps it up to three times (the first time from HBM, then from L2):
 //   1. the maximum (a NaN shows in it);
-//      then some 8,192 tokens, counted by quarter octaves of w, tells how
+//      then some 4,096 tokens, counted by quarter octaves of w, tells how
 //      far down the order the cuts lie: x >= x_cut, the row's head;
 //   2. the mass of all tokens (unless top-k makes it unneeded), and of the
 //      head either the tokens themselves, when they are few, or their counts
@@ -67,7 +67,9 @@ struct SampleParams {
   uint32_t table[64];  // 2^30 * 2^(j / 64)
 };
 
-// What the first CTA decides for its cluster.
+// What the first CTA decides for its cluster: the token is drawn; gather the
+// bins; a cut lies past the head; the head's list overflows.
+enum { kDone, kGather, kTooShort, kTooMany };
 struct Decision {
   int done;
   int kb, pb1, pb2, mb, ub1, ub2;  // bins to gather; empty ranges where a cut is not made
@@ -80,7 +82,8 @@ struct Decision {
 // A row's temperature and maximum as the weights need them.
 struct Scale {
   float max;
-  float floor;  // below it w = 0 (62 octaves under the maximum)
+  float floor;  // 62 octaves under the maximum
+  float zero;   // below it w = 0 (w of 2^-45 of the largest's octave is 0 already)
   float base;   // 0; the maximum where x / C would leave the integers of fp32: there
                 // x - max is exact for every x >= floor
   float least;  // rint(x / C) of the floor, as kMagic + k: smaller ones count as it
@@ -100,21 +103,21 @@ struct Smem {
   uint32_t count[kBins];  // this CTA's bins; first CTA later: a bin's first place in the list
   uint4 ring[kStages][kThreads];  // vectors on their way in, a thread's own slots
   u64 queue[kThreads / 32][64];   // a warp's tokens of the head, taken 32 at a time
-  uint32_t coarse[kCoarse];
-  uint32_t coarse_all[kCoarse];
+  alignas(16) uint32_t coarse[kCoarse];
   uint32_t table[64];
   float table_f[64];
   u64 red[kThreads / 32];
+  uint32_t red_c[kThreads / 32];
   u64 out;
-  double log_kept;  // ln of the kept mass, the largest w being 1
-  double inv_t, c, t_log_m;
+  u64 slot[4];  // first CTA: the cuts' masses and the token
+  double inv_t;
+  float c_hi, c_lo, inv_c, m_hi, m_lo;  // see Scale; T ln min_p in two floats
   // first CTA: what the CTAs of the cluster hand it
   u64 part[kMaxCluster];      // their share of the row's mass
   int n_lists[kMaxCluster];   // tokens that they gathered
   int x_index[kMaxCluster];   // the maximum's first index in their stretch
   float max[kMaxCluster];     // (every CTA's) the maxima of the stretches
-  Scale sc;
-  int found[8];
+  int found[2];
   int n_list;
   Decision d;
 };
@@ -147,26 +150,35 @@ constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: adding it rounds to an inte
 // What does not depend on the maximum (one thread per CTA: fp64 runs at a 64th
 // of the fp32 rate).
 __device__ __forceinline__ void prepare_scale(Smem& s, float temp, float min_p) {
-  s.inv_t = 1.0 / (double)temp;
-  s.c = (double)temp * (0.69314718055994530942 / 64.0);
-  s.t_log_m = min_p > 0.f ? (double)temp * log((double)min_p) : 0.0;
+  const double c = (double)temp * (0.69314718055994530942 / 64.0), inv = 1.0 / (double)temp;
+  const double m = min_p > 0.f ? (double)temp * log((double)min_p) : 0.0;
+  s.inv_t = inv;
+  s.c_hi = (float)c;
+  s.c_lo = (float)(c - (double)s.c_hi);
+  s.inv_c = (float)(inv * (64.0 / 0.69314718055994530942));
+  s.m_hi = (float)m;
+  s.m_lo = (float)(m - (double)s.m_hi);
 }
 __device__ __forceinline__ Scale make_scale(const Smem& s, float max, float min_p) {
   Scale sc;
-  const double c = s.c;
   sc.max = max;
-  sc.c_hi = (float)c;
-  sc.c_lo = (float)(c - (double)sc.c_hi);
-  sc.inv_c = (float)(s.inv_t * (64.0 / 0.69314718055994530942));
+  sc.c_hi = s.c_hi;
+  sc.c_lo = s.c_lo;
+  sc.inv_c = s.inv_c;
   sc.inv_t = (float)s.inv_t;
-  sc.floor = __double2float_rd((double)max - 62.0 * 64.0 * c);
+  sc.floor = __fsub_rd(max, __fmul_ru(62.f * 64.f, s.c_hi));
+  sc.zero = __fsub_rd(max, __fmul_ru(48.f * 64.f, s.c_hi));
   sc.base = fabsf(max) * sc.inv_c < 2097152.f ? 0.f : max;
   const float t = fmaf(max - sc.base, sc.inv_c, kMagic);
   sc.top = __float_as_int(t) >> 6;
   sc.least = t - 62.f * 64.f;
   sc.cut = sc.floor;
   sc.bin_scale = 0.f;
-  sc.x_min = min_p > 0.f ? __double2float_ru((double)max + s.t_log_m) : -INFINITY;
+  sc.x_min = -INFINITY;
+  if (min_p > 0.f) {  // the least float that is not below max + T ln min_p
+    const float a = max + s.m_hi, b = a - max;
+    sc.x_min = __fadd_ru(a, ((max - (a - b)) + (s.m_hi - b)) + s.m_lo);
+  }
   return sc;
 }
 
@@ -294,12 +306,13 @@ __device__ __forceinline__ void sweep(Smem& s, const T* row, int lo, int hi, F&&
       });
 }
 
-// Calls each(x) for every token and f(entry, have) for the ones with x >= cut,
-// by whole warps: a warp collects such tokens in its queue and hands them over
+// Calls each(x) for every token with x >= least (and some others) and
+// f(entry, have) for the ones with x >= cut, by whole warps: a warp collects such tokens in its queue and hands them over
 // 32 at a time, one per lane (have: whether the lane has one), so that what f
 // waits for is paid once for 32 of them.
 template <typename T, typename Each, typename F>
-__device__ __forceinline__ void sweep_head(Smem& s, const T* row, int lo, int hi, float cut, Each&& each, F&& f) {
+__device__ __forceinline__ void sweep_head(Smem& s, const T* row, int lo, int hi, float cut, float least, Each&& each,
+                                           F&& f) {
   const int lane = threadIdx.x & 31;
   u64* queue = s.queue[threadIdx.x >> 5];
   int waiting = 0;  // the same in every lane
@@ -327,7 +340,7 @@ __device__ __forceinline__ void sweep_head(Smem& s, const T* row, int lo, int hi
         float m = -INFINITY;
 #pragma unroll
         for (int k = 0; k < VE; ++k) m = fmaxf(m, to_f(e[k]));
-        if (in) {
+        if (in && m >= least) {
 #pragma unroll
           for (int k = 0; k < VE; ++k) each(to_f(e[k]));
         }
@@ -413,36 +426,55 @@ __device__ __forceinline__ u64 block_scan(u64 x, u64* red) {
 }
 
 // Counts and masses of the bins become those of each bin and all before it.
-__device__ __forceinline__ void accumulate_bins(uint32_t* count, u64* mass, u64* red) {
-  const int b = kBinsPer * threadIdx.x;
-  u64 c = 0, m = 0;
+__device__ __forceinline__ void accumulate_bins(uint32_t* count, u64* mass, u64* red, uint32_t* red_c) {
+  const int b = kBinsPer * threadIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint32_t c[kBinsPer], c_all = 0;
+  u64 m[kBinsPer], m_all = 0;
 #pragma unroll
   for (int i = 0; i < kBinsPer; ++i) {
-    c += count[b + i];
-    m += mass[b + i];
+    c[i] = c_all += count[b + i];
+    m[i] = m_all += mass[b + i];
   }
-  c = block_scan(c, red);
-  m = block_scan(m, red);
+  uint32_t ci = c_all;
+  u64 mi = m_all;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t x = __shfl_up_sync(0xffffffffu, ci, o);
+    const u64 y = __shfl_up_sync(0xffffffffu, mi, o);
+    if (lane >= o) {
+      ci += x;
+      mi += y;
+    }
+  }
+  if (lane == 31) {
+    red_c[warp] = ci;
+    red[warp] = mi;
+  }
+  __syncthreads();
+  uint32_t c0 = ci - c_all;
+  u64 m0 = mi - m_all;
+  for (int w = 0; w < warp; ++w) {
+    c0 += red_c[w];
+    m0 += red[w];
+  }
 #pragma unroll
   for (int i = 0; i < kBinsPer; ++i) {
-    c += count[b + i];
-    m += mass[b + i];
-    count[b + i] = (uint32_t)c;
-    mass[b + i] = m;
+    count[b + i] = c0 + c[i];
+    mass[b + i] = m0 + m[i];
   }
   __syncthreads();
 }
 
-// First bin for which past(bin) holds (it holds for all later ones); kBins - 1
-// if none.
-template <typename F>
-__device__ __forceinline__ int first_bin(F&& past, int* slot) {
-  if (threadIdx.x == 0) *slot = kBins - 1;
-  __syncthreads();
-  for (int b = kBinsPer * threadIdx.x; b < kBinsPer * (int)(threadIdx.x + 1); ++b)
-    if (past(b) && (b == 0 || !past(b - 1))) *slot = b;
-  __syncthreads();
-  return *slot;
+// First bin whose running count or mass reaches t; kBins - 1 if none.  (Every
+// thread searches for itself: eleven broadcast reads, no barrier.)
+template <typename V>
+__device__ __forceinline__ int first_bin(const V* running, V t) {
+  int lo = -1, hi = kBins - 1;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (running[mid] >= t) hi = mid; else lo = mid;
+  }
+  return hi;
 }
 
 // Sorts the first n entries of s.list (n <= kList) ascending, through s.mass:
@@ -526,6 +558,93 @@ __device__ __forceinline__ void sum_list(Smem& s, int n, const Scale& sc) {
     s.mass[threadIdx.x * kPer + k] = at;
   }
   __syncthreads();
+}
+
+// The cuts and the draw among the n gathered tokens (n >= 1): the whole head,
+// or (binned) the tokens of the bins that the cuts lie in.  top_k 0, top_p 1
+// and has_m false: no such cut.  kept: the mass where nothing is cut; on
+// return the kept mass, and the token.  False when a cut lies past the tokens.
+__device__ __forceinline__ bool finish(Smem& s, int n, const Scale& sc, bool binned, int mb, uint32_t top_k,
+                                       float top_p, bool has_m, float u, u64* kept, u64* token) {
+  constexpr int kPer = kList / kThreads;
+  constexpr u64 kNone = ~0ull;
+  if (binned)
+    sort_list(s, n);
+  else
+    sort_list(s, n, sc.max, sc.bin_scale);
+  // a thread's tokens: adjacent ones
+  const int i0 = threadIdx.x * kPer;
+  float x[kPer], x_next = -INFINITY;
+  u64 w[kPer], g[kPer], mine = 0;
+  uint32_t rank[kPer];
+  int bin[kPer], bin_prev = -1;
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    const bool in = i0 + k < n;
+    x[k] = in ? entry_x(s.list[i0 + k]) : -INFINITY;
+    w[k] = in ? weigh(x[k], sc, s.table, s.table_f) : 0;
+    mine += w[k];
+    g[k] = mine;
+    rank[k] = i0 + k + 1;
+    bin[k] = in && binned ? bin_of(x[k], sc) : -1;
+  }
+  if (i0 + kPer < n) x_next = entry_x(s.list[i0 + kPer]);
+  if (binned && i0 > 0 && i0 < n) bin_prev = bin_of(entry_x(s.list[i0 - 1]), sc);
+  if (threadIdx.x < 4) {
+    u64 v = kNone;
+    if (threadIdx.x == 2) v = binned && has_m ? (mb ? s.tot_mass[mb - 1] : 0ull) : kNone;
+    s.slot[threadIdx.x] = v;
+  }
+  const u64 before = block_scan(mine, s.red);
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) g[k] += before;
+  if (binned) {
+    // places and masses in the whole order: by each bin's first token
+#pragma unroll
+    for (int k = 0; k < kPer; ++k)
+      if (bin[k] >= 0 && bin[k] != (k ? bin[k - 1] : bin_prev)) {
+        s.count[bin[k]] = i0 + k;
+        s.mass[bin[k]] = g[k] - w[k];
+      }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kPer; ++k)
+      if (bin[k] >= 0) {
+        const int b = bin[k];
+        rank[k] = (b ? s.tot_count[b - 1] : 0u) + (i0 + k - s.count[b]) + 1;
+        g[k] = (b ? s.tot_mass[b - 1] : 0ull) + g[k] - s.mass[b];
+      }
+  }
+  bool ok = true;
+  if (top_k) {
+#pragma unroll
+    for (int k = 0; k < kPer; ++k)
+      if (i0 + k < n && rank[k] == top_k) s.slot[0] = g[k];
+    __syncthreads();
+    ok = s.slot[0] != kNone;
+    if (ok) *kept = s.slot[0];
+  }
+  if (top_p < 1.f || has_m) {
+    const u64 t = at_least(top_p < 1.f ? top_p : 0.f, *kept);
+#pragma unroll
+    for (int k = 0; k < kPer; ++k)
+      if (i0 + k < n) {
+        if (top_p < 1.f && g[k] >= t && (g[k] - w[k] < t || rank[k] == 1)) s.slot[1] = g[k];
+        const float xn = k + 1 < kPer ? x[k + 1 < kPer ? k + 1 : k] : x_next;
+        if (has_m && (!binned || bin[k] == mb) && x[k] >= sc.x_min && !(xn >= sc.x_min)) s.slot[2] = g[k];
+      }
+    __syncthreads();
+    if (top_p < 1.f) ok = ok && s.slot[1] != kNone;
+    *kept = min(*kept, min(s.slot[1], s.slot[2]));
+  }
+  const u64 t = above(u, *kept);
+#pragma unroll
+  for (int k = 0; k < kPer; ++k)
+    if (i0 + k < n && g[k] >= t && g[k] - w[k] < t) s.slot[3] = s.list[i0 + k];
+  __syncthreads();
+  ok = ok && s.slot[3] != kNone;
+  *token = s.slot[3];
+  return ok;
 }
 
 // Appends tokens to this CTA's list; what does not fit is only counted.
@@ -657,8 +776,9 @@ __device__ __noinline__ void find_in_bin(Smem& s, const T* row, int vocab, const
     });
     __syncthreads();
     join_bins(s);
-    accumulate_bins(s.count, s.mass, s.red);
-    const int at = first_bin([&](int i) { return past(c_before + s.count[i], m_before + s.mass[i]); }, s.found);
+    accumulate_bins(s.count, s.mass, s.red, s.red_c);
+    const int at = rank ? first_bin(s.count, rank - c_before)
+                        : first_bin(s.mass, target > m_before ? target - m_before : 0ull);
     if (at > 0) {
       c_before += s.count[at - 1];
       m_before += s.mass[at - 1];
@@ -721,7 +841,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     // the maximum's first index
     if (!bad) {
       int first = p.vocab;
-      sweep_head(s, row, lo_i, hi_i, row_max, [](float) {},
+      sweep_head(s, row, lo_i, hi_i, row_max, INFINITY, [](float) {},
                  [&](u64 e, bool have) { first = have ? min(first, (int)(uint32_t)e) : first; });
       first = (int)block_min((u64)first, s.red);
       if (tid == 0) s0.x_index[c_rank] = first;
@@ -739,9 +859,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     }
     return;
   }
-  if (tid == 0) s.sc = make_scale(s, row_max, min_p);
-  __syncthreads();
-  Scale sc = s.sc;
+  Scale sc = make_scale(s, row_max, min_p);
   const float x_min = sc.x_min;
   const bool want_k = top_k > 0 && top_k < p.vocab, has_p = top_p < 1.f, want_m = min_p > 0.f;
   const bool m_only = want_m && !want_k && !has_p;  // the head is what min_p keeps
@@ -757,19 +875,22 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     });
     cluster.sync();
     const float f = (float)p.sample_every;
-    if (tid < kCoarse) {
-      uint32_t n = 0;
-#pragma unroll
-      for (int c = 0; c < kMaxCluster; ++c)
-        if (c < c_size) n += cluster.map_shared_rank(&s, c)->coarse[tid];
-      s.coarse_all[tid] = n;
-    }
-    __syncthreads();
     if (tid < 32) {  // a warp: lane l holds eight bins
       float cnt[8], wgt[8], c8 = 0.f, w8 = 0.f, sure = 0.f;
+      uint32_t n[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) n[i] = 0;
+#pragma unroll
+      for (int c = 0; c < kMaxCluster; ++c)
+        if (c < c_size) {
+          const uint4* o = reinterpret_cast<const uint4*>(cluster.map_shared_rank(&s, c)->coarse) + tid * 2;
+          const uint4 a = o[0], b = o[1];
+          n[0] += a.x; n[1] += a.y; n[2] += a.z; n[3] += a.w;
+          n[4] += b.x; n[5] += b.y; n[6] += b.z; n[7] += b.w;
+        }
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        cnt[i] = (float)s.coarse_all[tid * 8 + i];
+        cnt[i] = (float)n[i];
         const float w = exp2f(-0.25f * (float)(tid * 8 + i));
         wgt[i] = f * cnt[i] * w;
         c8 += cnt[i];
@@ -830,17 +951,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
 
   u64 total = 0;  // first CTA: the row's mass, where need_all
   u64 kept = 0, token = 0;
-  for (int round = 0;; ++round) {
-    if (round) {  // the head was too short: every token with any mass
-      set_cut(sc, sc.floor);
-      direct = false;
-    }
-    const bool complete = sc.cut <= sc.floor;
+  bool first_round = true;
+  for (;;) {
+    const bool complete = sc.cut <= sc.floor;  // the head is every token with any mass
     // ---- 2. the mass of all, the head's tokens or bins ----
     if (!direct) clear_bins(s);
     if (tid == 0) s.n_list = 0;
     __syncthreads();
-    const bool all = need_all && round == 0;
+    const bool all = need_all && first_round;
     auto take = [&](u64 e, bool have) {
       if (direct) {
         append_warp(s, e, have);
@@ -851,11 +969,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     };
     if (all) {
       u64 sum = 0;
-      sweep_head(s, row, lo_i, hi_i, sc.cut, [&](float x) { sum += weigh(x, sc, s.table, s.table_f); }, take);
+      sweep_head(s, row, lo_i, hi_i, sc.cut, sc.zero, [&](float x) { sum += weigh(x, sc, s.table, s.table_f); },
+                 take);
       sum = block_sum(sum, s.red);
       if (tid == 0) s0.part[c_rank] = sum;
     } else {
-      sweep_head(s, row, lo_i, hi_i, sc.cut, [](float) {}, take);
+      sweep_head(s, row, lo_i, hi_i, sc.cut, INFINITY, [](float) {}, take);
       __syncthreads();
     }
     if (tid == 0) s0.n_lists[c_rank] = s.n_list;
@@ -898,10 +1017,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       *n_out = n;
       return fits;
     };
-    bool has_k = want_k;
     const bool has_m = want_m && x_min >= sc.cut;
     Decision d;
-    d.done = 0;
+    d.done = kTooShort;
     d.kb = d.mb = -1;
     d.pb1 = d.ub1 = 0;
     d.pb2 = d.ub2 = -1;
@@ -910,69 +1028,38 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         for (int c = 0; c < c_size; ++c) total += s.part[c];
       if (direct) {
         int n;
-        if (merge_lists(&n) && n > 0) {
-          sort_list(s, n, sc.max, sc.bin_scale);
-          sum_list(s, n, sc);
-          const u64 head = s.mass[n - 1];
-          bool ok = true;
-          if (has_k && n < top_k) {
-            ok = complete;
-            has_k = false;
+        if (!merge_lists(&n) || n < 1) {
+          d.done = kTooMany;
+        } else {
+          // all of a complete head may be fewer than top_k
+          const uint32_t k = want_k && !(complete && n < top_k) ? (uint32_t)top_k : 0u;
+          kept = total;
+          if (!need_all && !k) {  // the head's mass
+            sort_list(s, n, sc.max, sc.bin_scale);
+            sum_list(s, n, sc);
+            kept = s.mass[n - 1];
+            __syncthreads();
           }
-          kept = has_k ? s.mass[top_k - 1] : (need_all ? total : head);
-          // the list is sorted: a cut is where a thread's entry is past it and the one before is not
-          if (has_p) {
-            const u64 t = at_least(top_p, kept);
-            ok = ok && head >= t;
-            if (tid == 0) s.out = kept;
-            __syncthreads();
-            for (int i = tid; i < n; i += kThreads)
-              if (s.mass[i] >= t && (i == 0 || s.mass[i - 1] < t)) s.out = min(kept, s.mass[i]);
-            __syncthreads();
-            kept = s.out;
-          }
-          if (has_m) {
-            if (tid == 0) s.part[0] = kept;
-            __syncthreads();
-            for (int i = tid; i < n; i += kThreads)
-              if (entry_x(s.list[i]) >= x_min && (i == n - 1 || entry_x(s.list[i + 1]) < x_min))
-                s.part[0] = min(kept, s.mass[i]);
-            __syncthreads();
-            kept = s.part[0];
-          }
-          const u64 t = above(u, kept);
-          ok = ok && head >= t;
-          if (tid == 0) s.red[0] = s.list[n - 1];
-          __syncthreads();
-          for (int i = tid; i < n; i += kThreads)
-            if (s.mass[i] >= t && (i == 0 || s.mass[i - 1] < t)) s.red[0] = s.list[i];
-          if (tid == kThreads - 1) s.log_kept = log_share(kept, sc, s);
-          __syncthreads();
-          token = s.red[0];
-          d.done = ok;
+          if (finish(s, n, sc, false, 0, k, top_p, has_m, u, &kept, &token)) d.done = kDone;
         }
       } else {
-        accumulate_bins(s.tot_count, s.tot_mass, s.red);
+        accumulate_bins(s.tot_count, s.tot_mass, s.red, s.red_c);
         const uint32_t n_head = s.tot_count[kBins - 1];
         const u64 head = s.tot_mass[kBins - 1];
-        bool ok = true;
-        if (has_k && n_head < (uint32_t)top_k) {
-          ok = complete;
-          has_k = false;
-        }
+        const bool has_k = want_k && !(complete && n_head < (uint32_t)top_k);
+        bool ok = !has_k || n_head >= (uint32_t)top_k;
         // a cut's mass lies between the mass before its first bin and with its last
-        auto reaches = [&](u64 t, int* slot) { return first_bin([&](int b) { return s.tot_mass[b] >= t; }, slot); };
         u64 lo = need_all ? total : head, hi = lo;
         if (has_k) {
-          d.kb = first_bin([&](int b) { return s.tot_count[b] >= (uint32_t)top_k; }, s.found);
+          d.kb = first_bin(s.tot_count, (uint32_t)top_k);
           lo = m_before(d.kb);
           hi = s.tot_mass[d.kb];
         }
         if (has_p) {
           const u64 t = at_least(top_p, hi);
           ok = ok && head >= t;
-          d.pb1 = reaches(at_least(top_p, lo), s.found + 1);
-          d.pb2 = has_k ? reaches(t, s.found + 2) : d.pb1;
+          d.pb1 = first_bin(s.tot_mass, at_least(top_p, lo));
+          d.pb2 = has_k ? first_bin(s.tot_mass, t) : d.pb1;
           lo = min(lo, m_before(d.pb1));
           hi = min(hi, s.tot_mass[d.pb2]);
         }
@@ -983,14 +1070,25 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         }
         const u64 t = above(u, hi);
         ok = ok && head >= t;
-        d.ub1 = reaches(above(u, lo), s.found + 3);
-        d.ub2 = lo < hi ? reaches(t, s.found + 4) : d.ub1;
-        uint32_t mine = 0;
-        for (int b = kBinsPer * tid; b < kBinsPer * (tid + 1); ++b)
-          if (d.wanted(b)) mine += s.tot_count[b] - c_before(b);
-        const uint32_t n = (uint32_t)block_sum(mine, s.red);
-        d.done = ok || round ? 2 : 0;
-        if (d.done && n > kList) {
+        d.ub1 = first_bin(s.tot_mass, above(u, lo));
+        d.ub2 = lo < hi ? first_bin(s.tot_mass, t) : d.ub1;
+        // the tokens of those bins, counted once
+        uint32_t n = 0;
+        {
+          int a[4] = {d.kb, has_p ? d.pb1 : -1, d.mb, d.ub1}, b[4] = {d.kb, d.pb2, d.mb, d.ub2};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            int from = a[i], to = b[i];
+#pragma unroll
+            for (int j = 0; j < i; ++j) {  // less the bins of the ranges before
+              if (a[j] < 0 || a[j] > to || b[j] < from) continue;
+              if (a[j] <= from) from = b[j] + 1; else if (b[j] >= to) to = a[j] - 1;
+            }
+            if (from >= 0 && from <= to) n += s.tot_count[to] - c_before(from);
+          }
+        }
+        if (ok || complete) d.done = kGather;
+        if (d.done == kGather && n > kList) {
           // ---- one cut after the other, without the other CTAs ----
           kept = need_all ? total : head;
           if (has_k)
@@ -998,7 +1096,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
                         &token);
           if (has_p) {
             const u64 tp = at_least(top_p, kept);
-            const int b = reaches(tp, s.found);
+            const int b = first_bin(s.tot_mass, tp);
             u64 m;
             find_in_bin(s, row, p.vocab, sc, b, c_before(b), m_before(b), 0, tp, &m, &token);
             kept = min(kept, m);
@@ -1011,29 +1109,32 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
             kept = min(kept, block_sum(w, s.red));
           }
           const u64 tu = above(u, kept);
-          const int b = reaches(tu, s.found);
+          const int b = first_bin(s.tot_mass, tu);
           u64 m;
           find_in_bin(s, row, p.vocab, sc, b, c_before(b), m_before(b), 0, tu, &m, &token);
-          if (tid == 0) s.log_kept = log_share(kept, sc, s);
-          d.done = 1;
+          d.done = kDone;
         }
       }
       if (tid == 0) s.d = d;
     }
     cluster.sync();
     d = s0.d;
-    if (d.done == 0 && round == 0) {
+    if (d.done == kTooMany || d.done == kTooShort) {
+      // once more with bins; where a cut lies past the head, with all tokens that have mass
+      direct = false;
+      first_round = false;
+      if (d.done == kTooShort) set_cut(sc, sc.floor);
       cluster.sync();  // the decision is read before it is written again
       continue;
     }
-    if (d.done != 2) {
+    if (d.done == kDone) {
       cluster.sync();  // the first CTA does not end while its decision is read
       break;
     }
     // ---- 3. the tokens of the cuts' bins ----
     if (tid == 0) s.n_list = 0;
     __syncthreads();
-    sweep_head(s, row, lo_i, hi_i, sc.cut, [](float) {},
+    sweep_head(s, row, lo_i, hi_i, sc.cut, INFINITY, [](float) {},
                [&](u64 e, bool have) { append_warp(s, e, have && d.wanted(bin_of(entry_x(e), sc))); });
     __syncthreads();
     if (tid == 0) s0.n_lists[c_rank] = s.n_list;
@@ -1041,65 +1142,16 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     if (c_rank == 0) {
       int n;
       merge_lists(&n);  // counted above: they fit
-      sort_list(s, n);
-      sum_list(s, n, sc);
-      for (int i = tid; i < n; i += kThreads) {
-        const int b = bin_of(entry_x(s.list[i]), sc);
-        if (i == 0 || bin_of(entry_x(s.list[i - 1]), sc) != b) s.count[b] = i;
-      }
-      __syncthreads();
-      // entry i: its bin, rank and running mass in the whole order
-      auto place = [&](int i, int* b, uint32_t* rank, u64* g) {
-        *b = bin_of(entry_x(s.list[i]), sc);
-        const int f = s.count[*b];
-        *rank = c_before(*b) + (i - f) + 1;
-        *g = m_before(*b) + s.mass[i] - (f ? s.mass[f - 1] : 0ull);
-      };
-      // the smallest running mass among the entries that `in` admits
-      auto least = [&](auto&& in) {
-        u64 m = ~0ull;
-        for (int i = tid; i < n; i += kThreads) {
-          int b;
-          uint32_t rank;
-          u64 g;
-          place(i, &b, &rank, &g);
-          if (in(b, rank, g)) m = min(m, g);
-        }
-        return block_min(m, s.red);
-      };
       kept = need_all ? total : s.tot_mass[kBins - 1];
-      if (d.kb >= 0) kept = least([&](int b, uint32_t rank, u64) { return b == d.kb && rank == (uint32_t)top_k; });
-      if (has_p) {
-        const u64 t = at_least(top_p, kept);
-        kept = min(kept, least([&](int, uint32_t, u64 g) { return g >= t; }));
-      }
-      if (has_m) {
-        u64 w = 0;
-        for (int i = tid; i < n; i += kThreads) {
-          const float x = entry_x(s.list[i]);
-          if (bin_of(x, sc) == d.mb && x >= x_min) w += weigh(x, sc, s.table, s.table_f);
-        }
-        kept = min(kept, m_before(d.mb) + block_sum(w, s.red));
-      }
-      const u64 t = above(u, kept);
-      u64 at = n - 1;
-      for (int i = tid; i < n; i += kThreads) {
-        int b;
-        uint32_t rank;
-        u64 g;
-        place(i, &b, &rank, &g);
-        if (g >= t) at = min(at, (u64)i);
-      }
-      if (tid == kThreads - 1) s.log_kept = log_share(kept, sc, s);
-      at = block_min(at, s.red);
-      token = s.list[at];
+      if (n > 0) finish(s, n, sc, true, d.mb, d.kb >= 0 ? (uint32_t)top_k : 0u, top_p, has_m, u, &kept, &token);
     }
     cluster.sync();  // no CTA ends while the first one reads its list
     break;
   }
   if (c_rank == 0 && tid == 0) {
     p.ids[r] = (int32_t)(uint32_t)token;
-    if (p.logprob) p.logprob[r] = (float)(((double)entry_x(token) - (double)sc.max) * s.inv_t - s.log_kept);
+    if (p.logprob)
+      p.logprob[r] = (float)(((double)entry_x(token) - (double)sc.max) * s.inv_t - log_share(kept, sc, s));
   }
 }
 
@@ -1112,7 +1164,7 @@ cudaError_t launch_sample(SampleParams& p, cudaStream_t st) {
   while (c < kMaxCluster && (int64_t)p.n_rows * c * 2 <= 2 * sm && p.vocab / (2 * c) >= 2048) c *= 2;
   constexpr int VE = 16 / sizeof(T);
   p.stretch = ((p.vocab + c - 1) / c + VE - 1) / VE * VE;
-  p.sample_every = std::max(1, p.vocab / 8192);
+  p.sample_every = std::max(1, p.vocab / 4096);
   const size_t smem = sizeof(Smem);
   cudaError_t e = cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e == cudaSuccess) {
