@@ -4,17 +4,22 @@
 // Every filter and the draw itself is a cut of one order (logit descending,
 // then index ascending) at a given count or a given mass, so no sort of the
 // vocabulary is needed.  A cluster of CTAs shares a row, each CTA a stretch of
-// it, and sweeps it up to three times (the first time from HBM, then from L2):
-//   1. the maximum (a NaN shows in it);
-//      then some 4,096 tokens, counted by quarter octaves of w, tells how
-//      far down the order the cuts lie: x >= x_cut, the row's head;
-//   2. the mass of all tokens (unless top-k makes it unneeded), and of the
-//      head either the tokens themselves, when they are few, or their counts
-//      and masses in 2,048 bins;
-//   3. the tokens of the few bins that the cuts lie in.
-// The first CTA sorts the gathered tokens and makes the cuts exactly.  The
-// sample only chooses x_cut: when the head turns out too short, steps 2 and 3
-// run once more with every token that has any mass.
+// it:
+//   1. One pass over the stretch finds the maximum (a NaN shows in it) of each
+//      of some thousand groups of tokens, and from the largest of those a
+//      value that about as many tokens exceed as the cuts should need.
+//   2. A second pass (from shared memory where the stretch fits, else from L2)
+//      gathers the tokens above it, and adds up the mass of all (unless top-k
+//      or min-p alone make that unneeded).
+// The first CTA merges the tokens above the largest of the CTAs' values, sorts
+// them, and makes the cuts exactly.  Where a cut lies further down (a flat
+// distribution, top-p of a long tail):
+//   3. A sample of some 4,096 tokens, counted by quarter octaves of w, tells
+//      how far down; the tokens from there up are counted and their masses
+//      added in 2,048 bins; the tokens of the few bins that the cuts lie in are
+//      gathered and sorted.  (Where even that falls short: once more, with every
+//      token that has any mass.)
+// What is chosen by groups and samples is only how much is gathered.
 //
 // Masses.  w = exp((x - max) / T) as an integer of scale 2^45.  With C =
 // T ln 2 / 64, k = rint(x / C) and z = x - k C (C in two floats; the first
@@ -28,6 +33,7 @@
 #include <string.h>
 
 #include <algorithm>
+#include <utility>
 
 #include "stv_device.cuh"
 
@@ -42,12 +48,14 @@ constexpr int kThreads = 512;
 constexpr int kBins = 2048;
 constexpr int kBinsPer = kBins / kThreads;
 constexpr int kList = 2048;      // tokens gathered around the cuts
-constexpr int kDirect = 1400;    // a head estimated at this many tokens is gathered at once
-constexpr float kLeastHead = 512.f;
+constexpr int kDirect = 1700;    // more tokens than this are not gathered at once
+constexpr float kLeastHead = 384.f;  // tokens gathered where top-k asks for no number
+constexpr float kBinnedHead = 512.f;
 constexpr int kCoarse = 256;     // quarter octaves of the sample
 constexpr int kMaxVocab = 1 << 19;
+constexpr int64_t kL2Bytes = 80 << 20;  // of 126 MB, for the rows at work at a time
 constexpr int kShift = 14;       // w < 2^45: 2^19 tokens stay below 2^64
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 16;
 constexpr int kStages = 4;       // one being read, three on their way
 
 struct SampleParams {
@@ -56,6 +64,7 @@ struct SampleParams {
   int n_rows, vocab, rows_per_param;
   int stretch;       // tokens per CTA of a cluster
   int sample_every;  // 1: the sample is everything
+  int resident;      // the stretches stay in shared memory
   const float* temperature;
   const int32_t* top_k;
   const float* top_p;
@@ -68,8 +77,8 @@ struct SampleParams {
 };
 
 // What the first CTA decides for its cluster: the token is drawn; gather the
-// bins; a cut lies past the head; the head's list overflows.
-enum { kDone, kGather, kTooShort, kTooMany };
+// bins; a cut lies past the head.
+enum { kDone, kGather, kTooShort };
 struct Decision {
   int done;
   int kb, pb1, pb2, mb, ub1, ub2;  // bins to gather; empty ranges where a cut is not made
@@ -94,14 +103,13 @@ struct Scale {
   float x_min;      // the least x that min_p keeps
 };
 
-struct Smem {
-  u64 tot_mass[kBins];  // first CTA: the row's bins, then of each and all before
+struct alignas(16) Smem {
+  u64 tot_mass[kBins];  // first CTA: the merged lists; or the row's bins, then of each and all before
   u64 mass[kBins];      // this CTA's bins (low and high words apart); first CTA later:
                         // running mass over the list
   u64 list[kList];      // (~key << 32) | index
   uint32_t tot_count[kBins];
   uint32_t count[kBins];  // this CTA's bins; first CTA later: a bin's first place in the list
-  uint4 ring[kStages][kThreads];  // vectors on their way in, a thread's own slots
   u64 queue[kThreads / 32][64];   // a warp's tokens of the head, taken 32 at a time
   alignas(16) uint32_t coarse[kCoarse];
   uint32_t table[64];
@@ -109,18 +117,25 @@ struct Smem {
   u64 red[kThreads / 32];
   uint32_t red_c[kThreads / 32];
   u64 out;
-  u64 slot[4];  // first CTA: the cuts' masses and the token
+  u64 slot[5];  // first CTA: the cuts' masses, the token, the tokens' mass
   double inv_t;
   float c_hi, c_lo, inv_c, m_hi, m_lo;  // see Scale; T ln min_p in two floats
   // first CTA: what the CTAs of the cluster hand it
   u64 part[kMaxCluster];      // their share of the row's mass
   int n_lists[kMaxCluster];   // tokens that they gathered
   int x_index[kMaxCluster];   // the maximum's first index in their stretch
+  float cut[kMaxCluster];     // the value above which they gathered
   float max[kMaxCluster];     // (every CTA's) the maxima of the stretches
   int found[2];
   int n_list;
   Decision d;
 };
+
+// Behind it: the slots that vectors come in through, a thread's own in each
+// row of kThreads; kStages rows, or the CTA's whole stretch (resident).
+__device__ __forceinline__ uint4* slots(Smem& s) {
+  return reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(&s) + sizeof(Smem));
+}
 
 template <typename T> __device__ __forceinline__ float to_f(T x);
 template <> __device__ __forceinline__ float to_f(float x) { return x; }
@@ -245,13 +260,19 @@ __device__ __forceinline__ void copy_async(uint4* dst, const uint4* src) {
                : "memory");
 }
 
+// How a CTA reads its stretch: through the ring, or held in shared memory from
+// the first pass on.
+enum Held { kStream, kLoad, kHeld };
+
 // Sweeps the tokens [lo, hi) of a row by whole warps: many(vector, its first
 // index, whether this lane has one) for the 16-byte vectors, one(value, index,
 // whether) for the ends that do not fill a vector (at most VE - 1 each, by the
-// first warp).  Vectors come in through the thread's own slots of the ring,
-// kStages - 1 ahead, without taking registers or barriers.
+// first warp).  Vectors come in through the thread's own slots, without taking
+// registers or barriers: kStages - 1 ahead (kStream), or all at once into their
+// places (kLoad), where they are found later (kHeld, the same tokens).
 template <typename T, typename Many, typename One>
-__device__ __forceinline__ void sweep_vectors(Smem& s, const T* row, int lo, int hi, Many&& many, One&& one) {
+__device__ __forceinline__ void sweep_vectors(Smem& s, const T* row, int lo, int hi, Held held, Many&& many,
+                                              One&& one) {
   constexpr int VE = 16 / sizeof(T);
   const int lane = threadIdx.x & 31;
   const T* p = row + lo;
@@ -259,28 +280,38 @@ __device__ __forceinline__ void sweep_vectors(Smem& s, const T* row, int lo, int
   const int head = min(n, (int)(((16 - ((uintptr_t)p & 15)) & 15) / sizeof(T)));
   const int n_vec = (n - head) / VE;
   const uint4* v = reinterpret_cast<const uint4*>(p + head);
-  uint4* ring = &s.ring[0][threadIdx.x];
+  uint4* ring = slots(s) + threadIdx.x;
   int i = threadIdx.x;
-#pragma unroll
-  for (int a = 0; a < kStages - 1; ++a) {
-    if (i + a * kThreads < n_vec) copy_async(ring + a * kThreads, v + i + a * kThreads);
+  if (held == kLoad) {
+    for (int j = i, at = 0; j < n_vec; j += kThreads, at += kThreads) copy_async(ring + at, v + j);
     asm volatile("cp.async.commit_group;" ::: "memory");
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+  } else if (held == kStream) {
+#pragma unroll
+    for (int a = 0; a < kStages - 1; ++a) {
+      if (i + a * kThreads < n_vec) copy_async(ring + a * kThreads, v + i + a * kThreads);
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    }
   }
   int at = 0, put = (kStages - 1) * kThreads;
 #pragma unroll 1
   for (; i - lane < n_vec; i += kThreads) {
-    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
     const bool in = i < n_vec;
-    const uint4 now = ring[at];
-    // the slot of the vector before, which has been used
-    const int next = i + (kStages - 1) * kThreads;
-    if (next < n_vec) copy_async(ring + put, v + next);
-    asm volatile("cp.async.commit_group;" ::: "memory");
-    put = at;
-    at = at == (kStages - 1) * kThreads ? 0 : at + kThreads;
+    if (held == kStream) asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+    const uint4 now = in || held == kStream ? ring[at] : make_uint4(0, 0, 0, 0);
+    if (held == kStream) {
+      // the slot of the vector before, which has been used
+      const int next = i + (kStages - 1) * kThreads;
+      if (next < n_vec) copy_async(ring + put, v + next);
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      put = at;
+      at = at == (kStages - 1) * kThreads ? 0 : at + kThreads;
+    } else {
+      at += kThreads;
+    }
     many(now, lo + head + i * VE, in);
   }
-  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  if (held == kStream) asm volatile("cp.async.wait_group 0;" ::: "memory");
   const int rest = n - head - n_vec * VE;
   if ((int)threadIdx.x < 32) {
     const bool in = lane < head + rest;
@@ -293,7 +324,7 @@ __device__ __forceinline__ void sweep_vectors(Smem& s, const T* row, int lo, int
 template <typename T, typename F>
 __device__ __forceinline__ void sweep(Smem& s, const T* row, int lo, int hi, F&& f) {
   sweep_vectors(
-      s, row, lo, hi,
+      s, row, lo, hi, kStream,
       [&](const uint4& q, int i, bool in) {
         const T* e = reinterpret_cast<const T*>(&q);
         if (in) {
@@ -311,8 +342,8 @@ __device__ __forceinline__ void sweep(Smem& s, const T* row, int lo, int hi, F&&
 // 32 at a time, one per lane (have: whether the lane has one), so that what f
 // waits for is paid once for 32 of them.
 template <typename T, typename Each, typename F>
-__device__ __forceinline__ void sweep_head(Smem& s, const T* row, int lo, int hi, float cut, float least, Each&& each,
-                                           F&& f) {
+__device__ __forceinline__ void sweep_head(Smem& s, const T* row, int lo, int hi, Held held, float cut, float least,
+                                           Each&& each, F&& f) {
   const int lane = threadIdx.x & 31;
   u64* queue = s.queue[threadIdx.x >> 5];
   int waiting = 0;  // the same in every lane
@@ -333,7 +364,7 @@ __device__ __forceinline__ void sweep_head(Smem& s, const T* row, int lo, int hi
     }
   };
   sweep_vectors(
-      s, row, lo, hi,
+      s, row, lo, hi, held,
       [&](const uint4& q, int i, bool in) {
         constexpr int VE = 16 / sizeof(T);
         const T* e = reinterpret_cast<const T*>(&q);
@@ -477,13 +508,27 @@ __device__ __forceinline__ int first_bin(const V* running, V t) {
   return hi;
 }
 
-// Sorts the first n entries of s.list (n <= kList) ascending, through s.mass:
-// a token's place is the number of tokens in the bins before its own (of 2,048
-// from `top` down, `scale` to a unit of x) and of smaller ones in it.  Few
-// tokens share a bin, unless they are equal.
-__device__ __forceinline__ void sort_list(Smem& s, int n, float top, float scale) {
+// Sorts n entries (n <= kList) of `src` ascending into s.list, by way of
+// s.mass; src may be s.list.
+//
+// Up to 256: two threads count the entries that precede one.  More: an entry's
+// place is the number of entries in the bins before its own (of 2,048 from
+// `top` down, `scale` to a unit of x) and of smaller ones in it; few share a
+// bin, unless they are equal.
+__device__ __forceinline__ void sort_list(Smem& s, const u64* src, int n, float top, float scale) {
   constexpr int kPer = kList / kThreads;
-  if (n <= 1) return;
+  if (n <= kThreads / 2) {
+    const int i = (int)threadIdx.x >> 1;
+    const u64 e = i < n ? src[i] : 0;
+    int before = 0;
+    if (i < n)
+      for (int j = threadIdx.x & 1; j < n; j += 2) before += src[j] < e;
+    before += __shfl_xor_sync(0xffffffffu, before, 1);
+    __syncthreads();
+    if (i < n && !(threadIdx.x & 1)) s.list[before] = e;
+    __syncthreads();
+    return;
+  }
 #pragma unroll
   for (int k = 0; k < kBinsPer; ++k) s.count[threadIdx.x + k * kThreads] = 0;
   __syncthreads();
@@ -493,7 +538,7 @@ __device__ __forceinline__ void sort_list(Smem& s, int n, float top, float scale
   for (int k = 0; k < kPer; ++k) {
     const int i = threadIdx.x + k * kThreads;
     if (i < n) {
-      e[k] = s.list[i];
+      e[k] = src[i];
       bin[k] = min(kBins - 1, __float2int_rd((top - entry_x(e[k])) * scale));
       atomicAdd(s.count + bin[k], 1u);
     }
@@ -530,15 +575,20 @@ __device__ __forceinline__ void sort_list(Smem& s, int n, float top, float scale
   __syncthreads();
 }
 
-// The same, with the bins laid between the list's largest and smallest value.
+// s.list in place, with the bins laid between its largest and smallest value.
 __device__ __forceinline__ void sort_list(Smem& s, int n) {
-  u64 lo = ~0ull, hi = 0;
-  for (int i = threadIdx.x; i < n; i += kThreads) {
-    lo = min(lo, s.list[i]);
-    hi = max(hi, s.list[i]);
+  float top = 0.f, scale = 0.f;
+  if (n > kThreads / 2) {
+    u64 lo = ~0ull, hi = 0;
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+      lo = min(lo, s.list[i]);
+      hi = max(hi, s.list[i]);
+    }
+    top = entry_x(block_min(lo, s.red));
+    const float low = entry_x(block_max(hi, s.red));
+    scale = top > low ? fminf((float)kBins / (top - low), 3e38f) : 0.f;
   }
-  const float top = entry_x(block_min(lo, s.red)), low = entry_x(block_max(hi, s.red));
-  sort_list(s, n, top, top > low ? fminf((float)kBins / (top - low), 3e38f) : 0.f);
+  sort_list(s, s.list, n, top, scale);
 }
 
 // Running masses (inclusive) over the sorted list into s.mass.
@@ -560,18 +610,16 @@ __device__ __forceinline__ void sum_list(Smem& s, int n, const Scale& sc) {
   __syncthreads();
 }
 
-// The cuts and the draw among the n gathered tokens (n >= 1): the whole head,
-// or (binned) the tokens of the bins that the cuts lie in.  top_k 0, top_p 1
-// and has_m false: no such cut.  kept: the mass where nothing is cut; on
-// return the kept mass, and the token.  False when a cut lies past the tokens.
+// The cuts and the draw among the n gathered tokens, sorted in s.list (n >= 1):
+// the whole head, or (binned) the tokens of the bins that the cuts lie in.
+// top_k 0, top_p 1 and has_m false: no such cut.  kept: the mass where nothing
+// is cut (kAll: that of the tokens); on return the kept mass, and the token.
+// False when a cut lies past the tokens.
+constexpr u64 kAll = ~0ull;
 __device__ __forceinline__ bool finish(Smem& s, int n, const Scale& sc, bool binned, int mb, uint32_t top_k,
                                        float top_p, bool has_m, float u, u64* kept, u64* token) {
   constexpr int kPer = kList / kThreads;
   constexpr u64 kNone = ~0ull;
-  if (binned)
-    sort_list(s, n);
-  else
-    sort_list(s, n, sc.max, sc.bin_scale);
   // a thread's tokens: adjacent ones
   const int i0 = threadIdx.x * kPer;
   float x[kPer], x_next = -INFINITY;
@@ -590,7 +638,7 @@ __device__ __forceinline__ bool finish(Smem& s, int n, const Scale& sc, bool bin
   }
   if (i0 + kPer < n) x_next = entry_x(s.list[i0 + kPer]);
   if (binned && i0 > 0 && i0 < n) bin_prev = bin_of(entry_x(s.list[i0 - 1]), sc);
-  if (threadIdx.x < 4) {
+  if (threadIdx.x < 5) {
     u64 v = kNone;
     if (threadIdx.x == 2) v = binned && has_m ? (mb ? s.tot_mass[mb - 1] : 0ull) : kNone;
     s.slot[threadIdx.x] = v;
@@ -598,6 +646,13 @@ __device__ __forceinline__ bool finish(Smem& s, int n, const Scale& sc, bool bin
   const u64 before = block_scan(mine, s.red);
 #pragma unroll
   for (int k = 0; k < kPer; ++k) g[k] += before;
+  if (*kept == kAll) {
+#pragma unroll
+    for (int k = 0; k < kPer; ++k)
+      if (i0 + k == n - 1) s.slot[4] = g[k];
+    __syncthreads();
+    *kept = s.slot[4];
+  }
   if (binned) {
     // places and masses in the whole order: by each bin's first token
 #pragma unroll
@@ -804,6 +859,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     s.table_f[tid] = (float)p.table[tid] * 0.25f;
   }
   if (tid < kCoarse) s.coarse[tid] = 0;
+  // shared memory of a CTA may be written by another once all have started
+  cg::cluster_group::arrival_token started = cluster.barrier_arrive();
   grid_dep_wait();
   grid_dep_launch();
   const T* row = static_cast<const T*>(p.x) + (int64_t)r * p.row_stride;
@@ -815,23 +872,86 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   const float min_p = p.min_p ? __ldg(p.min_p + pi) : 0.f;
   const float u = __ldg(p.u + r);
 
-  // ---- 1. the maximum, and whether anything is wrong ----
+  const Held load = p.resident ? kLoad : kStream, again = p.resident ? kHeld : kStream;
+  const bool want_k = top_k > 0 && top_k < p.vocab, has_p = top_p < 1.f, want_m = min_p > 0.f;
+  // the tokens that this CTA should gather: with the others', four deviations
+  // more than top_k
+  constexpr int VE = 16 / sizeof(T);
+  constexpr float kGroups = kThreads * VE;
+  float share = want_k ? (float)top_k / (float)c_size : kLeastHead / (float)c_size;
+  if (want_k && c_size > 1) share = fminf((float)top_k, share + 4.f * sqrtf(share) + 8.f);
+  // as many of kGroups groups' maxima lie that high as hold one of them or more
+  bool direct = share * (float)c_size * (share > 0.3f * kGroups ? 1.5f : 1.2f) <= (float)kDirect &&
+                share < 0.6f * kGroups;
+
+  // ---- 1. the groups' maxima, and whether anything is wrong ----
   if (tid == kThreads - 1) prepare_scale(s, temp, min_p);
+  float top[VE];  // of this thread's tokens, by their place in a vector
+#pragma unroll
+  for (int k = 0; k < VE; ++k) top[k] = -INFINITY;
+  float cta_max;
   {
-    float mx = -INFINITY;
-    sweep(s, row, lo_i, hi_i, [&](float x, int) { mx = max_nan(mx, x); });
+    float ends = -INFINITY;
+    sweep_vectors(
+        s, row, lo_i, hi_i, load,
+        [&](const uint4& q, int, bool in) {
+          const T* e = reinterpret_cast<const T*>(&q);
+          if (in) {
+#pragma unroll
+            for (int k = 0; k < VE; ++k) top[k] = max_nan(top[k], to_f(e[k]));
+          }
+        },
+        [&](float x, int, bool in) {
+          if (in) ends = x;
+        });
+    float mx = ends;
+#pragma unroll
+    for (int k = 0; k < VE; ++k) mx = max_nan(mx, top[k]);
 #pragma unroll
     for (int o = 16; o; o >>= 1) mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, o));
     float* red = reinterpret_cast<float*>(s.red);
     if ((tid & 31) == 0) red[tid >> 5] = mx;
     __syncthreads();
-    if (tid < c_size) {  // to every CTA of the cluster
-      mx = red[0];
-      for (int w = 1; w < kThreads / 32; ++w) mx = max_nan(mx, red[w]);
-      cluster.map_shared_rank(&s, tid)->max[c_rank] = mx;
+    cta_max = red[tid & (kThreads / 32 - 1)];
+#pragma unroll
+    for (int o = kThreads / 64; o; o >>= 1) cta_max = max_nan(cta_max, __shfl_xor_sync(0xffffffffu, cta_max, o));
+    cluster.barrier_wait(std::move(started));
+    if (tid < c_size) cluster.map_shared_rank(&s, tid)->max[c_rank] = cta_max;  // to every CTA
+  }
+  cg::cluster_group::arrival_token arrived = cluster.barrier_arrive();
+  // the value that about `share` of this CTA's tokens exceed: the groups'
+  // maxima counted by eighths of an octave
+  const float per8 = 8.f / 64.f * s.inv_c;  // to a unit of x
+  if (direct) {
+#pragma unroll
+    for (int k = 0; k < VE; ++k) {
+      const float y = (cta_max - top[k]) * per8;
+      if (y >= 0.f && y < (float)kCoarse) atomicAdd(s.coarse + (int)y, 1u);
+    }
+    __syncthreads();
+    if (tid < 32) {
+      uint32_t n[8], sum = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum += n[i] = s.coarse[tid * 8 + i];
+      uint32_t incl = sum;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t a = __shfl_up_sync(0xffffffffu, incl, o);
+        if (tid >= o) incl += a;
+      }
+      uint32_t c = incl - sum;
+      int b = kCoarse;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        c += n[i];
+        if (b == kCoarse && (float)c >= share) b = tid * 8 + i + 1;
+      }
+      b = __reduce_min_sync(0xffffffffu, b);
+      if (tid == 0) s.found[0] = b;
     }
   }
-  cluster.sync();
+  cluster.barrier_wait(std::move(arrived));
+  __syncthreads();
   float row_max = s.max[0];
   for (int c = 1; c < c_size; ++c) row_max = max_nan(row_max, s.max[c]);
   const bool bad = !(row_max > -INFINITY && row_max < INFINITY) ||
@@ -841,7 +961,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     // the maximum's first index
     if (!bad) {
       int first = p.vocab;
-      sweep_head(s, row, lo_i, hi_i, row_max, INFINITY, [](float) {},
+      sweep_head(s, row, lo_i, hi_i, again, row_max, INFINITY, [](float) {},
                  [&](u64 e, bool have) { first = have ? min(first, (int)(uint32_t)e) : first; });
       first = (int)block_min((u64)first, s.red);
       if (tid == 0) s0.x_index[c_rank] = first;
@@ -861,104 +981,98 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   }
   Scale sc = make_scale(s, row_max, min_p);
   const float x_min = sc.x_min;
-  const bool want_k = top_k > 0 && top_k < p.vocab, has_p = top_p < 1.f, want_m = min_p > 0.f;
   const bool m_only = want_m && !want_k && !has_p;  // the head is what min_p keeps
   const bool need_all = !want_k && !m_only;         // the mass of every token
-
-  // ---- the sample: how far down the cuts lie, and how many tokens that is ----
-  bool direct;
-  {
-    const float per = 4.f / 64.f * sc.inv_c;  // quarter octaves per unit of x
-    sweep_sample(row, lo_i, hi_i, p.sample_every, [&](float x) {
-      const float y = (sc.max - x) * per;
-      if (y < (float)(kCoarse - 8)) atomicAdd(s.coarse + (int)y, 1u);
-    });
-    cluster.sync();
-    const float f = (float)p.sample_every;
-    if (tid < 32) {  // a warp: lane l holds eight bins
-      float cnt[8], wgt[8], c8 = 0.f, w8 = 0.f, sure = 0.f;
-      uint32_t n[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) n[i] = 0;
-#pragma unroll
-      for (int c = 0; c < kMaxCluster; ++c)
-        if (c < c_size) {
-          const uint4* o = reinterpret_cast<const uint4*>(cluster.map_shared_rank(&s, c)->coarse) + tid * 2;
-          const uint4 a = o[0], b = o[1];
-          n[0] += a.x; n[1] += a.y; n[2] += a.z; n[3] += a.w;
-          n[4] += b.x; n[5] += b.y; n[6] += b.z; n[7] += b.w;
-        }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        cnt[i] = (float)n[i];
-        const float w = exp2f(-0.25f * (float)(tid * 8 + i));
-        wgt[i] = f * cnt[i] * w;
-        c8 += cnt[i];
-        w8 += wgt[i];
-        // surely there: two deviations under the sample's count
-        sure += fmaxf(cnt[i], f * (cnt[i] - 2.f * sqrtf(cnt[i]))) * w;
-      }
-#pragma unroll
-      for (int o = 16; o; o >>= 1) sure += __shfl_xor_sync(0xffffffffu, sure, o);
-      float c_incl = c8, w_incl = w8;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const float a = __shfl_up_sync(0xffffffffu, c_incl, o), b = __shfl_up_sync(0xffffffffu, w_incl, o);
-        if (tid >= o) {
-          c_incl += a;
-          w_incl += b;
-        }
-      }
-      const float w_all = __shfl_sync(0xffffffffu, w_incl, 31);
-      // enough: top_k tokens with four deviations of the sample's count; what
-      // min_p keeps; or a tail of under 0.7 of what the cut leaves out of the
-      // mass that is surely there, the maximum's 1 with it, below a head of so
-      // many tokens that the sample knows what lies beneath
-      const float k_need = (float)top_k / f;
-      const float enough = p.sample_every > 1 ? k_need + 4.f * sqrtf(k_need) + 8.f : k_need;
-      const float left = has_p ? 1.f - top_p : 1.f - u;
-      const float tail = 0.7f * left * (1.f + sure);
-      int b = kCoarse;
-      float n_head = 0.f, c = c_incl - c8, w = w_incl - w8;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {  // the bins up to this one are enough
-        c += cnt[i];
-        w += wgt[i];
-        const int past = tid * 8 + i + 1;
-        const bool ok = m_only ? (float)past > (sc.max - x_min) * per
-                               : (want_k ? c >= enough : w_all - w <= tail && c * f >= kLeastHead);
-        if (ok && b == kCoarse) {
-          b = past;
-          n_head = c;
-        }
-      }
-      const unsigned any = __ballot_sync(0xffffffffu, b < kCoarse);
-      const int src = any ? __ffs(any) - 1 : 31;
-      b = __shfl_sync(0xffffffffu, b, src);
-      n_head = __shfl_sync(0xffffffffu, any ? n_head : c_incl, src);
-      if (tid == 0) {
-        s.found[0] = b;
-        s.found[1] = (int)fminf(n_head * f, 1e9f);
-      }
-    }
-    __syncthreads();
+  if (direct) {
     const int b = s.found[0];
-    float cut = b < kCoarse - 8 ? sc.max - (float)b / per : sc.floor;
-    if (m_only) cut = x_min;
-    set_cut(sc, cut);
-    direct = s.found[1] <= kDirect;
+    set_cut(sc, m_only ? x_min : (b < kCoarse ? cta_max - (float)b / per8 : sc.floor));
   }
 
   u64 total = 0;  // first CTA: the row's mass, where need_all
   u64 kept = 0, token = 0;
-  bool first_round = true;
-  for (;;) {
-    const bool complete = sc.cut <= sc.floor;  // the head is every token with any mass
+  for (int round = 0;; ++round) {
+    if (round == 1) {
+      // ---- 3. the sample: how far down the cuts lie ----
+      if (tid < kCoarse) s.coarse[tid] = 0;
+      __syncthreads();
+      const float per = 4.f / 64.f * sc.inv_c;  // quarter octaves per unit of x
+      sweep_sample(row, lo_i, hi_i, p.sample_every, [&](float x) {
+        const float y = (sc.max - x) * per;
+        if (y < (float)(kCoarse - 8)) atomicAdd(s.coarse + (int)y, 1u);
+      });
+      cluster.sync();
+      const float f = (float)p.sample_every;
+      if (tid < 32) {  // a warp: lane l holds eight bins
+        float cnt[8], wgt[8], c8 = 0.f, w8 = 0.f, sure = 0.f;
+        uint32_t n[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) n[i] = 0;
+#pragma unroll
+        for (int c = 0; c < kMaxCluster; ++c)
+          if (c < c_size) {
+            const uint4* o = reinterpret_cast<const uint4*>(cluster.map_shared_rank(&s, c)->coarse) + tid * 2;
+            const uint4 a = o[0], b = o[1];
+            n[0] += a.x; n[1] += a.y; n[2] += a.z; n[3] += a.w;
+            n[4] += b.x; n[5] += b.y; n[6] += b.z; n[7] += b.w;
+          }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          cnt[i] = (float)n[i];
+          const float w = exp2f(-0.25f * (float)(tid * 8 + i));
+          wgt[i] = f * cnt[i] * w;
+          c8 += cnt[i];
+          w8 += wgt[i];
+          // surely there: two deviations under the sample's count
+          sure += fmaxf(cnt[i], f * (cnt[i] - 2.f * sqrtf(cnt[i]))) * w;
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) sure += __shfl_xor_sync(0xffffffffu, sure, o);
+        float c_incl = c8, w_incl = w8;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const float a = __shfl_up_sync(0xffffffffu, c_incl, o), b = __shfl_up_sync(0xffffffffu, w_incl, o);
+          if (tid >= o) {
+            c_incl += a;
+            w_incl += b;
+          }
+        }
+        const float w_all = __shfl_sync(0xffffffffu, w_incl, 31);
+        // enough: top_k tokens with four deviations of the sample's count; what
+        // min_p keeps; or a tail of under 0.7 of what the cut leaves out of the
+        // mass that is surely there, the maximum's 1 with it, below a head of so
+        // many tokens that the sample knows what lies beneath
+        const float k_need = (float)top_k / f;
+        const float enough = p.sample_every > 1 ? k_need + 4.f * sqrtf(k_need) + 8.f : k_need;
+        const float left = has_p ? 1.f - top_p : 1.f - u;
+        const float tail = 0.7f * left * (1.f + sure);
+        int b = kCoarse;
+        float c = c_incl - c8, w = w_incl - w8;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {  // the bins up to this one are enough
+          c += cnt[i];
+          w += wgt[i];
+          const int past = tid * 8 + i + 1;
+          const bool ok = m_only ? (float)past > (sc.max - x_min) * per
+                                 : (want_k ? c >= enough : w_all - w <= tail && c * f >= kBinnedHead);
+          if (ok && b == kCoarse) b = past;
+        }
+        b = __reduce_min_sync(0xffffffffu, b);
+        if (tid == 0) s.found[0] = b;
+      }
+      __syncthreads();
+      const int b = s.found[0];
+      set_cut(sc, m_only ? x_min : (b < kCoarse - 8 ? sc.max - (float)b / per : sc.floor));
+    } else if (round == 2) {
+      set_cut(sc, sc.floor);
+    }
+    direct = direct && round == 0;
+    if (round == 0 && !direct && !need_all) continue;  // nothing to do before the bins
+    bool complete = sc.cut <= sc.floor;  // the head is every token with any mass
     // ---- 2. the mass of all, the head's tokens or bins ----
-    if (!direct) clear_bins(s);
+    const bool binned = round > 0;
+    if (binned) clear_bins(s);
     if (tid == 0) s.n_list = 0;
     __syncthreads();
-    const bool all = need_all && first_round;
     auto take = [&](u64 e, bool have) {
       if (direct) {
         append_warp(s, e, have);
@@ -967,19 +1081,23 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         add_to_bin(s, bin_of(x, sc), weigh(x, sc, s.table, s.table_f));
       }
     };
-    if (all) {
+    const float cut = direct || binned ? sc.cut : INFINITY;
+    if (need_all && round == 0) {
       u64 sum = 0;
-      sweep_head(s, row, lo_i, hi_i, sc.cut, sc.zero, [&](float x) { sum += weigh(x, sc, s.table, s.table_f); },
-                 take);
+      sweep_head(s, row, lo_i, hi_i, again, cut, sc.zero,
+                 [&](float x) { sum += weigh(x, sc, s.table, s.table_f); }, take);
       sum = block_sum(sum, s.red);
       if (tid == 0) s0.part[c_rank] = sum;
     } else {
-      sweep_head(s, row, lo_i, hi_i, sc.cut, INFINITY, [](float) {}, take);
+      sweep_head(s, row, lo_i, hi_i, again, cut, INFINITY, [](float) {}, take);
       __syncthreads();
     }
-    if (tid == 0) s0.n_lists[c_rank] = s.n_list;
+    if (tid == 0) {
+      s0.n_lists[c_rank] = s.n_list;
+      s0.cut[c_rank] = sc.cut;
+    }
     cluster.sync();
-    if (!direct) {
+    if (binned) {
       // each CTA adds up a share of the bins, for the first one
       const int per = kBins / c_size;
       for (int i = c_rank * per + tid; i < (c_rank + 1) * per; i += kThreads) {
@@ -999,48 +1117,54 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     }
     auto c_before = [&](int b) { return b ? s.tot_count[b - 1] : 0u; };
     auto m_before = [&](int b) { return b ? s.tot_mass[b - 1] : 0ull; };
-    // the tokens of every CTA's list in the first one's; false if they do not fit
-    auto merge_lists = [&](int* n_out) {
-      int n = 0;
-      bool fits = true;
-      for (int c = 0; c < c_size; ++c) {
-        n += s.n_lists[c];
-        fits = fits && n <= kList;
-      }
-      if (fits)
-        for (int i = s.n_lists[0] + tid; i < n; i += kThreads) {
-          int c = 1, j = i - s.n_lists[0];
-          while (j >= s.n_lists[c]) j -= s.n_lists[c++];
-          s.list[i] = cluster.map_shared_rank(&s, c)->list[j];
-        }
-      __syncthreads();
-      *n_out = n;
-      return fits;
+    // entry i of the CTAs' lists, one after the other
+    auto entry = [&](int i) {
+      int c = 0;
+      while (i >= s.n_lists[c]) i -= s.n_lists[c++];
+      return cluster.map_shared_rank(&s, c)->list[i];
     };
-    const bool has_m = want_m && x_min >= sc.cut;
     Decision d;
     d.done = kTooShort;
     d.kb = d.mb = -1;
     d.pb1 = d.ub1 = 0;
     d.pb2 = d.ub2 = -1;
+    bool has_m = want_m && x_min >= sc.cut;
     if (c_rank == 0) {
-      if (all)
+      if (need_all && round == 0)
         for (int c = 0; c < c_size; ++c) total += s.part[c];
-      if (direct) {
-        int n;
-        if (!merge_lists(&n) || n < 1) {
-          d.done = kTooMany;
-        } else {
-          // all of a complete head may be fewer than top_k
-          const uint32_t k = want_k && !(complete && n < top_k) ? (uint32_t)top_k : 0u;
-          kept = total;
-          if (!need_all && !k) {  // the head's mass
-            sort_list(s, n, sc.max, sc.bin_scale);
-            sum_list(s, n, sc);
-            kept = s.mass[n - 1];
-            __syncthreads();
+      if (!binned) {
+        int m = 0;
+        float least = sc.cut;
+        bool fits = direct;
+        for (int c = 0; c < c_size; ++c) {
+          m += s.n_lists[c];
+          fits = fits && s.n_lists[c] <= kList;
+          least = fmaxf(least, s.cut[c]);  // above the largest cut every CTA has all its tokens
+        }
+        if (fits) {
+          if (tid == 0) s.n_list = 0;
+          __syncthreads();
+          for (int i = tid; i - (tid & 31) < m; i += kThreads) {
+            const u64 e = i < m ? entry(i) : 0ull;
+            const bool in = i < m && entry_x(e) >= least;
+            const unsigned mask = __ballot_sync(0xffffffffu, in);
+            int at = 0;
+            if ((tid & 31) == 0 && mask) at = atomicAdd(&s.n_list, __popc(mask));
+            at = __shfl_sync(0xffffffffu, at, 0) + __popc(mask & ((1u << (tid & 31)) - 1u));
+            if (in && at < kList) s.tot_mass[at] = e;
           }
-          if (finish(s, n, sc, false, 0, k, top_p, has_m, u, &kept, &token)) d.done = kDone;
+          __syncthreads();
+          const int n = s.n_list;
+          if (n >= 1 && n <= kList) {
+            set_cut(sc, least);
+            complete = sc.cut <= sc.floor;
+            has_m = want_m && x_min >= sc.cut;
+            sort_list(s, s.tot_mass, n, sc.max, sc.bin_scale);
+            // all of a complete head may be fewer than top_k
+            const uint32_t k = want_k && !(complete && n < top_k) ? (uint32_t)top_k : 0u;
+            kept = need_all ? total : kAll;
+            if (finish(s, n, sc, false, 0, k, top_p, has_m, u, &kept, &token)) d.done = kDone;
+          }
         }
       } else {
         accumulate_bins(s.tot_count, s.tot_mass, s.red, s.red_c);
@@ -1119,11 +1243,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     }
     cluster.sync();
     d = s0.d;
-    if (d.done == kTooMany || d.done == kTooShort) {
-      // once more with bins; where a cut lies past the head, with all tokens that have mass
-      direct = false;
-      first_round = false;
-      if (d.done == kTooShort) set_cut(sc, sc.floor);
+    if (d.done == kTooShort) {
       cluster.sync();  // the decision is read before it is written again
       continue;
     }
@@ -1134,14 +1254,17 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     // ---- 3. the tokens of the cuts' bins ----
     if (tid == 0) s.n_list = 0;
     __syncthreads();
-    sweep_head(s, row, lo_i, hi_i, sc.cut, INFINITY, [](float) {},
+    sweep_head(s, row, lo_i, hi_i, again, sc.cut, INFINITY, [](float) {},
                [&](u64 e, bool have) { append_warp(s, e, have && d.wanted(bin_of(entry_x(e), sc))); });
     __syncthreads();
     if (tid == 0) s0.n_lists[c_rank] = s.n_list;
     cluster.sync();
     if (c_rank == 0) {
-      int n;
-      merge_lists(&n);  // counted above: they fit
+      int n = 0;  // at most kList, as counted above
+      for (int c = 0; c < c_size; ++c) n += s.n_lists[c];
+      for (int i = s.n_lists[0] + tid; i < n; i += kThreads) s.list[i] = entry(i);
+      __syncthreads();
+      sort_list(s, n);
       kept = need_all ? total : s.tot_mass[kBins - 1];
       if (n > 0) finish(s, n, sc, true, d.mb, d.kb >= 0 ? (uint32_t)top_k : 0u, top_p, has_m, u, &kept, &token);
     }
@@ -1159,13 +1282,23 @@ template <typename T>
 cudaError_t launch_sample(SampleParams& p, cudaStream_t st) {
   int sm = 0;
   if (device_sm_count(&sm) != STV_OK) return cudaErrorUnknown;
-  // CTAs per row: enough to give every SM two, of 2,048 tokens at least
-  int c = 1;
-  while (c < kMaxCluster && (int64_t)p.n_rows * c * 2 <= 2 * sm && p.vocab / (2 * c) >= 2048) c *= 2;
   constexpr int VE = 16 / sizeof(T);
+  constexpr int kMost = 8;  // CTAs of a cluster
+  // CTAs per row: enough to give every SM two, of 2,048 tokens at least; and as
+  // many as keep the rows at work at a time within L2, which they are read
+  // again from
+  const int64_t row_bytes = (int64_t)p.vocab * sizeof(T);
+  int c = 1;
+  while (c < kMost && p.vocab / (2 * c) >= 2048 &&
+         ((int64_t)p.n_rows * c * 2 <= 2 * sm || std::min<int64_t>(p.n_rows, 2 * sm / c) * row_bytes > kL2Bytes))
+    c *= 2;
   p.stretch = ((p.vocab + c - 1) / c + VE - 1) / VE * VE;
   p.sample_every = std::max(1, p.vocab / 4096);
-  const size_t smem = sizeof(Smem);
+  // one CTA per SM anyway: the stretches stay in shared memory
+  const size_t stretch_rows = (p.stretch / VE + kThreads - 1) / kThreads;
+  p.resident = (int64_t)p.n_rows * c <= sm && sizeof(Smem) + stretch_rows * kThreads * 16 <= 226 * 1024;
+  const size_t slot_rows = std::max<size_t>(p.resident ? stretch_rows : 0, kStages);
+  const size_t smem = sizeof(Smem) + slot_rows * kThreads * 16;
   cudaError_t e = cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e == cudaSuccess) {
     cudaLaunchConfig_t cfg = {};
