@@ -8,8 +8,7 @@
 //   1. One pass over the stretch finds the maximum (a NaN shows in it) of each
 //      of some thousand groups of tokens, and from the largest of those a
 //      value that about as many tokens exceed as the cuts should need.
-//   2. A second pass (from shared memory where the stretch fits, else from L2)
-//      gathers the tokens above it, and adds up the mass of all (unless top-k
+//   2. A second pass (from L2) gathers the tokens above it, and adds up the mass of all (unless top-k
 //      or min-p alone make that unneeded).
 // The first CTA merges the tokens above the largest of the CTAs' values, sorts
 // them, and makes the cuts exactly.  Where a cut lies further down (a flat
@@ -64,7 +63,6 @@ struct SampleParams {
   int n_rows, vocab, rows_per_param;
   int stretch;       // tokens per CTA of a cluster
   int sample_every;  // 1: the sample is everything
-  int resident;      // the stretches stay in shared memory
   const float* temperature;
   const int32_t* top_k;
   const float* top_p;
@@ -110,6 +108,7 @@ struct alignas(16) Smem {
   u64 list[kList];      // (~key << 32) | index
   uint32_t tot_count[kBins];
   uint32_t count[kBins];  // this CTA's bins; first CTA later: a bin's first place in the list
+  uint4 ring[kStages][kThreads];  // vectors on their way in, a thread's own slots
   u64 queue[kThreads / 32][64];   // a warp's tokens of the head, taken 32 at a time
   alignas(16) uint32_t coarse[kCoarse];
   uint32_t table[64];
@@ -126,16 +125,11 @@ struct alignas(16) Smem {
   int x_index[kMaxCluster];   // the maximum's first index in their stretch
   float cut[kMaxCluster];     // the value above which they gathered
   float max[kMaxCluster];     // (every CTA's) the maxima of the stretches
+  Scale sc;       // of this CTA: its cut, until the bins have one
   int found[2];
   int n_list;
   Decision d;
 };
-
-// Behind it: the slots that vectors come in through, a thread's own in each
-// row of kThreads; kStages rows, or the CTA's whole stretch (resident).
-__device__ __forceinline__ uint4* slots(Smem& s) {
-  return reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(&s) + sizeof(Smem));
-}
 
 template <typename T> __device__ __forceinline__ float to_f(T x);
 template <> __device__ __forceinline__ float to_f(float x) { return x; }
@@ -260,19 +254,14 @@ __device__ __forceinline__ void copy_async(uint4* dst, const uint4* src) {
                : "memory");
 }
 
-// How a CTA reads its stretch: through the ring, or held in shared memory from
-// the first pass on.
-enum Held { kStream, kLoad, kHeld };
-
 // Sweeps the tokens [lo, hi) of a row by whole warps: many(vector, its first
-// index, whether this lane has one) for the 16-byte vectors, one(value, index,
-// whether) for the ends that do not fill a vector (at most VE - 1 each, by the
-// first warp).  Vectors come in through the thread's own slots, without taking
-// registers or barriers: kStages - 1 ahead (kStream), or all at once into their
-// places (kLoad), where they are found later (kHeld, the same tokens).
+// index, whether this lane has one, where it lies in shared memory) for the
+// 16-byte vectors, one(value, index, whether) for the ends that do not fill a
+// vector (at most VE - 1 each, by the first warp).  Vectors come in through the
+// thread's own slots of the ring, kStages - 1 ahead, without taking registers
+// or barriers.
 template <typename T, typename Many, typename One>
-__device__ __forceinline__ void sweep_vectors(Smem& s, const T* row, int lo, int hi, Held held, Many&& many,
-                                              One&& one) {
+__device__ __forceinline__ void sweep_vectors(Smem& s, const T* row, int lo, int hi, Many&& many, One&& one) {
   constexpr int VE = 16 / sizeof(T);
   const int lane = threadIdx.x & 31;
   const T* p = row + lo;
@@ -280,38 +269,26 @@ __device__ __forceinline__ void sweep_vectors(Smem& s, const T* row, int lo, int
   const int head = min(n, (int)(((16 - ((uintptr_t)p & 15)) & 15) / sizeof(T)));
   const int n_vec = (n - head) / VE;
   const uint4* v = reinterpret_cast<const uint4*>(p + head);
-  uint4* ring = slots(s) + threadIdx.x;
+  uint4* ring = &s.ring[0][threadIdx.x];
   int i = threadIdx.x;
-  if (held == kLoad) {
-    for (int j = i, at = 0; j < n_vec; j += kThreads, at += kThreads) copy_async(ring + at, v + j);
-    asm volatile("cp.async.commit_group;" ::: "memory");
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
-  } else if (held == kStream) {
 #pragma unroll
-    for (int a = 0; a < kStages - 1; ++a) {
-      if (i + a * kThreads < n_vec) copy_async(ring + a * kThreads, v + i + a * kThreads);
-      asm volatile("cp.async.commit_group;" ::: "memory");
-    }
+  for (int a = 0; a < kStages - 1; ++a) {
+    if (i + a * kThreads < n_vec) copy_async(ring + a * kThreads, v + i + a * kThreads);
+    asm volatile("cp.async.commit_group;" ::: "memory");
   }
   int at = 0, put = (kStages - 1) * kThreads;
 #pragma unroll 1
   for (; i - lane < n_vec; i += kThreads) {
-    const bool in = i < n_vec;
-    if (held == kStream) asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
-    const uint4 now = in || held == kStream ? ring[at] : make_uint4(0, 0, 0, 0);
-    if (held == kStream) {
-      // the slot of the vector before, which has been used
-      const int next = i + (kStages - 1) * kThreads;
-      if (next < n_vec) copy_async(ring + put, v + next);
-      asm volatile("cp.async.commit_group;" ::: "memory");
-      put = at;
-      at = at == (kStages - 1) * kThreads ? 0 : at + kThreads;
-    } else {
-      at += kThreads;
-    }
-    many(now, lo + head + i * VE, in);
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+    // into the slot of the vector before, which has been used
+    const int next = i + (kStages - 1) * kThreads;
+    if (next < n_vec) copy_async(ring + put, v + next);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    many(ring[at], lo + head + i * VE, i < n_vec, ring + at);
+    put = at;
+    at = at == (kStages - 1) * kThreads ? 0 : at + kThreads;
   }
-  if (held == kStream) asm volatile("cp.async.wait_group 0;" ::: "memory");
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
   const int rest = n - head - n_vec * VE;
   if ((int)threadIdx.x < 32) {
     const bool in = lane < head + rest;
@@ -324,8 +301,8 @@ __device__ __forceinline__ void sweep_vectors(Smem& s, const T* row, int lo, int
 template <typename T, typename F>
 __device__ __forceinline__ void sweep(Smem& s, const T* row, int lo, int hi, F&& f) {
   sweep_vectors(
-      s, row, lo, hi, kStream,
-      [&](const uint4& q, int i, bool in) {
+      s, row, lo, hi,
+      [&](const uint4& q, int i, bool in, const uint4*) {
         const T* e = reinterpret_cast<const T*>(&q);
         if (in) {
 #pragma unroll
@@ -335,58 +312,6 @@ __device__ __forceinline__ void sweep(Smem& s, const T* row, int lo, int hi, F&&
       [&](float x, int i, bool in) {
         if (in) f(x, i);
       });
-}
-
-// Calls each(x) for every token with x >= least (and some others) and
-// f(entry, have) for the ones with x >= cut, by whole warps: a warp collects such tokens in its queue and hands them over
-// 32 at a time, one per lane (have: whether the lane has one), so that what f
-// waits for is paid once for 32 of them.
-template <typename T, typename Each, typename F>
-__device__ __forceinline__ void sweep_head(Smem& s, const T* row, int lo, int hi, Held held, float cut, float least,
-                                           Each&& each, F&& f) {
-  const int lane = threadIdx.x & 31;
-  u64* queue = s.queue[threadIdx.x >> 5];
-  int waiting = 0;  // the same in every lane
-  auto put = [&](float x, int i, bool in) {
-    const unsigned m = __ballot_sync(0xffffffffu, in);
-    if (m) {
-      if (in) queue[waiting + __popc(m & ((1u << lane) - 1u))] = entry_of(x, i);
-      waiting += __popc(m);
-      if (waiting >= 32) {
-        __syncwarp();
-        f(queue[lane], true);
-        waiting -= 32;
-        const u64 e = queue[32 + lane];
-        __syncwarp();
-        if (lane < waiting) queue[lane] = e;
-        __syncwarp();
-      }
-    }
-  };
-  sweep_vectors(
-      s, row, lo, hi, held,
-      [&](const uint4& q, int i, bool in) {
-        constexpr int VE = 16 / sizeof(T);
-        const T* e = reinterpret_cast<const T*>(&q);
-        float m = -INFINITY;
-#pragma unroll
-        for (int k = 0; k < VE; ++k) m = fmaxf(m, to_f(e[k]));
-        if (in && m >= least) {
-#pragma unroll
-          for (int k = 0; k < VE; ++k) each(to_f(e[k]));
-        }
-        if (__any_sync(0xffffffffu, in && m >= cut)) {
-#pragma unroll
-          for (int k = 0; k < VE; ++k) put(to_f(e[k]), i + k, in && to_f(e[k]) >= cut);
-        }
-      },
-      [&](float x, int i, bool in) {
-        if (in) each(x);
-        put(x, i, in && x >= cut);
-      });
-  __syncwarp();
-  if (waiting) f(lane < waiting ? queue[lane] : 0ull, lane < waiting);
-  __syncwarp();
 }
 
 // Calls f(x) for one group of 32 vectors in `every` (and for no tokens outside
@@ -515,7 +440,7 @@ __device__ __forceinline__ int first_bin(const V* running, V t) {
 // place is the number of entries in the bins before its own (of 2,048 from
 // `top` down, `scale` to a unit of x) and of smaller ones in it; few share a
 // bin, unless they are equal.
-__device__ __forceinline__ void sort_list(Smem& s, const u64* src, int n, float top, float scale) {
+__device__ __noinline__ void sort_list(Smem& s, const u64* src, int n, float top, float scale) {
   constexpr int kPer = kList / kThreads;
   if (n <= kThreads / 2) {
     const int i = (int)threadIdx.x >> 1;
@@ -616,8 +541,9 @@ __device__ __forceinline__ void sum_list(Smem& s, int n, const Scale& sc) {
 // is cut (kAll: that of the tokens); on return the kept mass, and the token.
 // False when a cut lies past the tokens.
 constexpr u64 kAll = ~0ull;
-__device__ __forceinline__ bool finish(Smem& s, int n, const Scale& sc, bool binned, int mb, uint32_t top_k,
-                                       float top_p, bool has_m, float u, u64* kept, u64* token) {
+__device__ __noinline__ bool finish(Smem& s, int n, bool binned, int mb, uint32_t top_k, float top_p, bool has_m,
+                                    float u, u64* kept, u64* token) {
+  const Scale sc = s.sc;
   constexpr int kPer = kList / kThreads;
   constexpr u64 kNone = ~0ull;
   // a thread's tokens: adjacent ones
@@ -752,6 +678,89 @@ __device__ __forceinline__ void clear_bins(Smem& s) {
   }
 }
 
+// What sweep_row does with the tokens x >= cut.
+enum Take { kAppend, kToBins, kAppendWanted, kFirstIndex };
+
+// Sweeps the tokens [lo, hi) of a row: the mass of all of them, where asked
+// for, and the tokens x >= cut to this CTA's list (all, or those of the bins
+// of s.d), to its bins, or only their least index.  Returns the thread's share
+// of the mass, or its least index.
+//
+// A warp collects the tokens x >= cut in its queue and handles them 32 at a
+// time, one per lane, so that atomics and dependent arithmetic are waited for
+// once for 32 of them.  One copy serves the kernel: its phases run each once,
+// and mostly wait for their instructions.
+template <typename T>
+__device__ __noinline__ u64 sweep_row(Smem& s, const T* row, int lo, int hi, float cut, bool all, Take take) {
+  const Scale sc = s.sc;
+  const int lane = threadIdx.x & 31;
+  u64* queue = s.queue[threadIdx.x >> 5];
+  const Decision d = s.d;
+  u64 sum = take == kFirstIndex ? ~0ull : 0ull;
+  int waiting = 0;  // the same in every lane
+  auto handle = [&](u64 e, bool have) {
+    if (take == kAppend || take == kAppendWanted) {
+      if (take == kAppendWanted) have = have && d.wanted(bin_of(entry_x(e), sc));
+      append_warp(s, e, have);
+    } else if (have) {
+      if (take == kToBins) {
+        const float x = entry_x(e);
+        add_to_bin(s, bin_of(x, sc), weigh(x, sc, s.table, s.table_f));
+      } else {
+        sum = min(sum, (u64)(uint32_t)e);
+      }
+    }
+  };
+  // (once more, after the last token, for those that still wait)
+  auto put = [&](float x, int i, bool in, bool last) {
+    const unsigned m = __ballot_sync(0xffffffffu, in);
+    if (m || last) {
+      if (in) queue[waiting + __popc(m & ((1u << lane) - 1u))] = entry_of(x, i);
+      waiting += __popc(m);
+      if (waiting >= 32 || last) {
+        __syncwarp();
+        handle(queue[lane], lane < waiting);
+        const u64 e = queue[32 + lane];
+        __syncwarp();
+        queue[lane] = e;
+        waiting -= 32;
+        __syncwarp();
+      }
+    }
+  };
+  constexpr int VE = 16 / sizeof(T);
+  float end_x = -INFINITY;
+  int end_i = 0;
+  sweep_vectors(
+      s, row, lo, hi,
+      [&](const uint4& q, int i, bool in, const uint4* slot) {
+        const T* e = reinterpret_cast<const T*>(&q);
+        float m = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < VE; ++k) m = fmaxf(m, to_f(e[k]));
+        if (all && in && m >= sc.zero) {
+#pragma unroll
+          for (int k = 0; k < VE; ++k) sum += weigh(to_f(e[k]), sc, s.table, s.table_f);
+        }
+        if (__any_sync(0xffffffffu, in && m >= cut)) {
+#pragma unroll 1
+          for (int k = 0; k < VE; ++k) {
+            const float x = to_f(reinterpret_cast<const T*>(slot)[k]);
+            put(x, i + k, in && x >= cut, false);
+          }
+        }
+      },
+      [&](float x, int i, bool in) {
+        if (all && in) sum += weigh(x, sc, s.table, s.table_f);
+        end_x = x;
+        end_i = i;
+      });
+  // the ends (the first warp's), and what waits: at most 31 and 32
+#pragma unroll 1
+  for (int k = 0; k < 2; ++k) put(end_x, end_i, k == 0 && end_x >= cut && end_x > -INFINITY, k == 1);
+  return sum;
+}
+
 // The cut of the order inside bin `b` of the head (any number of tokens): the
 // first token whose rank (1, 2, ...) reaches `rank`, or, where rank is 0, whose
 // running mass reaches `target`.  *mass: the running mass with it; *entry: the
@@ -872,7 +881,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   const float min_p = p.min_p ? __ldg(p.min_p + pi) : 0.f;
   const float u = __ldg(p.u + r);
 
-  const Held load = p.resident ? kLoad : kStream, again = p.resident ? kHeld : kStream;
   const bool want_k = top_k > 0 && top_k < p.vocab, has_p = top_p < 1.f, want_m = min_p > 0.f;
   // the tokens that this CTA should gather: with the others', four deviations
   // more than top_k
@@ -893,8 +901,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   {
     float ends = -INFINITY;
     sweep_vectors(
-        s, row, lo_i, hi_i, load,
-        [&](const uint4& q, int, bool in) {
+        s, row, lo_i, hi_i,
+        [&](const uint4& q, int, bool in, const uint4*) {
           const T* e = reinterpret_cast<const T*>(&q);
           if (in) {
 #pragma unroll
@@ -960,9 +968,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   if (bad || temp == 0.f) {
     // the maximum's first index
     if (!bad) {
-      int first = p.vocab;
-      sweep_head(s, row, lo_i, hi_i, again, row_max, INFINITY, [](float) {},
-                 [&](u64 e, bool have) { first = have ? min(first, (int)(uint32_t)e) : first; });
+      int first = (int)min((u64)p.vocab, sweep_row(s, row, lo_i, hi_i, row_max, false, kFirstIndex));
       first = (int)block_min((u64)first, s.red);
       if (tid == 0) s0.x_index[c_rank] = first;
     }
@@ -1071,26 +1077,20 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     // ---- 2. the mass of all, the head's tokens or bins ----
     const bool binned = round > 0;
     if (binned) clear_bins(s);
-    if (tid == 0) s.n_list = 0;
+    if (tid == 0) {
+      s.n_list = 0;
+      s.sc = sc;
+    }
     __syncthreads();
-    auto take = [&](u64 e, bool have) {
-      if (direct) {
-        append_warp(s, e, have);
-      } else if (have) {
-        const float x = entry_x(e);
-        add_to_bin(s, bin_of(x, sc), weigh(x, sc, s.table, s.table_f));
+    {
+      const bool all = need_all && round == 0;
+      u64 sum = sweep_row(s, row, lo_i, hi_i, direct || binned ? sc.cut : INFINITY, all, binned ? kToBins : kAppend);
+      if (all) {
+        sum = block_sum(sum, s.red);
+        if (tid == 0) s0.part[c_rank] = sum;
+      } else {
+        __syncthreads();
       }
-    };
-    const float cut = direct || binned ? sc.cut : INFINITY;
-    if (need_all && round == 0) {
-      u64 sum = 0;
-      sweep_head(s, row, lo_i, hi_i, again, cut, sc.zero,
-                 [&](float x) { sum += weigh(x, sc, s.table, s.table_f); }, take);
-      sum = block_sum(sum, s.red);
-      if (tid == 0) s0.part[c_rank] = sum;
-    } else {
-      sweep_head(s, row, lo_i, hi_i, again, cut, INFINITY, [](float) {}, take);
-      __syncthreads();
     }
     if (tid == 0) {
       s0.n_lists[c_rank] = s.n_list;
@@ -1157,13 +1157,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
           const int n = s.n_list;
           if (n >= 1 && n <= kList) {
             set_cut(sc, least);
+            if (tid == 0) s.sc = sc;
             complete = sc.cut <= sc.floor;
             has_m = want_m && x_min >= sc.cut;
             sort_list(s, s.tot_mass, n, sc.max, sc.bin_scale);
             // all of a complete head may be fewer than top_k
             const uint32_t k = want_k && !(complete && n < top_k) ? (uint32_t)top_k : 0u;
             kept = need_all ? total : kAll;
-            if (finish(s, n, sc, false, 0, k, top_p, has_m, u, &kept, &token)) d.done = kDone;
+            if (finish(s, n, false, 0, k, top_p, has_m, u, &kept, &token)) d.done = kDone;
           }
         }
       } else {
@@ -1252,10 +1253,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       break;
     }
     // ---- 3. the tokens of the cuts' bins ----
-    if (tid == 0) s.n_list = 0;
+    if (tid == 0) {
+      s.n_list = 0;
+      s.d = d;
+    }
     __syncthreads();
-    sweep_head(s, row, lo_i, hi_i, again, sc.cut, INFINITY, [](float) {},
-               [&](u64 e, bool have) { append_warp(s, e, have && d.wanted(bin_of(entry_x(e), sc))); });
+    sweep_row(s, row, lo_i, hi_i, sc.cut, false, kAppendWanted);
     __syncthreads();
     if (tid == 0) s0.n_lists[c_rank] = s.n_list;
     cluster.sync();
@@ -1266,7 +1269,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       __syncthreads();
       sort_list(s, n);
       kept = need_all ? total : s.tot_mass[kBins - 1];
-      if (n > 0) finish(s, n, sc, true, d.mb, d.kb >= 0 ? (uint32_t)top_k : 0u, top_p, has_m, u, &kept, &token);
+      if (n > 0) finish(s, n, true, d.mb, d.kb >= 0 ? (uint32_t)top_k : 0u, top_p, has_m, u, &kept, &token);
     }
     cluster.sync();  // no CTA ends while the first one reads its list
     break;
@@ -1294,11 +1297,7 @@ cudaError_t launch_sample(SampleParams& p, cudaStream_t st) {
     c *= 2;
   p.stretch = ((p.vocab + c - 1) / c + VE - 1) / VE * VE;
   p.sample_every = std::max(1, p.vocab / 4096);
-  // one CTA per SM anyway: the stretches stay in shared memory
-  const size_t stretch_rows = (p.stretch / VE + kThreads - 1) / kThreads;
-  p.resident = (int64_t)p.n_rows * c <= sm && sizeof(Smem) + stretch_rows * kThreads * 16 <= 226 * 1024;
-  const size_t slot_rows = std::max<size_t>(p.resident ? stretch_rows : 0, kStages);
-  const size_t smem = sizeof(Smem) + slot_rows * kThreads * 16;
+  const size_t smem = sizeof(Smem);
   cudaError_t e = cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e == cudaSuccess) {
     cudaLaunchConfig_t cfg = {};
