@@ -55,7 +55,8 @@ constexpr int kMaxVocab = 1 << 19;
 constexpr int64_t kL2Bytes = 80 << 20;  // of 126 MB, for the rows at work at a time
 constexpr int kShift = 14;       // w < 2^45: 2^19 tokens stay below 2^64
 constexpr int kMaxCluster = 16;
-constexpr int kStages = 4;       // one being read, three on their way
+constexpr int kStages = 7;       // one being read, six on their way
+constexpr int kBinnedStages = 4; // where the bins' totals take the place of the others
 
 struct SampleParams {
   const void* x;
@@ -80,6 +81,7 @@ enum { kDone, kGather, kTooShort };
 struct Decision {
   int done;
   int kb, pb1, pb2, mb, ub1, ub2;  // bins to gather; empty ranges where a cut is not made
+  float lo[2], hi[2];              // two ranges of x that hold them (the draw's; all others)
 
   __device__ bool wanted(int b) const {
     return b == kb || (b >= pb1 && b <= pb2) || b == mb || (b >= ub1 && b <= ub2);
@@ -102,13 +104,18 @@ struct Scale {
 };
 
 struct alignas(16) Smem {
-  u64 tot_mass[kBins];  // first CTA: the merged lists; or the row's bins, then of each and all before
   u64 mass[kBins];      // this CTA's bins (low and high words apart); first CTA later:
                         // running mass over the list
   u64 list[kList];      // (~key << 32) | index
-  uint32_t tot_count[kBins];
   uint32_t count[kBins];  // this CTA's bins; first CTA later: a bin's first place in the list
-  uint4 ring[kStages][kThreads];  // vectors on their way in, a thread's own slots
+  uint4 ring[kBinnedStages][kThreads];  // vectors on their way in, a thread's own slots
+  union {
+    uint4 more[kStages - kBinnedStages][kThreads];  // the ring goes on here, or
+    struct {  // first CTA: the merged lists; the row's bins, then of each and all before
+      u64 tot_mass[kBins];
+      uint32_t tot_count[kBins];
+    };
+  };
   u64 queue[kThreads / 32][64];   // a warp's tokens of the head, taken 32 at a time
   alignas(16) uint32_t coarse[kCoarse];
   uint32_t table[64];
@@ -191,6 +198,16 @@ __device__ __forceinline__ Scale make_scale(const Smem& s, float max, float min_
   return sc;
 }
 
+// w from rint(x / C) (the bits of kMagic + k) and the correction of 2^(k/64),
+// in quarters (kMagic + q).
+__device__ __forceinline__ u64 weight_of(int kb, float q, const Scale& sc, const uint32_t* table) {
+  const uint32_t m = table[kb & 63] + ((uint32_t)(__float_as_int(q) - 0x4b400000) << 2);
+  const u64 w = ((u64)m << kShift) >> (sc.top - (kb >> 6));
+  // cut to even, plus one where anything is left: no bias
+  const uint32_t lo = (uint32_t)w;
+  return (w & 0xffffffff00000000ull) | (lo | min(lo, 1u));
+}
+
 // w of a token that is not NaN (0 for -inf and whatever lies below the floor).
 __device__ __forceinline__ u64 weigh(float x, const Scale& sc, const uint32_t* table, const float* table_f) {
   const float v = x - sc.base;
@@ -199,14 +216,51 @@ __device__ __forceinline__ u64 weigh(float x, const Scale& sc, const uint32_t* t
   const float k = t - kMagic;
   const float z = fmaf(k, -sc.c_lo, fmaf(k, -sc.c_hi, v)) * sc.inv_t;
   const float p = fmaf(fmaf(z, 1.f / 6.f, 0.5f), z, 1.f);  // e^z - 1 = z p
-  const int j = kb & 63;
   // table_f = 2^28 2^(j/64), a quarter of the integer entry: |table_f z p| < 2^22
-  const float q = fmaf(table_f[j] * z, p, kMagic);
-  const uint32_t m = table[j] + ((uint32_t)(__float_as_int(q) - 0x4b400000) << 2);
-  const u64 w = ((u64)m << kShift) >> (sc.top - (kb >> 6));
-  // cut to even, plus one where anything is left: no bias
-  const uint32_t lo = (uint32_t)w;
-  return (w & 0xffffffff00000000ull) | (lo | min(lo, 1u));
+  const float q = fmaf(table_f[kb & 63] * z, p, kMagic);
+  return weight_of(kb, q, sc, table);
+}
+
+// Two tokens at once, in paired fp32 instructions: the same operations, and so
+// the same w.
+__device__ __forceinline__ u64 pack2(float a, float b) {
+  u64 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(u64 r, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(r));
+}
+__device__ __forceinline__ u64 fma2(u64 a, u64 b, u64 c) {
+  u64 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ u64 add2(u64 a, u64 b) {
+  u64 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ u64 mul2(u64 a, u64 b) {
+  u64 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ u64 weigh_two(float xa, float xb, const Scale& sc, const uint32_t* table,
+                                         const float* table_f) {
+  const u64 v = add2(pack2(xa, xb), pack2(-sc.base, -sc.base));
+  float ta, tb;
+  unpack2(fma2(v, pack2(sc.inv_c, sc.inv_c), pack2(kMagic, kMagic)), ta, tb);
+  ta = fmaxf(ta, sc.least);
+  tb = fmaxf(tb, sc.least);
+  const int ka = __float_as_int(ta), kb = __float_as_int(tb);
+  const u64 k = add2(pack2(ta, tb), pack2(-kMagic, -kMagic));
+  const u64 z = mul2(fma2(k, pack2(-sc.c_lo, -sc.c_lo), fma2(k, pack2(-sc.c_hi, -sc.c_hi), v)),
+                     pack2(sc.inv_t, sc.inv_t));
+  const u64 p = fma2(fma2(z, pack2(1.f / 6.f, 1.f / 6.f), pack2(0.5f, 0.5f)), z, pack2(1.f, 1.f));
+  float qa, qb;
+  unpack2(fma2(mul2(pack2(table_f[ka & 63], table_f[kb & 63]), z), p, pack2(kMagic, kMagic)), qa, qb);
+  return weight_of(ka, qa, sc, table) + weight_of(kb, qb, sc, table);
 }
 
 // Bin of a token of the head.
@@ -258,9 +312,9 @@ __device__ __forceinline__ void copy_async(uint4* dst, const uint4* src) {
 // index, whether this lane has one, where it lies in shared memory) for the
 // 16-byte vectors, one(value, index, whether) for the ends that do not fill a
 // vector (at most VE - 1 each, by the first warp).  Vectors come in through the
-// thread's own slots of the ring, kStages - 1 ahead, without taking registers
+// thread's own slots of the ring, kAhead - 1 ahead, without taking registers
 // or barriers.
-template <typename T, typename Many, typename One>
+template <int kAhead, typename T, typename Many, typename One>
 __device__ __forceinline__ void sweep_vectors(Smem& s, const T* row, int lo, int hi, Many&& many, One&& one) {
   constexpr int VE = 16 / sizeof(T);
   const int lane = threadIdx.x & 31;
@@ -272,21 +326,21 @@ __device__ __forceinline__ void sweep_vectors(Smem& s, const T* row, int lo, int
   uint4* ring = &s.ring[0][threadIdx.x];
   int i = threadIdx.x;
 #pragma unroll
-  for (int a = 0; a < kStages - 1; ++a) {
+  for (int a = 0; a < kAhead - 1; ++a) {
     if (i + a * kThreads < n_vec) copy_async(ring + a * kThreads, v + i + a * kThreads);
     asm volatile("cp.async.commit_group;" ::: "memory");
   }
-  int at = 0, put = (kStages - 1) * kThreads;
+  int at = 0, put = (kAhead - 1) * kThreads;
 #pragma unroll 1
   for (; i - lane < n_vec; i += kThreads) {
-    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+    asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 2) : "memory");
     // into the slot of the vector before, which has been used
-    const int next = i + (kStages - 1) * kThreads;
+    const int next = i + (kAhead - 1) * kThreads;
     if (next < n_vec) copy_async(ring + put, v + next);
     asm volatile("cp.async.commit_group;" ::: "memory");
     many(ring[at], lo + head + i * VE, i < n_vec, ring + at);
     put = at;
-    at = at == (kStages - 1) * kThreads ? 0 : at + kThreads;
+    at = at == (kAhead - 1) * kThreads ? 0 : at + kThreads;
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
   const int rest = n - head - n_vec * VE;
@@ -300,7 +354,7 @@ __device__ __forceinline__ void sweep_vectors(Smem& s, const T* row, int lo, int
 // Calls f(x, index) for the tokens [lo, hi) of a row.
 template <typename T, typename F>
 __device__ __forceinline__ void sweep(Smem& s, const T* row, int lo, int hi, F&& f) {
-  sweep_vectors(
+  sweep_vectors<kBinnedStages>(
       s, row, lo, hi,
       [&](const uint4& q, int i, bool in, const uint4*) {
         const T* e = reinterpret_cast<const T*>(&q);
@@ -690,12 +744,14 @@ enum Take { kAppend, kToBins, kAppendWanted, kFirstIndex };
 // time, one per lane, so that atomics and dependent arithmetic are waited for
 // once for 32 of them.  One copy serves the kernel: its phases run each once,
 // and mostly wait for their instructions.
-template <typename T>
+template <int kAhead, typename T>
 __device__ __noinline__ u64 sweep_row(Smem& s, const T* row, int lo, int hi, float cut, bool all, Take take) {
   const Scale sc = s.sc;
   const int lane = threadIdx.x & 31;
   u64* queue = s.queue[threadIdx.x >> 5];
   const Decision d = s.d;
+  const bool in_ranges = take == kAppendWanted;
+  auto near = [&](float x) { return (x >= d.lo[0] && x <= d.hi[0]) || (x >= d.lo[1] && x <= d.hi[1]); };
   u64 sum = take == kFirstIndex ? ~0ull : 0ull;
   int waiting = 0;  // the same in every lane
   auto handle = [&](u64 e, bool have) {
@@ -731,7 +787,7 @@ __device__ __noinline__ u64 sweep_row(Smem& s, const T* row, int lo, int hi, flo
   constexpr int VE = 16 / sizeof(T);
   float end_x = -INFINITY;
   int end_i = 0;
-  sweep_vectors(
+  sweep_vectors<kAhead>(
       s, row, lo, hi,
       [&](const uint4& q, int i, bool in, const uint4* slot) {
         const T* e = reinterpret_cast<const T*>(&q);
@@ -740,13 +796,20 @@ __device__ __noinline__ u64 sweep_row(Smem& s, const T* row, int lo, int hi, flo
         for (int k = 0; k < VE; ++k) m = fmaxf(m, to_f(e[k]));
         if (all && in && m >= sc.zero) {
 #pragma unroll
-          for (int k = 0; k < VE; ++k) sum += weigh(to_f(e[k]), sc, s.table, s.table_f);
+          for (int k = 0; k < VE; k += 2)
+            sum += weigh_two(to_f(e[k]), to_f(e[k + 1]), sc, s.table, s.table_f);
         }
-        if (__any_sync(0xffffffffu, in && m >= cut)) {
+        bool some = in && m >= cut;
+        if (in_ranges && some) {
+          some = false;
+#pragma unroll
+          for (int k = 0; k < VE; ++k) some = some || near(to_f(e[k]));
+        }
+        if (__any_sync(0xffffffffu, some)) {
 #pragma unroll 1
           for (int k = 0; k < VE; ++k) {
             const float x = to_f(reinterpret_cast<const T*>(slot)[k]);
-            put(x, i + k, in && x >= cut, false);
+            put(x, i + k, in && x >= cut && (!in_ranges || near(x)), false);
           }
         }
       },
@@ -900,7 +963,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   float cta_max;
   {
     float ends = -INFINITY;
-    sweep_vectors(
+    sweep_vectors<kStages>(
         s, row, lo_i, hi_i,
         [&](const uint4& q, int, bool in, const uint4*) {
           const T* e = reinterpret_cast<const T*>(&q);
@@ -968,7 +1031,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   if (bad || temp == 0.f) {
     // the maximum's first index
     if (!bad) {
-      int first = (int)min((u64)p.vocab, sweep_row(s, row, lo_i, hi_i, row_max, false, kFirstIndex));
+      int first = (int)min((u64)p.vocab, sweep_row<kStages>(s, row, lo_i, hi_i, row_max, false, kFirstIndex));
       first = (int)block_min((u64)first, s.red);
       if (tid == 0) s0.x_index[c_rank] = first;
     }
@@ -1084,7 +1147,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     __syncthreads();
     {
       const bool all = need_all && round == 0;
-      u64 sum = sweep_row(s, row, lo_i, hi_i, direct || binned ? sc.cut : INFINITY, all, binned ? kToBins : kAppend);
+      u64 sum = binned ? sweep_row<kBinnedStages>(s, row, lo_i, hi_i, sc.cut, false, kToBins)
+                       : sweep_row<kStages>(s, row, lo_i, hi_i, direct ? sc.cut : INFINITY, all, kAppend);
       if (all) {
         sum = block_sum(sum, s.red);
         if (tid == 0) s0.part[c_rank] = sum;
@@ -1213,6 +1277,19 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
           }
         }
         if (ok || complete) d.done = kGather;
+        {
+          // x of a bin lies within its bounds widened by the rounding of (max - x) bin_scale
+          auto high = [&](int b) { return b > 0 ? sc.max - (float)b / sc.bin_scale * 0.99999f : sc.max; };
+          auto low = [&](int b) { return fmaxf(sc.cut, sc.max - (float)(b + 1) / sc.bin_scale * 1.00001f); };
+          int b1 = kBins, b2 = -1;
+          if (d.kb >= 0) b1 = min(b1, d.kb), b2 = max(b2, d.kb);
+          if (has_p) b1 = min(b1, d.pb1), b2 = max(b2, d.pb2);
+          if (d.mb >= 0) b1 = min(b1, d.mb), b2 = max(b2, d.mb);
+          d.lo[0] = b2 >= 0 ? low(b2) : INFINITY;
+          d.hi[0] = b2 >= 0 ? high(b1) : -INFINITY;
+          d.lo[1] = low(d.ub2);
+          d.hi[1] = high(d.ub1);
+        }
         if (d.done == kGather && n > kList) {
           // ---- one cut after the other, without the other CTAs ----
           kept = need_all ? total : head;
@@ -1258,7 +1335,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       s.d = d;
     }
     __syncthreads();
-    sweep_row(s, row, lo_i, hi_i, sc.cut, false, kAppendWanted);
+    sweep_row<kBinnedStages>(s, row, lo_i, hi_i, sc.cut, false, kAppendWanted);
     __syncthreads();
     if (tid == 0) s0.n_lists[c_rank] = s.n_list;
     cluster.sync();
