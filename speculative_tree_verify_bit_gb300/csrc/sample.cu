@@ -5,19 +5,19 @@
 // then index ascending) at a given count or a given mass, so no sort of the
 // vocabulary is needed.  A cluster of CTAs shares a row, each CTA a stretch of
 // it:
-//   1. One pass over the stretch finds the maximum (a NaN shows in it) of each
-//      of some thousand groups of tokens, and from the largest of those a
-//      value that about as many tokens exceed as the cuts should need.
-//   2. A second pass (from L2) gathers the tokens above it, and adds up the mass of all (unless top-k
-//      or min-p alone make that unneeded).
-// The first CTA merges the tokens above the largest of the CTAs' values, sorts
-// them, and makes the cuts exactly.  Where a cut lies further down (a flat
-// distribution, top-p of a long tail):
-//   3. A sample of some 4,096 tokens, counted by quarter octaves of w, tells
-//      how far down; the tokens from there up are counted and their masses
-//      added in 2,048 bins; the tokens of the few bins that the cuts lie in are
-//      gathered and sorted.  (Where even that falls short: once more, with every
-//      token that has any mass.)
+//   1. One pass over the stretch finds the maximum (a NaN shows in it).
+//   2. How far down the order do the cuts lie?  With top-k, the maxima of some
+//      thousand groups of tokens tell: as many tokens at least exceed a value as
+//      groups whose maximum does.  Otherwise a sample of some 8,192 tokens,
+//      counted by quarter octaves of w, tells how much mass lies below a value.
+//   3. A second pass (from L2) adds up the mass of all (unless top-k or min-p
+//      alone make that unneeded), and takes the tokens above that value, the
+//      head: gathers them when they are few, else counts them and adds their
+//      masses in 2,048 bins; then a third pass gathers the tokens of the few
+//      bins that the cuts lie in.
+//   4. The first CTA merges and sorts the gathered tokens and makes the cuts
+//      exactly.  Where one lies past the head, the bins are filled once more,
+//      with every token that has any mass.
 // What is chosen by groups and samples is only how much is gathered.
 //
 // Masses.  w = exp((x - max) / T) as an integer of scale 2^45.  With C =
@@ -47,9 +47,8 @@ constexpr int kThreads = 512;
 constexpr int kBins = 2048;
 constexpr int kBinsPer = kBins / kThreads;
 constexpr int kList = 2048;      // tokens gathered around the cuts
-constexpr int kDirect = 1700;    // more tokens than this are not gathered at once
-constexpr float kLeastHead = 384.f;  // tokens gathered where top-k asks for no number
-constexpr float kBinnedHead = 512.f;
+constexpr int kDirect = 1600;    // more tokens than this are not gathered at once
+constexpr float kLeastHead = 512.f;  // tokens, so that the sample knows what lies beneath
 constexpr int kCoarse = 256;     // quarter octaves of the sample
 constexpr int kMaxVocab = 1 << 19;
 constexpr int64_t kL2Bytes = 80 << 20;  // of 126 MB, for the rows at work at a time
@@ -118,6 +117,7 @@ struct alignas(16) Smem {
   };
   u64 queue[kThreads / 32][64];   // a warp's tokens of the head, taken 32 at a time
   alignas(16) uint32_t coarse[kCoarse];
+  uint32_t coarse_all[kCoarse];
   uint32_t table[64];
   float table_f[64];
   u64 red[kThreads / 32];
@@ -742,16 +742,22 @@ enum Take { kAppend, kToBins, kAppendWanted, kFirstIndex };
 //
 // A warp collects the tokens x >= cut in its queue and handles them 32 at a
 // time, one per lane, so that atomics and dependent arithmetic are waited for
-// once for 32 of them.  One copy serves the kernel: its phases run each once,
-// and mostly wait for their instructions.
-template <int kAhead, typename T>
-__device__ __noinline__ u64 sweep_row(Smem& s, const T* row, int lo, int hi, float cut, bool all, Take take) {
+// once for 32 of them.
+template <int kAhead, Take take, bool all, typename T>
+__device__ __noinline__ u64 sweep_row(Smem& s, const T* row, int lo, int hi, float cut) {
   const Scale sc = s.sc;
   const int lane = threadIdx.x & 31;
   u64* queue = s.queue[threadIdx.x >> 5];
-  const Decision d = s.d;
-  const bool in_ranges = take == kAppendWanted;
-  auto near = [&](float x) { return (x >= d.lo[0] && x <= d.hi[0]) || (x >= d.lo[1] && x <= d.hi[1]); };
+  constexpr bool in_ranges = take == kAppendWanted;
+  const Decision& d = s.d;
+  float lo0 = 0.f, hi0 = 0.f, lo1 = 0.f, hi1 = 0.f;
+  if (in_ranges) {
+    lo0 = d.lo[0];
+    hi0 = d.hi[0];
+    lo1 = d.lo[1];
+    hi1 = d.hi[1];
+  }
+  auto near = [&](float x) { return (x >= lo0 && x <= hi0) || (x >= lo1 && x <= hi1); };
   u64 sum = take == kFirstIndex ? ~0ull : 0ull;
   int waiting = 0;  // the same in every lane
   auto handle = [&](u64 e, bool have) {
@@ -945,15 +951,19 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   const float u = __ldg(p.u + r);
 
   const bool want_k = top_k > 0 && top_k < p.vocab, has_p = top_p < 1.f, want_m = min_p > 0.f;
-  // the tokens that this CTA should gather: with the others', four deviations
-  // more than top_k
+  const bool m_only = want_m && !want_k && !has_p;  // the head is what min_p keeps
+  const bool need_all = !want_k && !m_only;         // the mass of every token
+  // top-k: the tokens that this CTA should gather, with the others four
+  // deviations more than top_k; unless they are too many, or too many for
+  // groups' maxima to tell (share * (1 + 0.7 share / kGroups) tokens lie above
+  // the maximum that `share` groups reach)
   constexpr int VE = 16 / sizeof(T);
   constexpr float kGroups = kThreads * VE;
-  float share = want_k ? (float)top_k / (float)c_size : kLeastHead / (float)c_size;
-  if (want_k && c_size > 1) share = fminf((float)top_k, share + 4.f * sqrtf(share) + 8.f);
-  // as many of kGroups groups' maxima lie that high as hold one of them or more
-  bool direct = share * (float)c_size * (share > 0.3f * kGroups ? 1.5f : 1.2f) <= (float)kDirect &&
-                share < 0.6f * kGroups;
+  float share = (float)top_k / (float)c_size;
+  if (c_size > 1) share = fminf((float)top_k, share + 4.f * sqrtf(share) + 8.f);
+  const bool by_groups = want_k && share * (float)c_size * (1.f + 0.7f * share / kGroups) <= (float)kDirect &&
+                         share < 0.6f * kGroups;
+  const bool by_sample = !by_groups && !m_only;
 
   // ---- 1. the groups' maxima, and whether anything is wrong ----
   if (tid == kThreads - 1) prepare_scale(s, temp, min_p);
@@ -989,14 +999,21 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     cluster.barrier_wait(std::move(started));
     if (tid < c_size) cluster.map_shared_rank(&s, tid)->max[c_rank] = cta_max;  // to every CTA
   }
+  const float per = 4.f / 64.f * s.inv_c;  // quarter octaves of w to a unit of x
+  if (by_sample) {
+    sweep_sample(row, lo_i, hi_i, p.sample_every, [&](float x) {
+      const float y = (cta_max - x) * per;
+      if (y >= 0.f && y < (float)kCoarse) atomicAdd(s.coarse + (int)y, 1u);
+    });
+    if (tid < kCoarse) s.coarse_all[tid] = 0;
+  }
   cg::cluster_group::arrival_token arrived = cluster.barrier_arrive();
   // the value that about `share` of this CTA's tokens exceed: the groups'
   // maxima counted by eighths of an octave
-  const float per8 = 8.f / 64.f * s.inv_c;  // to a unit of x
-  if (direct) {
+  if (by_groups) {
 #pragma unroll
     for (int k = 0; k < VE; ++k) {
-      const float y = (cta_max - top[k]) * per8;
+      const float y = (cta_max - top[k]) * (2.f * per);
       if (y >= 0.f && y < (float)kCoarse) atomicAdd(s.coarse + (int)y, 1u);
     }
     __syncthreads();
@@ -1031,7 +1048,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   if (bad || temp == 0.f) {
     // the maximum's first index
     if (!bad) {
-      int first = (int)min((u64)p.vocab, sweep_row<kStages>(s, row, lo_i, hi_i, row_max, false, kFirstIndex));
+      int first = (int)min((u64)p.vocab, sweep_row<kStages, kFirstIndex, false>(s, row, lo_i, hi_i, row_max));
       first = (int)block_min((u64)first, s.red);
       if (tid == 0) s0.x_index[c_rank] = first;
     }
@@ -1050,95 +1067,92 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   }
   Scale sc = make_scale(s, row_max, min_p);
   const float x_min = sc.x_min;
-  const bool m_only = want_m && !want_k && !has_p;  // the head is what min_p keeps
-  const bool need_all = !want_k && !m_only;         // the mass of every token
-  if (direct) {
+  // ---- how far down the cuts lie ----
+  bool direct = true;
+  if (by_groups) {
     const int b = s.found[0];
-    set_cut(sc, m_only ? x_min : (b < kCoarse ? cta_max - (float)b / per8 : sc.floor));
+    set_cut(sc, b < kCoarse ? cta_max - (float)b / (2.f * per) : sc.floor);
+  } else if (m_only) {
+    set_cut(sc, x_min);
+  } else {
+    // the CTAs' samples, counted from their own maxima, as the row's
+    for (int i = tid; i < c_size * kCoarse; i += kThreads) {
+      const int c = i / kCoarse, k = i % kCoarse;
+      const uint32_t n = cluster.map_shared_rank(&s, c)->coarse[k];
+      const float g = (float)k + (sc.max - s.max[c]) * per;
+      if (n && g < (float)(kCoarse - 8)) atomicAdd(s.coarse_all + (int)g, n);
+    }
+    __syncthreads();
+    const float f = (float)p.sample_every;
+    if (tid < 32) {  // a warp: lane l holds eight bins
+      float cnt[8], wgt[8], c8 = 0.f, w8 = 0.f, sure = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        cnt[i] = (float)s.coarse_all[tid * 8 + i];
+        const float w = exp2f(-0.25f * (float)(tid * 8 + i));
+        wgt[i] = f * cnt[i] * w;
+        c8 += cnt[i];
+        w8 += wgt[i];
+        // surely there: two deviations under the sample's count
+        sure += fmaxf(cnt[i], f * (cnt[i] - 2.f * sqrtf(cnt[i]))) * w;
+      }
+#pragma unroll
+      for (int o = 16; o; o >>= 1) sure += __shfl_xor_sync(0xffffffffu, sure, o);
+      float c_incl = c8, w_incl = w8;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const float a = __shfl_up_sync(0xffffffffu, c_incl, o), b = __shfl_up_sync(0xffffffffu, w_incl, o);
+        if (tid >= o) {
+          c_incl += a;
+          w_incl += b;
+        }
+      }
+      const float w_all = __shfl_sync(0xffffffffu, w_incl, 31);
+      // enough: top_k tokens with four deviations of the sample's count; or a
+      // tail of under 0.7 of what the cut leaves out of the mass that is surely
+      // there, the maximum's 1 with it, below a head of so many tokens that the
+      // sample knows what lies beneath
+      const float k_need = (float)top_k / f;
+      const float enough = p.sample_every > 1 ? k_need + 4.f * sqrtf(k_need) + 8.f : k_need;
+      const float left = has_p ? 1.f - top_p : 1.f - u;
+      const float tail = 0.7f * left * (1.f + sure);
+      int b = kCoarse;
+      float c = c_incl - c8, w = w_incl - w8, n_head = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {  // the bins up to this one are enough
+        c += cnt[i];
+        w += wgt[i];
+        const int past = tid * 8 + i + 1;
+        if (b == kCoarse && (want_k ? c >= enough : w_all - w <= tail && c * f >= kLeastHead)) {
+          b = past;
+          n_head = c * f;
+        }
+      }
+      const unsigned any = __ballot_sync(0xffffffffu, b < kCoarse);
+      const int src = any ? __ffs(any) - 1 : 31;
+      b = __shfl_sync(0xffffffffu, b, src);
+      n_head = __shfl_sync(0xffffffffu, any ? n_head : c_incl * f, src);
+      if (tid == 0) {
+        s.found[0] = b;
+        s.found[1] = n_head <= (float)kDirect;
+      }
+    }
+    __syncthreads();
+    const int b = s.found[0];
+    direct = s.found[1];
+    set_cut(sc, b < kCoarse - 8 ? sc.max - (float)b / per : sc.floor);
   }
 
   u64 total = 0;  // first CTA: the row's mass, where need_all
   u64 kept = 0, token = 0;
   for (int round = 0;; ++round) {
-    if (round == 1) {
-      // ---- 3. the sample: how far down the cuts lie ----
-      if (tid < kCoarse) s.coarse[tid] = 0;
-      __syncthreads();
-      const float per = 4.f / 64.f * sc.inv_c;  // quarter octaves per unit of x
-      sweep_sample(row, lo_i, hi_i, p.sample_every, [&](float x) {
-        const float y = (sc.max - x) * per;
-        if (y < (float)(kCoarse - 8)) atomicAdd(s.coarse + (int)y, 1u);
-      });
-      cluster.sync();
-      const float f = (float)p.sample_every;
-      if (tid < 32) {  // a warp: lane l holds eight bins
-        float cnt[8], wgt[8], c8 = 0.f, w8 = 0.f, sure = 0.f;
-        uint32_t n[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) n[i] = 0;
-#pragma unroll
-        for (int c = 0; c < kMaxCluster; ++c)
-          if (c < c_size) {
-            const uint4* o = reinterpret_cast<const uint4*>(cluster.map_shared_rank(&s, c)->coarse) + tid * 2;
-            const uint4 a = o[0], b = o[1];
-            n[0] += a.x; n[1] += a.y; n[2] += a.z; n[3] += a.w;
-            n[4] += b.x; n[5] += b.y; n[6] += b.z; n[7] += b.w;
-          }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          cnt[i] = (float)n[i];
-          const float w = exp2f(-0.25f * (float)(tid * 8 + i));
-          wgt[i] = f * cnt[i] * w;
-          c8 += cnt[i];
-          w8 += wgt[i];
-          // surely there: two deviations under the sample's count
-          sure += fmaxf(cnt[i], f * (cnt[i] - 2.f * sqrtf(cnt[i]))) * w;
-        }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) sure += __shfl_xor_sync(0xffffffffu, sure, o);
-        float c_incl = c8, w_incl = w8;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const float a = __shfl_up_sync(0xffffffffu, c_incl, o), b = __shfl_up_sync(0xffffffffu, w_incl, o);
-          if (tid >= o) {
-            c_incl += a;
-            w_incl += b;
-          }
-        }
-        const float w_all = __shfl_sync(0xffffffffu, w_incl, 31);
-        // enough: top_k tokens with four deviations of the sample's count; what
-        // min_p keeps; or a tail of under 0.7 of what the cut leaves out of the
-        // mass that is surely there, the maximum's 1 with it, below a head of so
-        // many tokens that the sample knows what lies beneath
-        const float k_need = (float)top_k / f;
-        const float enough = p.sample_every > 1 ? k_need + 4.f * sqrtf(k_need) + 8.f : k_need;
-        const float left = has_p ? 1.f - top_p : 1.f - u;
-        const float tail = 0.7f * left * (1.f + sure);
-        int b = kCoarse;
-        float c = c_incl - c8, w = w_incl - w8;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {  // the bins up to this one are enough
-          c += cnt[i];
-          w += wgt[i];
-          const int past = tid * 8 + i + 1;
-          const bool ok = m_only ? (float)past > (sc.max - x_min) * per
-                                 : (want_k ? c >= enough : w_all - w <= tail && c * f >= kBinnedHead);
-          if (ok && b == kCoarse) b = past;
-        }
-        b = __reduce_min_sync(0xffffffffu, b);
-        if (tid == 0) s.found[0] = b;
-      }
-      __syncthreads();
-      const int b = s.found[0];
-      set_cut(sc, m_only ? x_min : (b < kCoarse - 8 ? sc.max - (float)b / per : sc.floor));
-    } else if (round == 2) {
+    if (round) {  // a cut lies further down: every token that has any mass
       set_cut(sc, sc.floor);
+      direct = false;
     }
-    direct = direct && round == 0;
-    if (round == 0 && !direct && !need_all) continue;  // nothing to do before the bins
     bool complete = sc.cut <= sc.floor;  // the head is every token with any mass
     // ---- 2. the mass of all, the head's tokens or bins ----
-    const bool binned = round > 0;
+    const bool binned = !direct;
     if (binned) clear_bins(s);
     if (tid == 0) {
       s.n_list = 0;
@@ -1147,8 +1161,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     __syncthreads();
     {
       const bool all = need_all && round == 0;
-      u64 sum = binned ? sweep_row<kBinnedStages>(s, row, lo_i, hi_i, sc.cut, false, kToBins)
-                       : sweep_row<kStages>(s, row, lo_i, hi_i, direct ? sc.cut : INFINITY, all, kAppend);
+      u64 sum = all ? (binned ? sweep_row<kStages, kToBins, true>(s, row, lo_i, hi_i, sc.cut)
+                              : sweep_row<kStages, kAppend, true>(s, row, lo_i, hi_i, sc.cut))
+                    : (binned ? sweep_row<kStages, kToBins, false>(s, row, lo_i, hi_i, sc.cut)
+                              : sweep_row<kStages, kAppend, false>(s, row, lo_i, hi_i, sc.cut));
       if (all) {
         sum = block_sum(sum, s.red);
         if (tid == 0) s0.part[c_rank] = sum;
@@ -1199,7 +1215,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       if (!binned) {
         int m = 0;
         float least = sc.cut;
-        bool fits = direct;
+        bool fits = true;
         for (int c = 0; c < c_size; ++c) {
           m += s.n_lists[c];
           fits = fits && s.n_lists[c] <= kList;
@@ -1335,7 +1351,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       s.d = d;
     }
     __syncthreads();
-    sweep_row<kBinnedStages>(s, row, lo_i, hi_i, sc.cut, false, kAppendWanted);
+    sweep_row<kBinnedStages, kAppendWanted, false>(s, row, lo_i, hi_i, sc.cut);
     __syncthreads();
     if (tid == 0) s0.n_lists[c_rank] = s.n_list;
     cluster.sync();
@@ -1373,7 +1389,7 @@ cudaError_t launch_sample(SampleParams& p, cudaStream_t st) {
          ((int64_t)p.n_rows * c * 2 <= 2 * sm || std::min<int64_t>(p.n_rows, 2 * sm / c) * row_bytes > kL2Bytes))
     c *= 2;
   p.stretch = ((p.vocab + c - 1) / c + VE - 1) / VE * VE;
-  p.sample_every = std::max(1, p.vocab / 4096);
+  p.sample_every = std::max(1, p.vocab / 8192);
   const size_t smem = sizeof(Smem);
   cudaError_t e = cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e == cudaSuccess) {
