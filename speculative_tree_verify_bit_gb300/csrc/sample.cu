@@ -51,9 +51,8 @@ constexpr int kDirect = 1600;    // more tokens than this are not gathered at on
 constexpr float kLeastHead = 512.f;  // tokens, so that the sample knows what lies beneath
 constexpr int kCoarse = 256;     // quarter octaves of the sample
 constexpr int kMaxVocab = 1 << 19;
-constexpr int64_t kL2Bytes = 80 << 20;  // of 126 MB, for the rows at work at a time
 constexpr int kShift = 14;       // w < 2^45: 2^19 tokens stay below 2^64
-constexpr int kMaxCluster = 16;
+constexpr int kMaxCluster = 8;
 constexpr int kStages = 7;       // one being read, six on their way
 constexpr int kBinnedStages = 4; // where the bins' totals take the place of the others
 
@@ -589,16 +588,17 @@ __device__ __forceinline__ void sum_list(Smem& s, int n, const Scale& sc) {
   __syncthreads();
 }
 
+constexpr u64 kAll = ~0ull;
+
 // The cuts and the draw among the n gathered tokens, sorted in s.list (n >= 1):
 // the whole head, or (binned) the tokens of the bins that the cuts lie in.
 // top_k 0, top_p 1 and has_m false: no such cut.  kept: the mass where nothing
 // is cut (kAll: that of the tokens); on return the kept mass, and the token.
 // False when a cut lies past the tokens.
-constexpr u64 kAll = ~0ull;
-__device__ __noinline__ bool finish(Smem& s, int n, bool binned, int mb, uint32_t top_k, float top_p, bool has_m,
-                                    float u, u64* kept, u64* token) {
+template <int kPer, bool binned>
+__device__ __noinline__ bool finish_by(Smem& s, int n, int mb, uint32_t top_k, float top_p, bool has_m, float u,
+                                       u64* kept, u64* token) {
   const Scale sc = s.sc;
-  constexpr int kPer = kList / kThreads;
   constexpr u64 kNone = ~0ull;
   // a thread's tokens: adjacent ones
   const int i0 = threadIdx.x * kPer;
@@ -682,6 +682,13 @@ __device__ __noinline__ bool finish(Smem& s, int n, bool binned, int mb, uint32_
   return ok;
 }
 
+template <bool binned>
+__device__ __forceinline__ bool finish(Smem& s, int n, int mb, uint32_t top_k, float top_p, bool has_m, float u,
+                                       u64* kept, u64* token) {
+  return n <= kThreads ? finish_by<1, binned>(s, n, mb, top_k, top_p, has_m, u, kept, token)
+                       : finish_by<kList / kThreads, binned>(s, n, mb, top_k, top_p, has_m, u, kept, token);
+}
+
 // Appends tokens to this CTA's list; what does not fit is only counted.
 __device__ __forceinline__ void append(Smem& s, float x, int i) {
   const int at = atomicAdd(&s.n_list, 1);
@@ -696,9 +703,59 @@ __device__ __forceinline__ void append_warp(Smem& s, u64 entry, bool have) {
   if (have && at < kList) s.list[at] = entry;
 }
 
-// ln of a mass, the largest w being 1.
-__device__ __forceinline__ double log_share(u64 mass, const Scale& sc, const Smem& s) {
-  return log((double)mass / (double)weigh(sc.max, sc, s.table, s.table_f));
+// Sums and products in two floats (48 bits).
+struct Pair {
+  float hi, lo;
+};
+__device__ __forceinline__ Pair add_pair(Pair a, Pair b) {
+  const float h = a.hi + b.hi, t = h - a.hi;
+  const float e = (a.hi - (h - t)) + (b.hi - t) + (a.lo + b.lo);
+  const float r = h + e;
+  return {r, e - (r - h)};
+}
+__device__ __forceinline__ Pair mul_pair(Pair a, Pair b) {
+  const float h = a.hi * b.hi;
+  return {h, fmaf(a.hi, b.hi, -h) + (a.hi * b.lo + a.lo * b.hi)};
+}
+
+// ln m, m >= 1, to 4e-9: m = 2^e f with f in [0.7, 1.42), and ln f =
+// 2 atanh(t), t = (f - 1) / (f + 1), by its series (|t| <= 0.18; past t only
+// 2^-8 of the sum is left, for which fp32 is enough).
+__device__ __forceinline__ Pair ln_of(u64 m) {
+  int e = 63 - __clzll((long long)m);
+  const u64 top = m << (63 - e);  // f in [1, 2) as top * 2^-63
+  Pair f = {(float)(uint32_t)(top >> 40) * 0x1p-23f, (float)(uint32_t)((top >> 8) & 0xffffffffu) * 0x1p-55f};
+  if (f.hi > 1.4142135f) {
+    f.hi *= 0.5f;
+    f.lo *= 0.5f;
+    ++e;
+  }
+  const float n = f.hi - 1.f;  // exact
+  const float d = f.hi + 1.f, d1 = d - f.hi, d_lost = (f.hi - (d - d1)) + (1.f - d1);
+  Pair t;
+  t.hi = n / d;
+  t.lo = (fmaf(-t.hi, d, n) + f.lo - t.hi * (f.lo + d_lost)) / d;
+  const float t2 = t.hi * t.hi;
+  float p = fmaf(t2, 1.f / 13.f, 1.f / 11.f);
+  p = fmaf(t2, p, 1.f / 9.f);
+  p = fmaf(t2, p, 1.f / 7.f);
+  p = fmaf(t2, p, 1.f / 5.f);
+  p = fmaf(t2, p, 1.f / 3.f);
+  const Pair ln_f = {2.f * t.hi, 2.f * t.lo + 2.f * t.hi * t2 * p};
+  constexpr double kLn2 = 0.69314718055994530942;
+  constexpr Pair ln2 = {(float)kLn2, (float)(kLn2 - (double)(float)kLn2)};
+  return add_pair(mul_pair({(float)e, 0.f}, ln2), ln_f);
+}
+
+// ln of a token's share of the kept mass: (x - max) / T - ln(kept / w of max).
+__device__ __forceinline__ float log_share(float x, u64 kept, const Scale& sc, const Smem& s) {
+  const float d = x - sc.max, t = d - x;
+  const Pair diff = {d, (x - (d - t)) + (-sc.max - t)};
+  const Pair inv = {(float)s.inv_t, (float)(s.inv_t - (double)(float)s.inv_t)};
+  const Pair a = ln_of(kept), b = ln_of(weigh(sc.max, sc, s.table, s.table_f));
+  Pair r = add_pair(mul_pair(diff, inv), {-a.hi, -a.lo});
+  r = add_pair(r, b);
+  return r.hi + r.lo;
 }
 
 // Adds one token of mass w to a bin.  The mass is kept as two words in
@@ -1244,7 +1301,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
             // all of a complete head may be fewer than top_k
             const uint32_t k = want_k && !(complete && n < top_k) ? (uint32_t)top_k : 0u;
             kept = need_all ? total : kAll;
-            if (finish(s, n, false, 0, k, top_p, has_m, u, &kept, &token)) d.done = kDone;
+            if (finish<false>(s, n, 0, k, top_p, has_m, u, &kept, &token)) d.done = kDone;
           }
         }
       } else {
@@ -1333,23 +1390,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
           d.done = kDone;
         }
       }
-      if (tid == 0) s.d = d;
+      if (tid < c_size) cluster.map_shared_rank(&s, tid)->d = d;
     }
     cluster.sync();
-    d = s0.d;
-    if (d.done == kTooShort) {
-      cluster.sync();  // the decision is read before it is written again
-      continue;
-    }
-    if (d.done == kDone) {
-      cluster.sync();  // the first CTA does not end while its decision is read
-      break;
-    }
+    d = s.d;
+    if (d.done == kTooShort) continue;
+    if (d.done == kDone) break;
     // ---- 3. the tokens of the cuts' bins ----
-    if (tid == 0) {
-      s.n_list = 0;
-      s.d = d;
-    }
+    if (tid == 0) s.n_list = 0;
     __syncthreads();
     sweep_row<kBinnedStages, kAppendWanted, false>(s, row, lo_i, hi_i, sc.cut);
     __syncthreads();
@@ -1362,15 +1410,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       __syncthreads();
       sort_list(s, n);
       kept = need_all ? total : s.tot_mass[kBins - 1];
-      if (n > 0) finish(s, n, true, d.mb, d.kb >= 0 ? (uint32_t)top_k : 0u, top_p, has_m, u, &kept, &token);
+      if (n > 0) finish<true>(s, n, d.mb, d.kb >= 0 ? (uint32_t)top_k : 0u, top_p, has_m, u, &kept, &token);
     }
     cluster.sync();  // no CTA ends while the first one reads its list
     break;
   }
   if (c_rank == 0 && tid == 0) {
     p.ids[r] = (int32_t)(uint32_t)token;
-    if (p.logprob)
-      p.logprob[r] = (float)(((double)entry_x(token) - (double)sc.max) * s.inv_t - log_share(kept, sc, s));
+    if (p.logprob) p.logprob[r] = log_share(entry_x(token), kept, sc, s);
   }
 }
 
@@ -1379,15 +1426,14 @@ cudaError_t launch_sample(SampleParams& p, cudaStream_t st) {
   int sm = 0;
   if (device_sm_count(&sm) != STV_OK) return cudaErrorUnknown;
   constexpr int VE = 16 / sizeof(T);
-  constexpr int kMost = 8;  // CTAs of a cluster
-  // CTAs per row: enough to give every SM two, of 2,048 tokens at least; and as
-  // many as keep the rows at work at a time within L2, which they are read
-  // again from
-  const int64_t row_bytes = (int64_t)p.vocab * sizeof(T);
+  // CTAs per row, of 2,048 tokens at least: as many as make up to four waves of
+  // two CTAs per SM.  A row's last steps are one CTA's, and rows differ in
+  // length several times over (see the bins), so short stretches pay: 128 fp16
+  // rows of 248,320 take 131 us with two, 100 with four, 104 with eight; 512
+  // fp32 rows, which L2 does not hold, 473 us with one, 344 with two, 364 with
+  // four.
   int c = 1;
-  while (c < kMost && p.vocab / (2 * c) >= 2048 &&
-         ((int64_t)p.n_rows * c * 2 <= 2 * sm || std::min<int64_t>(p.n_rows, 2 * sm / c) * row_bytes > kL2Bytes))
-    c *= 2;
+  while (c < kMaxCluster && p.vocab / (2 * c) >= 2048 && (int64_t)p.n_rows * 2 * c <= 8 * sm) c *= 2;
   p.stretch = ((p.vocab + c - 1) / c + VE - 1) / VE * VE;
   p.sample_every = std::max(1, p.vocab / 8192);
   const size_t smem = sizeof(Smem);
