@@ -12,7 +12,8 @@
 // would compute them again for every head), while the loads of its first items
 // are on their way.  An item is two 16-byte loads and stores of one head: a
 // piece of the first half of the rotary channels and its partner in the
-// second, or two pieces past them to copy.
+// second, or two pieces past them to copy, half of what lies there apart, so
+// that neighbouring threads read neighbouring pieces.
 //
 // The call reads and writes each element once: bound by HBM for prompts, by
 // the launch for a round's tree rows.
@@ -29,7 +30,8 @@ namespace {
 
 constexpr int kMaxPairs = 256;
 constexpr int kThreads = 256;  // at least kMaxPairs
-constexpr int kShare = 8;  // items of a thread, for a prompt
+constexpr int kCtasPerSm = 5;  // by registers; 3, 4 and 8 are slower (158, 160 and 186 us for that prompt)
+constexpr int kShare = 8;      // items of a thread, for a prompt
 constexpr int kMaxRowsPer = 8;
 constexpr int kMaxHeadsPer = 64;
 
@@ -70,7 +72,7 @@ __device__ __forceinline__ int quotient(int n, int d, uint32_t inv) {
 }
 
 template <typename T, int VE>
-__global__ void __launch_bounds__(kThreads, 5) rope_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) rope_kernel(const __grid_constant__ RopeParams p) {
   using V = Vec<T, VE>;
   extern __shared__ __align__(16) float table[];  // [rows][half] cosines, then as many sines
   grid_dep_wait();
@@ -93,8 +95,8 @@ __global__ void __launch_bounds__(kThreads, 5) rope_kernel(const __grid_constant
     it->row = quotient(unit, n_heads, heads_inv);
     const int h = h0 + unit - it->row * n_heads;
     it->turns = j < p.rot_items;
-    it->c0 = it->turns ? j * VE : 2 * p.half + (j - p.rot_items) * 2 * VE;
-    it->c1 = it->turns ? it->c0 + p.half : it->c0 + VE;
+    it->c0 = it->turns ? j * VE : 2 * p.half + (j - p.rot_items) * VE;
+    it->c1 = it->c0 + (it->turns ? p.half : (p.items - p.rot_items) * VE);
     const int t = h >= p.heads[0], hh = t ? h - p.heads[0] : h;
     const int64_t r = row0 + it->row;
     *src = static_cast<const T*>(p.in[t]) + r * p.in_row[t] + hh * p.in_head[t];
@@ -165,8 +167,9 @@ cudaError_t launch_rope(RopeParams& p, bool copy_rest, cudaStream_t s) {
   if (device_sm_count(&sm) != STV_OK) return cudaErrorUnknown;
   const int n_heads = p.heads[0] + p.heads[1];
   const int64_t all = (int64_t)p.n_rows * n_heads * p.items;
-  // A CTA's share: kShare items per thread for a prompt; down to one where that
-  // leaves SMs idle.
+  // A CTA's share: kShare items per thread for a prompt (32,768 rows of 28
+  // heads: 150 us; 164 at five; choosing the rows per CTA for whole waves made
+  // no difference), down to one where that leaves SMs idle.
   const int64_t share = std::max<int64_t>(kThreads, std::min<int64_t>(all / (4 * sm), kShare * kThreads));
   const int64_t row_items = (int64_t)n_heads * p.items;
   p.rows_per = (int)std::max<int64_t>(1, std::min<int64_t>({share / row_items, kMaxRowsPer, p.n_rows}));
