@@ -39,7 +39,7 @@
  *    arrays, commit counts) cannot be checked on the host.  Kernels check it
  *    as they read it, never touch memory outside the described buffers, and
  *    OR an STV_DEV_* bit into *dev_status (device int32, may be NULL).
- *  - Supported shape: head_dim 256, group 32, page_tokens 256, hq = G * hkv
+ *  - Supported shape of the round's calls: head_dim 256, group 32, page_tokens 256, hq = G * hkv
  *    with T * G <= 128 query rows per KV head, 1 <= T <= 32 tree nodes,
  *    1 <= n_seqs <= STV_MAX_SEQS.
  *
@@ -540,10 +540,11 @@ int stv_rope(const stv_rope_spec* spec, int dtype, int head_dim, const int32_t* 
  * The row's token is the first, in that order, whose running sum of kept w
  * exceeds u times the whole.  T = 0 takes the first token.
  *
- * Sums of w are exact sums of 64-bit integers, w having a relative error
- * below 2^-29 down to 2^-45 of the largest: the result does not depend on the
- * order in which threads add, and differs from the exact one only where u
- * falls that close to a border between two tokens.
+ * Sums of w are sums of 64-bit integers, w having a relative error below
+ * 2^-28 down to 2^-45 of the largest (and being 0 beyond): the result does not
+ * depend on the order in which threads add, nor on the batch, and differs from
+ * the exact one only where u, or top_p, falls within 2^-29 of the mass of a
+ * border between two tokens.
  *
  *  logits:   device, dtype (enum stv_dtype), row r at logits + r * row_stride
  *            elements; row_stride >= vocab (any alignment of the type).
@@ -589,10 +590,10 @@ typedef struct {
   int32_t n_pages, max_seqs, table_stride;
 } stv_page_pool;
 
-/* Workspace of stv_page_fork, stv_page_compact and stv_page_copy (a list of
- * page copies); no need to clear it.  Calls that overlap on the GPU, graphs
- * among them, need one each. */
-int stv_page_workspace_bytes(const stv_page_pool* pool, size_t* bytes);
+/* Workspace of stv_page_fork, stv_page_compact and stv_page_copy on n_pages
+ * pages (a list of page copies); no need to clear it.  Calls that overlap on
+ * the GPU, graphs among them, need one each. */
+int stv_page_workspace_bytes(int n_pages, size_t* bytes);
 
 /*
  * Gives each of the n sequences pages for ctx[s] + extra tokens (a round's
@@ -641,7 +642,7 @@ int stv_page_compact(const stv_shape* shape, const stv_layer_cache* layers, int 
  * dst are distinct and no dst is a source (STV_DEV_BAD_PAGE, and nothing is
  * copied); a source may be named many times.
  *  src, dst: device int32 [n], n <= n_pages, each in [0, n_pages).
- *  workspace: of a pool of n_pages pages.
+ *  workspace: stv_page_workspace_bytes(n_pages).
  */
 int stv_page_copy(const stv_shape* shape, const stv_layer_cache* layers, int n_layers, int n_pages,
                   const int32_t* src, const int32_t* dst, int n, void* workspace, size_t ws_bytes,

@@ -149,7 +149,7 @@ def load() -> ctypes.CDLL:
         lib.stv_sample.restype = I
         lib.stv_sample.argtypes = [P, I, I64, I, I, P, P, P, P, I, P, P, P, P, P]
         lib.stv_page_workspace_bytes.restype = I
-        lib.stv_page_workspace_bytes.argtypes = [P, P]
+        lib.stv_page_workspace_bytes.argtypes = [I, P]
         lib.stv_page_reserve.restype = I
         lib.stv_page_reserve.argtypes = [P, P, I, P, I, P, P]
         lib.stv_page_fork.restype = I
@@ -672,9 +672,11 @@ def _layer_array(layers, dev):
     return struct.pack("@" + "Pqi4x" * len(layers), *flat)
 
 
-def stv_page_workspace_bytes(pool: PagePool) -> int:
+def stv_page_workspace_bytes(pool) -> int:
+    """Workspace bytes of the page calls on a PagePool, or on so many pages."""
+    n = pool._c.n_pages if isinstance(pool, PagePool) else int(pool)
     out = ctypes.c_size_t()
-    _check("stv_page_workspace_bytes", load().stv_page_workspace_bytes(pool._ref, ctypes.byref(out)))
+    _check("stv_page_workspace_bytes", load().stv_page_workspace_bytes(n, ctypes.byref(out)))
     return out.value
 
 
@@ -727,7 +729,7 @@ def stv_page_compact(shape, layers, pool: PagePool, page_map, n_live, workspace,
 
 def stv_page_copy(shape, layers, src, dst, workspace, dev_status=None, stream=None):
     """Page src[i] to page dst[i] in every layer (int32 CUDA tensors); the
-    workspace is one of a pool of as many pages as the smallest layer's."""
+    workspace is one for as many pages as the smallest layer's pool has."""
     i32 = _t().int32
     dev = _device_of(workspace, "workspace")
     n = src.numel()

@@ -291,7 +291,7 @@ const char* stv_status_string(int status) {
   }
 }
 
-int stv_version(void) { return 2; }
+int stv_version(void) { return 3; }
 
 int stv_page_bytes(const stv_shape* shape, int64_t* bytes) {
   int rc = check_shape(shape, -1, nullptr);

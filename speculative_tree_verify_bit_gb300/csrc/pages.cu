@@ -519,10 +519,10 @@ using namespace stv;
 
 extern "C" {
 
-int stv_page_workspace_bytes(const stv_page_pool* pool, size_t* bytes) {
-  if (int rc = check_pool(pool)) return rc;
-  if (!bytes) return STV_ERR_INVALID_ARG;
-  *bytes = workspace_need(pool->n_pages);
+int stv_page_workspace_bytes(int n_pages, size_t* bytes) {
+  if (!bytes || n_pages < 1) return STV_ERR_INVALID_ARG;
+  if (n_pages > kMaxPages) return STV_ERR_SHAPE_UNSUPPORTED;
+  *bytes = workspace_need(n_pages);
   return STV_OK;
 }
 

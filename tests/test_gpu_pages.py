@@ -334,7 +334,7 @@ def test_pages_in_a_graph(gpu):
     k.check()
 
 
-def test_pages_python_refusals(gpu):
+def test_pages_python_refusals(gpu, monkeypatch):
     k = Kit()
     with pytest.raises(ValueError):
         stv.PagePool(k.pool.refs, k.pool.tables, k.pool.counts[:3])
@@ -347,3 +347,7 @@ def test_pages_python_refusals(gpu):
     with pytest.raises(stv.StvError) as e:
         stv.stv_page_fork(k.shape, k.layers, k.pool, k.ids([0]), k.ids([2]), k.ctx, k.ws[:64])
     assert e.value.status == stv.STV_ERR_WORKSPACE_TOO_SMALL
+    assert stv.stv_page_workspace_bytes(64) == stv.stv_page_workspace_bytes(k.pool)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)  # a pool on another device than the current one
+    with pytest.raises(ValueError):
+        stv.stv_page_free(k.pool, k.ids([0]))

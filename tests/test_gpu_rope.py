@@ -167,7 +167,18 @@ def test_rope_graph_and_stream(gpu):
     assert torch.equal(qo, want * 2)  # doubling is exact
 
 
-def test_rope_python_refusals(gpu):
+def test_rope_no_rows_and_one_view(gpu):
+    spec = stv.make_rope(64, (12, 10, 10))
+    e = torch.empty((0, 4, 64), device="cuda")
+    stv.stv_rope(spec, torch.empty((3, 0), dtype=torch.int32, device="cuda"), e, e)
+    q, k, pos = inputs(9, 4, 2, 64, "bf16", seed=11)
+    both, alone = torch.empty_like(k), torch.empty_like(k)
+    stv.stv_rope(spec, pos, q, torch.empty_like(q), k, both)
+    stv.stv_rope(spec, pos, None, None, k, alone)
+    assert torch.equal(both, alone)
+
+
+def test_rope_python_refusals(gpu, monkeypatch):
     q, k, pos = inputs(4, 2, 1, 64, "fp16")
     spec = stv.make_rope(64, (12, 10, 10))
     out = torch.empty_like(q)
@@ -184,3 +195,8 @@ def test_rope_python_refusals(gpu):
     with pytest.raises(stv.StvError) as e:
         stv.stv_rope(spec, pos, q[:, :1], q[:, :1].as_strided((4, 1, 64), (128, 64, 1), 32))
     assert e.value.status == stv.STV_ERR_INVALID_ARG
+    with pytest.raises(TypeError):
+        stv.stv_rope(spec, pos, q.cpu(), out)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)  # tensors on another device than the current one
+    with pytest.raises(ValueError):
+        stv.stv_rope(spec, pos, q, out)

@@ -1,9 +1,10 @@
 """stv_sample against its definition in 64 bits (opkit.sample).
 
 Ids must be equal, except where u falls within 2^-28 of the kept mass of a
-border between two tokens (weights carry a relative error below 2^-29, the cut
-of top_p and the draw one each); logprob is off by the fp32 rounding, 2^-24 of
-its value, and the masses' 2^-28."""
+border between two tokens: weights carry a relative error below 2^-28, so a
+share f of the mass is off by at most f (1 - f) 2^-27 <= 2^-29, at the cut of
+top_p and at the draw.  logprob is off by the fp32 rounding, 2^-24 of its
+value, and the errors of the masses and their logarithms, 2^-27."""
 import numpy as np
 import pytest
 import torch
@@ -61,6 +62,11 @@ SETS = [
     dict(t=[1e6], p=[0.5]),
     dict(k=[100000000], p=[1.5]),
     dict(k=[-3]),
+    dict(p=[1e-40]),
+    dict(p=[0.99999994]),
+    dict(m=[1e-40]),
+    dict(t=[0.3], m=[1e-6]),
+    dict(k=[2], p=[0.6], m=[0.9]),
 ]
 
 
@@ -213,7 +219,35 @@ def test_sample_graph_stream_and_large_offsets(gpu):
     assert np.array_equal(a[0], b[0]) and np.array_equal(a[1], b[1])
 
 
-def test_sample_python_refusals(gpu):
+def test_sample_no_rows(gpu):
+    e = torch.empty(0, device="cuda")
+    stv.stv_sample(torch.empty((0, 100), device="cuda"), e, torch.empty(0, dtype=torch.int32, device="cuda"), e)
+
+
+def test_sample_smallest_u_and_largest(gpu):
+    """u of 0, the least subnormal and the largest below 1, over a row whose
+    last token in the order has next to no mass."""
+    x = torch.tensor([[0.0, 20.0, -20.0, 5.0]], device="cuda").expand(4, 4).contiguous()
+    u = torch.tensor([0.0, 1e-45, 1.1754944e-38, 0.99999994], device="cuda")
+    check(x, u, rpp=4)
+    check(x, u, rpp=4, t=[30.0])
+
+
+@pytest.mark.parametrize("v", [60000, 248320])
+def test_sample_long_tails(gpu, v):
+    """A few heavy tokens over a wide tail: the cuts lie far down the order."""
+    g = torch.Generator(device="cuda").manual_seed(v)
+    x = torch.randn((12, v), generator=g, device="cuda")
+    x[:, 7::9001] += 9.0
+    x[6:] *= 0.2
+    u = torch.linspace(0.02, 0.9999, 12, device="cuda")
+    for a in (dict(), dict(p=[0.97]), dict(k=[v // 3], p=[0.8]), dict(k=[5000]), dict(m=[0.003]), dict(k=[1900]),
+              dict(t=[0.4], p=[0.9999]), dict(k=[v - 2], m=[1e-4])):
+        check(x, u, rpp=12, **a)
+    check(x.bfloat16(), u, rpp=12, p=[0.99])
+
+
+def test_sample_python_refusals(gpu, monkeypatch):
     logits, u = rows(4, 100, "fp32")
     ids = torch.zeros(4, dtype=torch.int32, device="cuda")
     with pytest.raises(ValueError):
@@ -228,3 +262,8 @@ def test_sample_python_refusals(gpu):
         stv.stv_sample(logits.double(), u, ids)
     with pytest.raises(ValueError):
         stv.stv_sample(logits, u, ids, rows_per_param=0)
+    with pytest.raises((TypeError, ValueError)):
+        stv.stv_sample(logits, u.cpu(), ids)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)  # tensors on another device than the current one
+    with pytest.raises(ValueError):
+        stv.stv_sample(logits, u, ids)

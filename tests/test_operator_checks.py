@@ -128,12 +128,17 @@ def pool(refs=D, tables=D, counts=D, n_pages=100, max_seqs=8, stride=20):
     (pool(n_pages=262144, max_seqs=4096), stv.STV_OK),
 ])
 def test_pool_checks(lib, p, rc):
-    out = ctypes.c_size_t()
-    assert lib.stv_page_workspace_bytes(ctypes.byref(p), ctypes.byref(out)) == rc
-    if rc == stv.STV_OK:
-        assert out.value == 16 + 8 * p.n_pages
     assert lib.stv_page_reserve(ctypes.byref(p), D, 0, D, 16, None, None) == rc
     assert lib.stv_page_free(ctypes.byref(p), D, 0, None, None) == rc
+
+
+@pytest.mark.parametrize("n,rc", [(1, stv.STV_OK), (100, stv.STV_OK), (262144, stv.STV_OK), (0, BAD), (-5, BAD),
+                                  (262145, SHAPE)])
+def test_page_workspace(lib, n, rc):
+    out = ctypes.c_size_t()
+    assert lib.stv_page_workspace_bytes(n, ctypes.byref(out)) == rc
+    assert rc != stv.STV_OK or out.value == 16 + 8 * n
+    assert lib.stv_page_workspace_bytes(n, None) != stv.STV_OK
 
 
 def test_page_list_checks(lib):
