@@ -30,8 +30,8 @@ namespace {
 
 constexpr int kMaxPairs = 256;
 constexpr int kThreads = 256;  // at least kMaxPairs
-constexpr int kCtasPerSm = 5;  // by registers; 3, 4 and 8 are slower (158, 160 and 186 us for that prompt)
-constexpr int kShare = 8;      // items of a thread, for a prompt
+constexpr int kCtasPerSm = 5;  // by registers
+constexpr int kShare = 14;     // items of a thread, for a prompt
 constexpr int kMaxRowsPer = 8;
 constexpr int kMaxHeadsPer = 64;
 
@@ -45,9 +45,8 @@ struct RopeParams {
   const int32_t* pos;
   int n_rows;
   int half, head_dim;
-  int rot_items, items;  // per head: items that turn pairs, and those plus the ones that copy
+  int rot_items, items;  // per head: items that turn pairs, and those plus the ones that copy (<= kThreads)
   int rows_per, heads_per, head_blocks;  // a CTA's rows and heads; CTAs per block of rows
-  uint32_t items_inv;                    // floor(2^32 / items) + 1 (see quotient)
   int negate;
 };
 
@@ -66,11 +65,6 @@ struct alignas(sizeof(T) * VE) Vec {
   T e[VE];
 };
 
-// n / d for n * d < 2^32, with inv = floor(2^32 / d) + 1 (d > 1).
-__device__ __forceinline__ int quotient(int n, int d, uint32_t inv) {
-  return d == 1 ? n : (int)__umulhi((uint32_t)n, inv);
-}
-
 template <typename T, int VE>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) rope_kernel(const __grid_constant__ RopeParams p) {
   using V = Vec<T, VE>;
@@ -81,41 +75,34 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) rope_kernel(const __grid
   const int row0 = (int)(blockIdx.x / p.head_blocks) * p.rows_per;
   const int n_rows = min(p.rows_per, p.n_rows - row0);
   const int h0 = hb * p.heads_per, n_heads = min(p.heads_per, p.heads[0] + p.heads[1] - h0);
-  const int n_items = n_rows * n_heads * p.items;
-  const uint32_t heads_inv = n_heads > 1 ? 0xffffffffu / n_heads + 1 : 0;
   float* sines = table + p.rows_per * p.half;
 
-  // an item: its row here, its two channels (c1 past the head: one piece only), its head's place
-  struct Item {
-    int row, c0, c1;
-    bool turns;
-  };
-  auto locate = [&](int e, Item* it, const T** src, T** dst) {
-    const int unit = quotient(e, p.items, p.items_inv), j = e - unit * p.items;
-    it->row = quotient(unit, n_heads, heads_inv);
-    const int h = h0 + unit - it->row * n_heads;
-    it->turns = j < p.rot_items;
-    it->c0 = it->turns ? j * VE : 2 * p.half + (j - p.rot_items) * VE;
-    it->c1 = it->c0 + (it->turns ? p.half : (p.items - p.rot_items) * VE);
-    const int t = h >= p.heads[0], hh = t ? h - p.heads[0] : h;
-    const int64_t r = row0 + it->row;
-    *src = static_cast<const T*>(p.in[t]) + r * p.in_row[t] + hh * p.in_head[t];
-    *dst = static_cast<T*>(p.out[t]) + r * p.out_row[t] + hh * p.out_head[t];
-  };
-  auto load = [&](int e, Item* it, T** dst, V* a, V* b) {
-    if (e < n_items) {
-      const T* src;
-      locate(e, it, &src, dst);
-      *a = *reinterpret_cast<const V*>(src + it->c0);
-      if (it->c1 < p.head_dim) *b = *reinterpret_cast<const V*>(src + it->c1);
+  // A thread keeps to one item of a head, its two pieces c0 and c1 (c1 past the
+  // head: one piece only), and steps over the (row, head) pairs.
+  const int at_once = kThreads / p.items;  // pairs
+  const int u0 = (int)threadIdx.x / p.items, j = (int)threadIdx.x - u0 * p.items;
+  const bool turns = j < p.rot_items;
+  const int c0 = turns ? j * VE : 2 * p.half + (j - p.rot_items) * VE;
+  const int c1 = c0 + (turns ? p.half : (p.items - p.rot_items) * VE);
+  const bool two = c1 < p.head_dim;
+  int row = u0 / n_heads, h = u0 - row * n_heads;
+  const int row_step = at_once / n_heads, h_step = at_once - row_step * n_heads;
+  if (u0 >= at_once) row = n_rows;
+
+  auto load = [&](int r, int hh, V& a, V& b) {
+    if (r < n_rows) {
+      hh += h0;
+      const int t = hh >= p.heads[0];
+      const T* src = static_cast<const T*>(p.in[t]) + (row0 + r) * p.in_row[t] +
+                     (hh - (t ? p.heads[0] : 0)) * p.in_head[t];
+      a = *reinterpret_cast<const V*>(src + c0);
+      if (two) b = *reinterpret_cast<const V*>(src + c1);
     }
   };
-  V a, b;
-  Item it;
-  T* dst;
-  load(threadIdx.x, &it, &dst, &a, &b);
+  V x, y;
+  load(row, h, x, y);
   {
-    // the table: a thread keeps to one pair, whose parameters it reads once
+    // the table: a thread keeps to one pair of channels, whose parameters it reads once
     const int rows_at_once = kThreads / p.half;
     const int r0 = (int)threadIdx.x / p.half, pair = (int)threadIdx.x - r0 * p.half;
     if (r0 < rows_at_once) {
@@ -133,28 +120,32 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) rope_kernel(const __grid
     __syncthreads();
   }
 #pragma unroll 1
-  for (int e = threadIdx.x; e < n_items; e += kThreads) {
-    // the next item's loads, ahead of this one's arithmetic and stores
-    V a1, b1;
-    Item it1;
-    T* dst1;
-    load(e + kThreads, &it1, &dst1, &a1, &b1);
-    if (it.turns) {
-      const Vec<float, VE>& c = *reinterpret_cast<const Vec<float, VE>*>(table + it.row * p.half + it.c0);
-      const Vec<float, VE>& s = *reinterpret_cast<const Vec<float, VE>*>(sines + it.row * p.half + it.c0);
+  while (row < n_rows) {
+    const int r = row, hh = h0 + h;
+    row += row_step;
+    h += h_step;
+    if (h >= n_heads) {
+      h -= n_heads;
+      ++row;
+    }
+    V x1, y1;
+    load(row, h, x1, y1);  // before this item's own loads are waited for
+    if (turns) {
+      const Vec<float, VE>& c = *reinterpret_cast<const Vec<float, VE>*>(table + r * p.half + c0);
+      const Vec<float, VE>& s = *reinterpret_cast<const Vec<float, VE>*>(sines + r * p.half + c0);
 #pragma unroll
       for (int i = 0; i < VE; ++i) {
-        const float x = to_f(a.e[i]), y = to_f(b.e[i]);
-        a.e[i] = from_f<T>(x * c.e[i] - y * s.e[i]);
-        b.e[i] = from_f<T>(y * c.e[i] + x * s.e[i]);
+        const float u = to_f(x.e[i]), v = to_f(y.e[i]);
+        x.e[i] = from_f<T>(u * c.e[i] - v * s.e[i]);
+        y.e[i] = from_f<T>(v * c.e[i] + u * s.e[i]);
       }
     }
-    *reinterpret_cast<V*>(dst + it.c0) = a;
-    if (it.c1 < p.head_dim) *reinterpret_cast<V*>(dst + it.c1) = b;
-    a = a1;
-    b = b1;
-    it = it1;
-    dst = dst1;
+    const int t = hh >= p.heads[0];
+    T* dst = static_cast<T*>(p.out[t]) + (row0 + r) * p.out_row[t] + (hh - (t ? p.heads[0] : 0)) * p.out_head[t];
+    *reinterpret_cast<V*>(dst + c0) = x;
+    if (two) *reinterpret_cast<V*>(dst + c1) = y;
+    x = x1;
+    y = y1;
   }
 }
 
@@ -167,17 +158,17 @@ cudaError_t launch_rope(RopeParams& p, bool copy_rest, cudaStream_t s) {
   if (device_sm_count(&sm) != STV_OK) return cudaErrorUnknown;
   const int n_heads = p.heads[0] + p.heads[1];
   const int64_t all = (int64_t)p.n_rows * n_heads * p.items;
-  // A CTA's share: kShare items per thread for a prompt (32,768 rows of 28
-  // heads: 150 us; 164 at five; choosing the rows per CTA for whole waves made
-  // no difference), down to one where that leaves SMs idle.
-  const int64_t share = std::max<int64_t>(kThreads, std::min<int64_t>(all / (4 * sm), kShare * kThreads));
+  // A CTA's share: up to kShare items per thread (32,768 rows of 28 heads: 148
+  // us at 14, 152 at 8, 168 at 5), but three waves of CTAs at least (4,097 fp32
+  // rows: 39 us in five waves, 47 in one and a third), and one item per thread
+  // where that leaves SMs idle.
+  const int64_t share = std::max<int64_t>(kThreads, std::min<int64_t>(all / (16 * sm), kShare * kThreads));
   const int64_t row_items = (int64_t)n_heads * p.items;
   p.rows_per = (int)std::max<int64_t>(1, std::min<int64_t>({share / row_items, kMaxRowsPer, p.n_rows}));
   p.heads_per = (int)std::max<int64_t>(1, std::min<int64_t>({share / p.items, n_heads, kMaxHeadsPer}));
   if (p.rows_per > 1) p.heads_per = std::min(n_heads, kMaxHeadsPer);
   p.head_blocks = (n_heads + p.heads_per - 1) / p.heads_per;
   p.heads_per = (n_heads + p.head_blocks - 1) / p.head_blocks;
-  p.items_inv = p.items > 1 ? (uint32_t)((1ull << 32) / p.items + 1) : 0;
   const int64_t grid = (int64_t)((p.n_rows + p.rows_per - 1) / p.rows_per) * p.head_blocks;
   if (grid > 0x7fffffff) return cudaErrorInvalidValue;
   const size_t smem = (size_t)p.rows_per * p.half * 2 * sizeof(float);
