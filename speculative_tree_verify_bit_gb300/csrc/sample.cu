@@ -93,9 +93,8 @@ struct Scale {
   float zero;   // below it w = 0 (w of 2^-45 of the largest's octave is 0 already)
   float base;   // 0; the maximum where x / C would leave the integers of fp32: there
                 // x - max is exact for every x >= floor
-  float least;  // rint(x / C) of the floor, as kMagic + k: smaller ones count as it
   float inv_c, c_hi, c_lo, inv_t;
-  int top;          // octave of the maximum
+  int top;          // octave of the maximum, plus 32 - kShift
   float cut;        // the head: x >= cut
   float bin_scale;  // bins of the head, from the maximum down
   float x_min;      // the least x that min_p keeps
@@ -117,8 +116,8 @@ struct alignas(16) Smem {
   u64 queue[kThreads / 32][64];   // a warp's tokens of the head, taken 32 at a time
   alignas(16) uint32_t coarse[kCoarse];
   uint32_t coarse_all[kCoarse];
-  uint32_t table[64];
-  float table_f[64];
+  uint32_t table[64];  // 2^30 2^(j / 64), less four times the bits of kMagic
+  float table_f[64];   // 2^28 2^(j / 64)
   u64 red[kThreads / 32];
   uint32_t red_c[kThreads / 32];
   u64 out;
@@ -184,9 +183,7 @@ __device__ __forceinline__ Scale make_scale(const Smem& s, float max, float min_
   sc.floor = __fsub_rd(max, __fmul_ru(62.f * 64.f, s.c_hi));
   sc.zero = __fsub_rd(max, __fmul_ru(48.f * 64.f, s.c_hi));
   sc.base = fabsf(max) * sc.inv_c < 2097152.f ? 0.f : max;
-  const float t = fmaf(max - sc.base, sc.inv_c, kMagic);
-  sc.top = __float_as_int(t) >> 6;
-  sc.least = t - 62.f * 64.f;
+  sc.top = (__float_as_int(fmaf(max - sc.base, sc.inv_c, kMagic)) >> 6) + 32 - kShift;
   sc.cut = sc.floor;
   sc.bin_scale = 0.f;
   sc.x_min = -INFINITY;
@@ -200,8 +197,9 @@ __device__ __forceinline__ Scale make_scale(const Smem& s, float max, float min_
 // w from rint(x / C) (the bits of kMagic + k) and the correction of 2^(k/64),
 // in quarters (kMagic + q).
 __device__ __forceinline__ u64 weight_of(int kb, float q, const Scale& sc, const uint32_t* table) {
-  const uint32_t m = table[kb & 63] + ((uint32_t)(__float_as_int(q) - 0x4b400000) << 2);
-  const u64 w = ((u64)m << kShift) >> (sc.top - (kb >> 6));
+  const uint32_t m = table[kb & 63] + ((uint32_t)__float_as_int(q) << 2);
+  u64 w;  // m 2^14 2^-octaves; a shift by 64 or more leaves 0
+  asm("shr.u64 %0, %1, %2;" : "=l"(w) : "l"((u64)m << 32), "r"(sc.top - (kb >> 6)));
   // cut to even, plus one where anything is left: no bias
   const uint32_t lo = (uint32_t)w;
   return (w & 0xffffffff00000000ull) | (lo | min(lo, 1u));
@@ -210,7 +208,8 @@ __device__ __forceinline__ u64 weight_of(int kb, float q, const Scale& sc, const
 // w of a token that is not NaN (0 for -inf and whatever lies below the floor).
 __device__ __forceinline__ u64 weigh(float x, const Scale& sc, const uint32_t* table, const float* table_f) {
   const float v = x - sc.base;
-  const float t = fmaxf(fmaf(v, sc.inv_c, kMagic), sc.least);  // (at 62 octaves any z gives w = 0)
+  // (far down, t is no longer kMagic + an integer; its bits are yet smaller, and w is 0 whatever z)
+  const float t = fmaf(v, sc.inv_c, kMagic);
   const int kb = __float_as_int(t);
   const float k = t - kMagic;
   const float z = fmaf(k, -sc.c_lo, fmaf(k, -sc.c_hi, v)) * sc.inv_t;
@@ -250,8 +249,6 @@ __device__ __forceinline__ u64 weigh_two(float xa, float xb, const Scale& sc, co
   const u64 v = add2(pack2(xa, xb), pack2(-sc.base, -sc.base));
   float ta, tb;
   unpack2(fma2(v, pack2(sc.inv_c, sc.inv_c), pack2(kMagic, kMagic)), ta, tb);
-  ta = fmaxf(ta, sc.least);
-  tb = fmaxf(tb, sc.least);
   const int ka = __float_as_int(ta), kb = __float_as_int(tb);
   const u64 k = add2(pack2(ta, tb), pack2(-kMagic, -kMagic));
   const u64 z = mul2(fma2(k, pack2(-sc.c_lo, -sc.c_lo), fma2(k, pack2(-sc.c_hi, -sc.c_hi), v)),
@@ -990,7 +987,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   const int r = blockIdx.x / c_size;
   Smem& s0 = *cluster.map_shared_rank(&s, 0);
   if (tid < 64) {
-    s.table[tid] = p.table[tid];
+    s.table[tid] = p.table[tid] - ((uint32_t)__float_as_int(kMagic) << 2);
     s.table_f[tid] = (float)p.table[tid] * 0.25f;
   }
   if (tid < kCoarse) s.coarse[tid] = 0;
