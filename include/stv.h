@@ -20,6 +20,9 @@
  *  - syv-ai README (mirror), split-KV scratch buffer section: the verify
  *    workspace must be sized and owned by someone.
  *    -> stv_verify_workspace_bytes; the caller owns the workspace.
+ * Around the round, where the pages say nothing: the rows' rotary positions
+ * before the append (stv_rope), the target's token at each node before the
+ * acceptance (stv_sample), and who owns which page (stv_page_*).
  *
  * Conventions (every entry point):
  *  - extern "C"; returns STV_OK (0) or a negative STV_ERR_* status.  Host

@@ -26,6 +26,15 @@
 // times e^(z / T), |z / T| <= ln 2 / 128, whose cubic is rounded to 2^-29 of w.
 // Integer sums do not depend on their order, so masses, bins and tokens depend
 // neither on the cluster's size nor on the batch.
+//
+// What bounds it.  16 bf16 rows of 248,320 tokens (8 MB, 1.2 us at the copy
+// bandwidth) take 21.5 us: a chain of steps of one to four microseconds with a
+// barrier after each (first pass 2.8, groups 2, second pass 4.7, merge and sort
+// 3.2, cuts and barriers 4; 41 % of the warps' time is spent waiting at
+// barriers).  512 fp32 rows (508 MB, 75 us) take 318 us: the sum of all weights
+// runs at the issue limit, 24 instructions a token (25.4 us for the 124,160
+// tokens of each of an SM's two CTAs), and the rows are read twice or three
+// times, in part from HBM.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <math.h>
@@ -1426,9 +1435,8 @@ cudaError_t launch_sample(SampleParams& p, cudaStream_t st) {
   // CTAs per row, of 2,048 tokens at least: as many as make up to four waves of
   // two CTAs per SM.  A row's last steps are one CTA's, and rows differ in
   // length several times over (see the bins), so short stretches pay: 128 fp16
-  // rows of 248,320 take 131 us with two, 100 with four, 104 with eight; 512
-  // fp32 rows, which L2 does not hold, 473 us with one, 344 with two, 364 with
-  // four.
+  // rows of 248,320 take 121 us with two, 92 with four, 93 with eight; 512 fp32
+  // rows, which L2 does not hold, 454 us with one, 318 with two, 326 with four.
   int c = 1;
   while (c < kMaxCluster && p.vocab / (2 * c) >= 2048 && (int64_t)p.n_rows * 2 * c <= 8 * sm) c *= 2;
   p.stretch = ((p.vocab + c - 1) / c + VE - 1) / VE * VE;
