@@ -163,6 +163,26 @@ def test_sample_row_counts(gpu, n):
     check(logits, u, t=[0.9], p=[0.9], rpp=n)
 
 
+@pytest.mark.parametrize("dt", ["fp32", "bf16"])
+@pytest.mark.parametrize("v", [1, 130, 2000, 16384])
+def test_sample_many_short_rows(gpu, dt, v):
+    """More short rows than SMs hold wide CTAs for: one narrow CTA per row.
+    Against the definition, and the same as the rows get a few at a time."""
+    n = 420
+    logits, u = rows(n, v, dt, seed=v, pad=3)
+    logits[5:9] = 0.5                      # flat
+    logits[9, : v // 2] = -float("inf")
+    logits[10] *= 0.01
+    kw = [dict(), dict(t=[0.7], p=[0.9]), dict(k=[40], p=[0.95], m=[0.01]), dict(k=[700], t=[2.0]), dict(t=[3.0], p=[0.99]),
+          dict(m=[0.3]), dict(t=[0.0])]
+    for a in kw:
+        ids, lp = draw(logits, u, rpp=n, **a)
+        few, lp2 = draw(logits[:40], u[:40], rpp=40, **a)
+        assert np.array_equal(ids[:40], few) and np.array_equal(lp[:40], lp2)
+    check(logits[:n], u, rpp=n, **kw[v % len(kw)])
+    check(logits[:n], u, rpp=n, t=[1.5], p=[0.97])
+
+
 def test_sample_does_not_depend_on_the_batch(gpu):
     """A row's token and logprob are the same alone, in a batch, twice, and
     wherever the row starts."""
