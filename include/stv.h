@@ -584,7 +584,9 @@ int stv_sample(const void* logits, int dtype, int64_t row_stride, int n_rows, in
  * stv_page_compact is all or nothing: when anything that it reads is wrong
  * (STV_DEV_BAD_SEQ, STV_DEV_BAD_PAGE) or pages are short (STV_DEV_NO_PAGES),
  * it changes nothing.  1 <= n_pages <= 262,144, 1 <= max_seqs <= 4,096 (else
- * STV_ERR_SHAPE_UNSUPPORTED); calls on one pool must not overlap.
+ * STV_ERR_SHAPE_UNSUPPORTED); a call of n sequences takes tables with up to
+ * 2^30 / n entries in use (more is STV_DEV_BAD_SEQ; sequences that hold each
+ * page once never have more); calls on one pool must not overlap.
  */
 typedef struct {
   int32_t* refs;

@@ -67,6 +67,7 @@ __device__ __forceinline__ int block_scan(int x, int* total) {
 }
 
 // In-place exclusive scan of a[0 .. n), a[n] = the sum.  Ends with a barrier.
+// Sums are 32-bit: see sum_fits.
 __device__ __forceinline__ void scan_array(int* a, int n) {
   const int per = (n + kBookThreads - 1) / kBookThreads;
   const int i0 = min((int)threadIdx.x * per, n), i1 = min(i0 + per, n);
@@ -81,6 +82,15 @@ __device__ __forceinline__ void scan_array(int* a, int n) {
   }
   if (threadIdx.x == 0) a[n] = total;
   __syncthreads();
+}
+
+// Whether n sequences with this many entries each can be added up, and stepped
+// through, in 32 bits.  Sequences that hold each page once always can (2^18
+// pages, 2^12 sequences); longer tables, with pages named again in them, may not.
+__device__ __forceinline__ bool sum_fits(int entries, int n) {
+  constexpr int64_t kMost = (int64_t)kMaxPages * kMaxPoolSeqs;
+  static_assert(kMost + kMaxPoolSeqs + kBookThreads < 0x7fffffff, "no sum of pages passes 32 bits");
+  return (int64_t)entries * n <= kMost;
 }
 
 // Last i in [0, n) with a[i] <= r, a ascending, a[0] <= r.
@@ -189,8 +199,8 @@ __global__ void __launch_bounds__(kBookThreads) page_reserve_kernel(const __grid
     const int64_t need = ((int64_t)c + p.extra + kPageTok - 1) / kPageTok;
     if (have < 0 || c < 0 || have > pool.table_stride || need > pool.table_stride)
       bad = STV_DEV_BAD_SEQ;
-    else if (need > have)
-      off[i] = (int)need - have;
+    else if (need > have)  // past n_pages, pages are short however many they are
+      off[i] = (int)min(need - have, (int64_t)pool.n_pages + 1);
   }
   if (call_fails(bad, p.status)) return;
   scan_array(off, p.n);
@@ -229,7 +239,7 @@ __global__ void __launch_bounds__(kBookThreads) page_free_kernel(const __grid_co
       continue;
     }
     const int have = pool.counts[s];
-    if (have < 0 || have > pool.table_stride) bad = STV_DEV_BAD_SEQ; else off[i] = have;
+    if (have < 0 || have > pool.table_stride || !sum_fits(have, p.n)) bad = STV_DEV_BAD_SEQ; else off[i] = have;
   }
   if (call_fails(bad, p.status)) return;
   scan_array(off, p.n);
@@ -274,7 +284,7 @@ __global__ void __launch_bounds__(kBookThreads) page_fork_kernel(const __grid_co
     }
     const int c = p.ctx[a], have = pool.counts[a];
     const int pages = c / kPageTok + (c % kPageTok != 0);
-    if (c < 0 || pages > have || have > pool.table_stride || pool.counts[b] != 0) {
+    if (c < 0 || pages > have || have > pool.table_stride || !sum_fits(pages, p.n) || pool.counts[b] != 0) {
       bad = STV_DEV_BAD_SEQ;
       continue;
     }

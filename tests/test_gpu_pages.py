@@ -351,3 +351,38 @@ def test_pages_python_refusals(gpu, monkeypatch):
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)  # a pool on another device than the current one
     with pytest.raises(ValueError):
         stv.stv_page_free(k.pool, k.ids([0]))
+
+
+@pytest.mark.parametrize("m,stride", [(4096, 1 << 19), (2048, (1 << 20) + 1024)])
+def test_totals_past_32_bits(gpu, m, stride):
+    """Every sequence with 2^31 / m pages or more: their sum passes an int.
+    The pool has far fewer pages, and no call changes anything."""
+    n_pages = 100
+    pool = stv.PagePool(torch.zeros(n_pages, dtype=torch.int32, device="cuda"),
+                        torch.full((m, stride), -1, dtype=torch.int32, device="cuda"),
+                        torch.zeros(m, dtype=torch.int32, device="cuda"))
+    layers = [stv.LayerCache.empty(n_pages, 1)]
+    ws = torch.empty(stv.stv_page_workspace_bytes(pool), dtype=torch.uint8, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    seqs = torch.arange(m, dtype=torch.int32, device="cuda")
+    ctx = torch.full((m,), stride * 256 - 16, dtype=torch.int32, device="cuda")
+
+    def unchanged(bit, counts, contexts):
+        assert int(status.item()) == bit
+        status.zero_()
+        assert not pool.refs.any() and torch.equal(pool.counts, counts) and torch.equal(ctx, contexts)
+        for t in pool.tables.split(512):
+            assert int(t.min().item()) == int(t.max().item()) == -1
+
+    want = ctx.clone()
+    stv.stv_page_reserve(pool, seqs, ctx, 16, dev_status=status)
+    unchanged(stv.STV_DEV_NO_PAGES, torch.zeros_like(seqs), want)
+    pool.counts.fill_(stride)  # tables that name pages over and over
+    held = pool.counts.clone()
+    stv.stv_page_free(pool, seqs, dev_status=status)
+    unchanged(stv.STV_DEV_BAD_SEQ, held, want)
+    pool.counts[1:] = 0  # one source, forked into all others
+    held = pool.counts.clone()
+    stv.stv_page_fork(stv.make_shape(6, 1), layers, pool, torch.zeros_like(seqs[1:]), seqs[1:], ctx, ws,
+                      dev_status=status)
+    unchanged(stv.STV_DEV_BAD_SEQ, held, want)
