@@ -487,10 +487,16 @@ int fill_copy(const stv_shape* shape, const stv_layer_cache* layers, int n_layer
   return STV_OK;
 }
 
+// The largest books' shared memory (fork's).  Books that need the attribute ask
+// for this much of it, always: it belongs to the function, so a smaller value
+// would lower what a call of another thread on larger books has just set.
+constexpr size_t kPlainSmem = 40 * 1024;
+size_t most_smem() { return (size_t)(kMaxPoolSeqs + 1) * 8 + LiveMap::bytes(kMaxPages); }
+
 template <typename... KArgs>
 cudaError_t launch_book(void (*kernel)(KArgs...), size_t smem, const BookParams& b, cudaStream_t s) {
-  if (smem > 40 * 1024) {
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (smem > kPlainSmem) {
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most_smem());
     if (e != cudaSuccess) {
       (void)cudaGetLastError();
       return e;

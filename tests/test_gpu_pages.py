@@ -386,3 +386,45 @@ def test_totals_past_32_bits(gpu, m, stride):
     stv.stv_page_fork(stv.make_shape(6, 1), layers, pool, torch.zeros_like(seqs[1:]), seqs[1:], ctx, ws,
                       dev_status=status)
     unchanged(stv.STV_DEV_BAD_SEQ, held, want)
+
+
+def big_books(n_pages):
+    pool = stv.PagePool.empty(n_pages, 2, 64)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    one = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ctx = torch.tensor([700, 0], dtype=torch.int32, device="cuda")
+    return pool, status, one, ctx
+
+
+def test_books_of_two_sizes_from_two_threads(gpu):
+    """A call on large books is launched whatever size another thread's have."""
+    from concurrent.futures import ThreadPoolExecutor
+
+    def work(n_pages):
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            pool, status, one, ctx = big_books(n_pages)
+            for _ in range(3000):
+                stv.stv_page_reserve(pool, one, ctx, 16, dev_status=status)
+            stream.synchronize()
+            assert int(status.item()) == 0 and pool.tables[0, :3].tolist() == [0, 1, 2]
+            assert int(pool.counts[0].item()) == 3
+        return True
+
+    with ThreadPoolExecutor(2) as ex:
+        assert all(ex.map(work, (262144, 170000)))
+
+
+def test_books_of_two_sizes_in_a_graph(gpu):
+    """A graph with calls on large and then smaller books replays both."""
+    kits = [big_books(n) for n in (262144, 170000)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        for pool, status, one, ctx in kits:
+            stv.stv_page_reserve(pool, one, ctx, 16, dev_status=status)
+    graph.replay()
+    torch.cuda.synchronize()
+    for pool, status, one, ctx in kits:
+        assert int(status.item()) == 0 and pool.tables[0, :3].tolist() == [0, 1, 2]
