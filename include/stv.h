@@ -543,11 +543,17 @@ int stv_rope(const stv_rope_spec* spec, int dtype, int head_dim, const int32_t* 
  * The row's token is the first, in that order, whose running sum of kept w
  * exceeds u times the whole.  T = 0 takes the first token.
  *
- * Sums of w are sums of 64-bit integers, w having a relative error below
- * 2^-28 down to 2^-45 of the largest (and being 0 beyond): the result does not
- * depend on the order in which threads add, nor on the batch, and differs from
- * the exact one only where u, or top_p, falls within 2^-29 of the mass of a
- * border between two tokens.
+ * Sums of w are sums of 64-bit integers, so the result does not depend on the
+ * order in which threads add, nor on the batch.  w is off by less than 2^-28
+ * of itself plus 2^-44 of the largest (under which it may be 0).  The result
+ * differs from the exact one only where u, or top_p, falls within
+ *     2^-29 + n 2^-44 / m
+ * of the mass's border between two tokens, where n tokens are added up and m
+ * is their mass in units of the largest w: at most 2^-28 for
+ * 32,768 tokens and about 2^-25 for 524,288 (half the step that a u in fp32
+ * has below 1), which takes tokens that are nearly all equal, so that their
+ * errors add up, and so far down that the largest has nearly all the mass.
+ * logprob is off by its rounding, 2^-27 and n 2^-44 / m.
  *
  *  logits:   device, dtype (enum stv_dtype), row r at logits + r * row_stride
  *            elements; row_stride >= vocab (any alignment of the type).

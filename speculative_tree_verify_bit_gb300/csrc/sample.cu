@@ -24,7 +24,11 @@
 // T ln 2 / 64, k = rint(x / C) and z = x - k C (C in two floats; the first
 // product's remainder is exact), w is 2^(k / 64) from a table of 64 entries
 // times e^(z / T), |z / T| <= ln 2 / 128, whose cubic is rounded to 2^-29 of w.
-// Integer sums do not depend on their order, so masses, bins and tokens depend
+// With the table, the constants and the products that is less than 2^-28 of w,
+// and cutting w to a whole number adds up to a unit, at most 2^-44 of the
+// largest: from 2^-16 of the largest down, the unit is what counts.  2^19
+// tokens of scale 2^45 are all that 64 bits add up; finer units would take sums
+// of two words, in the loop with the most instructions.  Integer sums do not depend on their order, so masses, bins and tokens depend
 // neither on the cluster's size nor on the batch.
 //
 // What bounds it.  16 bf16 rows of 248,320 tokens (8 MB, 1.2 us at the copy

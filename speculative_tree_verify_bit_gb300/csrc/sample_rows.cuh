@@ -138,7 +138,8 @@ __device__ __forceinline__ u64 weight_of(int kb, float q, const Scale& sc, const
   const uint32_t m = table[kb & 63] + ((uint32_t)__float_as_int(q) << 2);
   u64 w;  // m 2^14 2^-octaves; a shift by 64 or more leaves 0
   asm("shr.u64 %0, %1, %2;" : "=l"(w) : "l"((u64)m << 32), "r"(sc.top - (kb >> 6)));
-  // cut to even, plus one where anything is left: no bias
+  // the last bit set where anything is left: off by up to one either way, which
+  // evens out over tokens that differ (equal ones are all off by the same)
   const uint32_t lo = (uint32_t)w;
   return (w & 0xffffffff00000000ull) | (lo | min(lo, 1u));
 }
