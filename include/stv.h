@@ -492,8 +492,9 @@ enum stv_dtype { STV_F32 = 0, STV_F16 = 1, STV_BF16 = 2 };
  *     out[i + h] = x[i + h] cos(phi) + x[i] sin(phi)
  * and channels from rotary_dim on are copied.  inverse turns by -phi: the
  * gradient of the call, and what takes a position back out of a row.
- * Products are formed in fp32 and rounded once; phi is exact to 2^-31 of a
- * turn for every int32 position, negative ones among them.
+ * Products are formed in fp32 and rounded once; phi is off by at most 2^-26
+ * of a turn (its rounding to fp32) and 2^-31 for every int32 position,
+ * negative ones among them.
  */
 typedef struct {
   int32_t rotary_dim;  /* even, 2 .. head_dim */

@@ -3,9 +3,11 @@
 //
 // Angles.  A frequency is kept in turns as a 64-bit fixed-point fraction F =
 // f / (2 pi) * 2^64, so pos * F mod 2^64 is the phase without any range
-// reduction and without loss at far positions: its top 32 bits, a signed
-// fraction of half a turn, go to sincospif.  An fp32 product pos * f would be
-// off by up to 2^-7 rad at a position of 262,144.
+// reduction: its top 32 bits, a signed fraction of half a turn, go to sincospif.
+// F is formed in pairs of doubles and is right to half its last place, 2^-34 of
+// a turn at a position of 2^31 (with a frequency in one double, 2^-24); the
+// conversion to fp32 costs 2^-26 of a turn, the cut to 32 bits 2^-32.  An fp32
+// product pos * f would be off by up to 2^-7 rad at a position of 262,144.
 //
 // A CTA takes a few rows and some of their heads.  It computes each row's sines
 // and cosines once, into shared memory (a thread that turned its own channels
@@ -175,6 +177,30 @@ cudaError_t launch_rope(RopeParams& p, bool copy_rest, cudaStream_t s) {
   return launch_pdl(rope_kernel<T, VE>, (int)grid, kThreads, smem, s, p);
 }
 
+// A sum of two doubles, some 104 bits (Dekker's arithmetic; the product's
+// remainder by fma).
+struct Twofold {
+  double hi, lo;
+};
+Twofold mul(Twofold a, Twofold b) {
+  const double p = a.hi * b.hi;
+  const double e = fma(a.hi, b.hi, -p) + (a.hi * b.lo + a.lo * b.hi);
+  const double s = p + e;
+  return {s, e - (s - p)};
+}
+
+// theta^(-1 / n): the double nearby, and one step of Newton's method for
+// r^n theta = 1, whose relative residual is formed in two doubles.
+Twofold root_of_inverse(double theta, int n) {
+  const double r = pow(theta, -1.0 / n);
+  Twofold y = {theta, 0.0}, s = {r, 0.0};
+  for (int m = n; m; m >>= 1) {
+    if (m & 1) y = mul(y, s);
+    s = mul(s, s);
+  }
+  return {r, -r * (((y.hi - 1.0) + y.lo) / n)};
+}
+
 // Every pair's frequency in turns per position, 2^64 a turn.  The last ones
 // this thread made are kept: a model's layers ask for the same ones.
 const uint64_t* turns_of(double theta, int rotary_dim) {
@@ -184,8 +210,12 @@ const uint64_t* turns_of(double theta, int rotary_dim) {
     uint64_t turn[kMaxPairs];
   } memo;
   if (memo.rotary_dim != rotary_dim || memo.theta != theta) {
-    for (int i = 0; i < rotary_dim / 2; ++i)
-      memo.turn[i] = (uint64_t)ldexp(pow(theta, -2.0 * i / rotary_dim) * 0.15915494309189533577, 64);
+    const Twofold step = root_of_inverse(theta, rotary_dim / 2);
+    Twofold f = {0x1.45f306dc9c883p-3, -0x1.6b01ec5417056p-57};  // 1 / (2 pi)
+    for (int i = 0; i < rotary_dim / 2; ++i, f = mul(f, step)) {
+      const double hi = ldexp(f.hi, 64), whole = floor(hi);
+      memo.turn[i] = (uint64_t)whole + (uint64_t)llrint((hi - whole) + ldexp(f.lo, 64));
+    }
     memo.theta = theta;
     memo.rotary_dim = rotary_dim;
   }

@@ -200,3 +200,34 @@ def test_rope_python_refusals(gpu, monkeypatch):
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)  # tensors on another device than the current one
     with pytest.raises(ValueError):
         stv.stv_rope(spec, pos, q, out)
+
+
+@pytest.mark.parametrize("theta,rd", [(1.0, 64), (1e4, 64), (1e4, 256), (5e5, 128), (1e7, 96), (1e7, 256), (1e300, 8),
+                                      (1e4, 2)])
+def test_rope_phase_of_far_positions(gpu, theta, rd):
+    """The phase at positions up to +-2^31, against frequencies formed to 70
+    digits.  Rows of (1, 0) pairs come back as (cos, sin).  The phase is off by
+    2^-26 of a turn when it is made an fp32 fraction of half a turn, 2^-32 when
+    it is cut to 32 bits and 2^-34 from the frequency (2^-65 a position): below
+    9.6e-8 rad; sine and cosine by at most 2 units of 2^-24 (1.2e-7); the
+    products by 1 and 0 are exact."""
+    from decimal import Decimal, localcontext
+
+    pos = np.concatenate([2 ** 31 - 1 - np.arange(0, 4000, 97), -2 ** 31 + np.arange(0, 4000, 89),
+                          2 ** 30 + np.arange(5), [0, 1, -1, 262143, 2 ** 24 + 1]])
+    h, n = rd // 2, pos.size
+    turns = np.empty((n, h))
+    with localcontext() as c:
+        c.prec = 70
+        two_pi = 2 * Decimal("3.14159265358979323846264338327950288419716939937510582097494459230781640628620899863")
+        for i in range(h):
+            f = Decimal(theta) ** (Decimal(-2 * i) / Decimal(rd)) / two_pi
+            turns[:, i] = [float((f * int(p)) % 1) for p in pos]
+    x = torch.zeros((n, 1, rd), device="cuda")
+    x[..., :h] = 1
+    y = torch.empty_like(x)
+    spec = stv.make_rope(rd, (h,), theta=theta)
+    stv.stv_rope(spec, torch.as_tensor(pos.astype(np.int32), device="cuda")[None], x, y)
+    got = y[:, 0].double().cpu().numpy()
+    want = np.concatenate([np.cos(2 * np.pi * turns), np.sin(2 * np.pi * turns)], 1)
+    assert np.abs(got - want).max() <= 9.6e-8 + 1.2e-7, np.abs(got - want).max()
