@@ -213,8 +213,6 @@ def head_block_bytes(group: int = GROUP) -> int:
 class LayerCache:
     """One layer's paged pool: a uint8 CUDA tensor of n_pages * page_bytes."""
 
-    _checked = None  # (address, device) of the storage that _layer_array looked over
-
     def __init__(self, pool, hkv: int, group: int = GROUP):
         import torch
 
@@ -659,16 +657,13 @@ class PagePool:
 
 
 def _layer_array(layers, dev):
-    """The layers' stv_layer_cache array, packed.  A pool's storage is looked
-    over when its address is a new one to its LayerCache."""
+    """The layers' stv_layer_cache array, packed."""
     flat = []
     for l in layers:
-        at = l.pool.data_ptr()
-        if l._checked != (at, dev):
-            if l.pool.get_device() != dev or not l.pool.is_contiguous():
-                raise ValueError(f"the layers' pools must be contiguous CUDA tensors on cuda:{dev}")
-            l._checked = (at, dev)
-        flat += (at, l.page_bytes, l.n_pages)
+        pool = l.pool
+        if pool.get_device() != dev or not pool.is_contiguous():
+            raise ValueError(f"the layers' pools must be contiguous CUDA tensors on cuda:{dev}")
+        flat += (pool.data_ptr(), l.page_bytes, l.n_pages)
     return struct.pack("@" + "Pqi4x" * len(layers), *flat)
 
 

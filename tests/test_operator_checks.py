@@ -2,9 +2,11 @@
 argument is checked before anything is enqueued, so they need no GPU.  Device
 addresses are dummies and never dereferenced."""
 import ctypes
+import struct
 
 import numpy as np
 import pytest
+import torch
 
 import opkit
 import speculative_tree_verify_bit_gb300 as stv
@@ -184,6 +186,22 @@ def test_compact_needs_its_outputs(lib):
     sh, p, lay = stv.make_shape(), pool(), layers()
     for m, n in ((None, D), (D, None)):
         assert lib.stv_page_compact(ctypes.byref(sh), lay, 2, ctypes.byref(p), m, n, D, 816, None, None) == BAD
+
+
+def test_layers_are_looked_over_in_every_call():
+    """A pool that is given another tensor at the same address between two
+    calls (CPU tensors: device -1)."""
+    storage = torch.zeros(2 * 2 * 57344, dtype=torch.uint8)
+    layer = stv.LayerCache(storage[:2 * 57344], 1)
+    want = struct.pack("@Pqi4x", storage.data_ptr(), 57344, 2)
+    assert stv._layer_array([layer], -1) == want
+    layer.pool = storage[::2]
+    with pytest.raises(ValueError):
+        stv._layer_array([layer], -1)
+    layer.pool = storage[:2 * 57344]
+    assert stv._layer_array([layer, layer], -1) == 2 * want
+    with pytest.raises(ValueError):
+        stv._layer_array([layer], 0)
 
 
 # ---------------------------------------------- the plain forms themselves --
