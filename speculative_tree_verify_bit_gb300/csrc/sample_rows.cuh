@@ -205,7 +205,7 @@ __device__ __forceinline__ int bin_of(float x, const Scale& sc) {
 
 // floor(f * m) for f in [0, 1); *exact tells whether nothing was cut off.
 __device__ __forceinline__ u64 share(float f, u64 m, bool* exact) {
-  const uint32_t b = __float_as_uint(f);
+  const uint32_t b = __float_as_uint(f) & 0x7fffffffu;  // -0 is 0
   const int e = (int)(b >> 23);
   const u64 frac = (b & 0x7fffffu) | (e ? 0x800000u : 0u);
   const int sh = 150 - max(e, 1);  // f = frac * 2^-sh, sh in [24, 149]

@@ -253,6 +253,21 @@ def test_sample_smallest_u_and_largest(gpu):
     check(x, u, rpp=4, t=[30.0])
 
 
+@pytest.mark.parametrize("v", [7, 1901, 70001])
+def test_sample_negative_zeros(gpu, v):
+    """u, top_p, min_p and T of -0 are zeros."""
+    logits, _ = rows(3, v, "fp32", seed=21)
+    u0, u1 = torch.zeros(3, device="cuda"), torch.full((3,), -0.0, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for a in (dict(), dict(k=[5]), dict(p=[0.0]), dict(t=[0.7], p=[0.9], m=[0.0]), dict(t=[0.0])):
+        neg = {key: [-x if x == 0 else x for x in val] if key != "k" else val for key, val in a.items()}
+        want, got = draw(logits, u0, rpp=3, **a), draw(logits, u1, rpp=3, status=status, **neg)
+        assert np.array_equal(want[0], got[0]) and np.array_equal(want[1], got[1])
+        check(logits, u1, rpp=3, **neg)
+    check(logits, torch.tensor([0.2, 0.6, 0.97], device="cuda"), rpp=3, p=[-0.0])
+    assert int(status.item()) == 0
+
+
 @pytest.mark.parametrize("v", [60000, 248320])
 def test_sample_long_tails(gpu, v):
     """A few heavy tokens over a wide tail: the cuts lie far down the order."""
