@@ -519,8 +519,11 @@ typedef struct {
  *  q, q_out: input and output views of the same number of heads; k, k_out
  *            likewise; either pair may be NULL.  An output may be its own
  *            input (the same data and strides: in place, channels from
- *            rotary_dim on are then not touched), or lie in other columns of
- *            the same rows; any other overlap is STV_ERR_INVALID_ARG.
+ *            rotary_dim on then keep their values), lie in other columns of
+ *            the same rows (one row stride), or in other columns of the same
+ *            heads (one head stride and one row stride: q, k and v side by
+ *            side in each head).  Any other two views whose extents meet are
+ *            STV_ERR_INVALID_ARG, where one of them is written.
  * n_rows = 0 enqueues nothing.
  */
 int stv_rope(const stv_rope_spec* spec, int dtype, int head_dim, const int32_t* pos, int n_rows, const stv_rows* q,

@@ -230,8 +230,20 @@ bool rows_ok(const stv_rows* v, int head_dim, int n_rows) {
   return n_rows <= 1 || v->row_stride >= (v->heads - 1) * v->head_stride + head_dim;
 }
 
+// Whether elements of a row of a and of one of b that starts d bytes after it
+// can meet: their extents (wa, wb) do, and they are not different columns of
+// heads with one stride.
+bool rows_may_meet(const stv_rows* a, const stv_rows* b, int64_t d, int64_t wa, int64_t wb, int head_dim, int64_t es) {
+  if (d >= wa || d + wb <= 0) return false;
+  if (a->heads == 1 && b->heads == 1) return true;
+  if (a->heads > 1 && b->heads > 1 && a->head_stride != b->head_stride) return true;
+  const int64_t st = (a->heads > 1 ? a : b)->head_stride * es, hw = head_dim * es;
+  const int64_t c = (d % st + st) % st;  // column of b's heads against a's
+  return !(c >= hw && c + hw <= st);
+}
+
 // Whether elements of two views can meet: their extents do, and they are not
-// different columns of rows with one stride.
+// different columns of rows with one stride, or in those of heads with one.
 bool may_meet(const stv_rows* a, const stv_rows* b, int head_dim, int n_rows, int64_t es) {
   const int64_t wa = ((a->heads - 1) * a->head_stride + head_dim) * es;
   const int64_t wb = ((b->heads - 1) * b->head_stride + head_dim) * es;
@@ -239,11 +251,13 @@ bool may_meet(const stv_rows* a, const stv_rows* b, int head_dim, int n_rows, in
   const uintptr_t a1 = a0 + (n_rows - 1) * a->row_stride * es + wa;
   const uintptr_t b1 = b0 + (n_rows - 1) * b->row_stride * es + wb;
   if (a1 <= b0 || b1 <= a0) return false;
-  if (n_rows == 1 || a->row_stride != b->row_stride) return true;
-  const int64_t st = a->row_stride * es;
-  int64_t d = (int64_t)(b0 - a0) % st;  // column of b's row 0 against a's
-  if (d < 0) d += st;
-  return !(d >= wa && d + wb <= st);
+  const int64_t apart = (int64_t)(b0 - a0);
+  if (n_rows == 1) return rows_may_meet(a, b, apart, wa, wb, head_dim, es);
+  if (a->row_stride != b->row_stride) return true;
+  // a row is no longer than the stride, so of b's rows only the first at or
+  // after one of a's and the one before it can reach that
+  const int64_t st = a->row_stride * es, d = (apart % st + st) % st;
+  return rows_may_meet(a, b, d, wa, wb, head_dim, es) || rows_may_meet(a, b, d - st, wa, wb, head_dim, es);
 }
 
 bool same_view(const stv_rows* a, const stv_rows* b, int n_rows) {

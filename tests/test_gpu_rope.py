@@ -86,6 +86,28 @@ def test_rope_strided_views_and_neighbours(gpu, dt):
     assert torch.equal(row[:, -8:], before[:, -8:])
 
 
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("n,heads,pad", [(1, 5, 0), (45, 6, 0), (45, 6, 24), (300, 1, 0)])
+def test_rope_heads_side_by_side(gpu, dt, n, heads, pad):
+    """q | k | v in each head: q and k turned in place; then q into v's place."""
+    hd, rd, sec = 64, 48, (8, 8, 8)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    row = torch.randn((n, heads * 3 * hd + pad), generator=g, device="cuda").to(DT[dt])
+    pos = torch.randint(0, 9000, (3, n), generator=g, device="cuda", dtype=torch.int32)
+    x = row[:, :heads * 3 * hd].unflatten(1, (heads, 3, hd))
+    q, k, v = x[:, :, 0], x[:, :, 1], x[:, :, 2]
+    q0, k0, v0, rest = q.clone(), k.clone(), v.clone(), row[:, heads * 3 * hd:].clone()
+    spec = stv.make_rope(rd, sec)
+    stv.stv_rope(spec, pos, q, q, k, k)
+    check(q, q0, pos, rd, sec, 1e4)
+    check(k, k0, pos, rd, sec, 1e4)
+    assert torch.equal(v, v0) and torch.equal(row[:, heads * 3 * hd:], rest)
+    q1, k1 = q.clone(), k.clone()
+    stv.stv_rope(spec, pos, q, v)
+    check(v, q1, pos, rd, sec, 1e4)
+    assert torch.equal(q, q1) and torch.equal(k, k1)
+
+
 def test_rope_odd_strides_take_the_narrow_path(gpu):
     n, h, hd = 12, 3, 64
     buf = torch.randn((n, h, hd + 1), device="cuda", dtype=torch.float16)

@@ -86,6 +86,16 @@ def test_rope_spec_axes_agree_with_the_plain_form(lib):
     (dict(q=rows(), qo=rows(row=2048), n=2), BAD),            # same data, other strides
     (dict(q=rows(), qo=rows(D + 1 << 30), k=rows(D + (1 << 20)), ko=rows(), n=2), BAD),  # k_out over q
     (dict(q=rows(), qo=rows(D + (1 << 20)), k=rows(D + (2 << 20)), ko=rows(D + (1 << 20)), n=2), BAD),  # q_out, k_out
+    (dict(q=rows(row=4096, head=768), qo=rows(row=4096, head=768), k=rows(D + 256, 4096, 768),
+          ko=rows(D + 256, 4096, 768), n=2), BAD),                # k's heads begin inside q's
+    (dict(q=rows(row=4096, head=768), qo=rows(row=4096, head=768), k=rows(D + 1300, 4096, 768),
+          ko=rows(D + 1300, 4096, 768), n=1), BAD),               # and end inside q's next ones
+    (dict(q=rows(row=4096, head=768), qo=rows(row=4096, head=768), k=rows(D + 512, 4096, 512),
+          ko=rows(D + 512, 4096, 512), n=2), BAD),                # head strides that differ
+    (dict(q=rows(row=4096, head=768), qo=rows(row=4096, head=768), k=rows(D + 512, 4112, 768),
+          ko=rows(D + 512, 4112, 768), n=2), BAD),                # row strides that differ
+    (dict(q=rows(row=3100, head=768), qo=rows(row=3100, head=768), k=rows(D + 2 * 2900, 3100, 256, 1),
+          ko=rows(D + 2 * 2900, 3100, 256, 1), n=3), BAD),        # k's head reaches q's next row
     (dict(q=rows(row=1 << 46), qo=rows(row=1 << 46), n=1 << 20), BAD),  # offsets past 2^48
 ])
 def test_rope_refusals(lib, kw, rc):
