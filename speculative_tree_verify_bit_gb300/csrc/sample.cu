@@ -35,10 +35,12 @@
 // bandwidth) take 21.5 us: a chain of steps of one to four microseconds with a
 // barrier after each (first pass 2.8, groups 2, second pass 4.7, merge and sort
 // 3.2, cuts and barriers 4; 41 % of the warps' time is spent waiting at
-// barriers).  512 fp32 rows (508 MB, 75 us) take 318 us: the sum of all weights
-// runs at the issue limit, 24 instructions a token (25.4 us for the 124,160
-// tokens of each of an SM's two CTAs), and the rows are read twice or three
-// times, in part from HBM.
+// barriers).  512 fp32 rows (508 MB, 75 us) take 318 us, of which no one limit
+// accounts for all: 942 MB come from HBM (139 us; L2 does not hold the rows
+// between the passes), the instructions fill 63 % of the issue slots of busy SMs
+// (166 us spread over all; the sum of all weights, 24 instructions a token in
+// the 216 rows that need it, is a fifth of them), and a quarter of the warps'
+// time goes to barriers and loads.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <math.h>
