@@ -108,6 +108,8 @@ enum stv_path { STV_PATH_EXACT = 0, STV_PATH_INT8 = 1 };
 enum stv_kv_format {
   STV_KV_BY_GROUP = 0, /* by stv_shape.group: 32 the 3-bit cache, 256 the int4 per-token-head cache */
   STV_KV_K4V2 = 2,     /* the KVarN-style cache: K 4 bits, V 2 bits, group 32 (see the notes below) */
+  STV_KV_ROWS_F16 = 4,  /* the drafter's cache: rows as they are, fp16 (group 0; see stv_kv_write) */
+  STV_KV_ROWS_BF16 = 5, /* the same in bf16 */
 };
 
 typedef struct {
@@ -662,6 +664,140 @@ int stv_page_compact(const stv_shape* shape, const stv_layer_cache* layers, int 
 int stv_page_copy(const stv_shape* shape, const stv_layer_cache* layers, int n_layers, int n_pages,
                   const int32_t* src, const int32_t* dst, int n, void* workspace, size_t ws_bytes,
                   int32_t* dev_status, stv_stream_t stream);
+
+/* ======================================================================== */
+/* The drafter's side of a round: rows of a ragged batch, a 16-bit paged     */
+/* cache, attention over it, and acceptance by probabilities.                */
+/* ======================================================================== */
+
+/*
+ * Pages and rows for a ragged batch of new tokens (prompts and single tokens
+ * in one call): what stv_page_reserve does with one length for all, and the
+ * lists that the appends and the attention take.  With s = seqs[i] and L =
+ * n_new[i], sequence s gets pages for ctx[s] + L tokens (in the order of the
+ * list, the lowest free ones; it keeps what it has), and
+ *   row_start: device int32 [n + 1]: n_new added up; row_start[0] = 0.
+ *   row_seq:   device int32 [max_rows] or NULL: the entry i of row r,
+ *              row_start[i] <= r < row_start[i + 1].
+ *   row_pos:   device int32 [max_rows] or NULL: ctx[s] + r - row_start[i].
+ *              (row_seq and row_pos as stv_kv_append_pack takes them, its
+ *              seqs being the list's.)
+ *   slots:     device int32 [max_rows] or NULL: page * 256 + row_pos % 256.
+ * Entries from row_start[n] on are -1.  ctx is not changed.
+ *  seqs: device int32 [n], distinct, or NULL: entry i is sequence i.
+ *  n_new: device int32 [n], >= 0.   ctx: device int32 [max_seqs].
+ *  max_rows: 0 .. 2^26 (else STV_ERR_SHAPE_UNSUPPORTED).
+ * All or nothing: where anything is wrong (STV_DEV_BAD_SEQ; STV_DEV_NO_PAGES;
+ * STV_DEV_BAD_ROW: a negative n_new, or more rows than max_rows) the books stay
+ * as they were, row_start is 0 and the maps are -1, so that the calls after it
+ * find no rows.  A row on a table entry outside the pool gets slot -1
+ * (STV_DEV_BAD_PAGE).  n = 0 writes row_start[0] and the maps.
+ */
+int stv_page_extend(const stv_page_pool* pool, const int32_t* seqs, int n, const int32_t* n_new, const int32_t* ctx,
+                    int32_t* row_start, int32_t* row_seq, int32_t* row_pos, int32_t* slots, int max_rows,
+                    int32_t* dev_status, stv_stream_t stream);
+
+/*
+ * The drafter's cache (stv_shape.kv_format STV_KV_ROWS_F16 or
+ * STV_KV_ROWS_BF16, group 0, head_dim 64, 128 or 256, hq = G * hkv with G <=
+ * 128, hkv <= 1,024): a page is [hkv][2][256][head_dim] elements, K and V of
+ * each KV head (page_bytes = hkv * 1024 * head_dim), hkv * n_pages < 2^22.
+ * stv_page_bytes and the page calls (fork, compact, copy) take it as well; the
+ * calls of the quantized caches return STV_ERR_SHAPE_UNSUPPORTED.
+ *
+ * stv_kv_write puts row r of k and v, hkv heads each, into slot slots[r].
+ *  k, v:  views of n_rows rows (heads = hkv), of the cache's type; any strides
+ *         (k and v may lie inside the rows of one projection).
+ *  slots: device int32 [n_rows], distinct; -1: the row is left out; any other
+ *         slot outside the pool is left out and reported (STV_DEV_BAD_PAGE).
+ */
+int stv_kv_write(const stv_shape* shape, const stv_layer_cache* layer, const stv_rows* k, const stv_rows* v,
+                 const int32_t* slots, int n_rows, int32_t* dev_status, stv_stream_t stream);
+
+/* Which keys a row sees.  The row at position P of a sequence of E = ctx + L
+ * tokens sees key k iff k < E, and k <= P or not causal, and window = 0 or
+ * k > P - window or k < sinks. */
+typedef struct {
+  int32_t window; /* 0: no window; else >= 1: the row itself and the window - 1 before it */
+  int32_t sinks;  /* >= 0: the first tokens that stay visible outside the window */
+  int32_t causal; /* 1, or 0: a block whose rows see one another (a block drafter) */
+  float scale;    /* of q . k, finite and > 0; 0 for head_dim^-1/2 */
+} stv_attn_spec;
+
+/*
+ * Attention of the new rows of n sequences over the drafter's cache, which
+ * holds them already (stv_kv_write): single tokens, blocks of drafted rows and
+ * prompts.  Entry i of the list is sequence s = seqs[i] with rows row_start[i]
+ * .. row_start[i + 1] - 1 of q and o, at positions ctx[s] and on.
+ *  pool:      tables and counts of the sequences (refs are not read).
+ *  seqs:      device int32 [n] or NULL: entry i is sequence i.   n <= 4,096.
+ *  row_start: device int32 [n + 1] (as stv_page_extend writes it), or NULL:
+ *             entry i has row i alone, n_rows >= n.
+ *  max_new:   at least the rows of any entry (host): picks the kernel.  Up to
+ *             16 rows of Q per KV head (max_new * G <= 16) keys are split over
+ *             all SMs and mma.sync does the products; past that, tiles of 128 rows
+ *             on the tensor cores of tcgen05, split in the same way.
+ *  q, o:      views of n_rows rows (heads = hq), of the cache's type; no
+ *             element of o in q or in the cache; rows from row_start[n] on
+ *             are left as they were.
+ *  workspace: device, 16-byte aligned, at least
+ *             stv_paged_attn_workspace_bytes(...) bytes; need not be cleared.
+ *             Calls that overlap on the GPU need one each.
+ * Scores and softmax are formed in fp32, P is rounded to the cache's type for
+ * P . V (sums in fp32), o rounded once.  The split depends on the lengths
+ * alone and partials are joined in order: the result is the same every time.
+ * Keys that no row of a tile sees are not read, or have no effect whatever
+ * they hold: pages that lie outside window and first tokens may have been
+ * given up (their table entries are not looked at).  Keys of a page past
+ * counts[s], or on a table entry outside the pool, are left out
+ * (STV_DEV_BAD_PAGE); a row without keys is zero.  An entry whose rows are not
+ * within [0, n_rows) in ascending order, or are more than max_new, is left
+ * out (STV_DEV_BAD_ROW), as is one whose sequence is not in the pool or whose
+ * ctx is negative or past 2^30 (STV_DEV_BAD_SEQ).
+ */
+int stv_paged_attn_workspace_bytes(const stv_shape* shape, int max_new, size_t* bytes);
+int stv_paged_attn(const stv_shape* shape, const stv_attn_spec* spec, const stv_layer_cache* layer,
+                   const stv_page_pool* pool, const int32_t* seqs, int n, const int32_t* ctx,
+                   const int32_t* row_start, int max_new, const stv_rows* q, const stv_rows* o, int n_rows,
+                   void* workspace, size_t ws_bytes, int32_t* dev_status, stv_stream_t stream);
+
+/*
+ * Verification of drafted tokens against the target's probabilities (the
+ * sampled counterpart of stv_tree_accept; what is committed is distributed as
+ * the target's own sampling).  At a node with target row p and draft row q,
+ * from R = p, Z = 1, S = q, its children c are tried in index order, x being
+ * draft_ids[c]:
+ *     c is accepted iff  u[c] Z S(x) < R(x); the walk goes on at c;
+ *     else R(y) = max(R(y) - Z S(y), 0) for every y and Z = sum R (both stay
+ *     as they were if nothing would be left), and
+ *       STV_DRAFTS_REPLACED: S stays (children drawn independently),
+ *       STV_DRAFTS_DISTINCT: S(x) = 0 and S is divided by its sum (children
+ *       drawn without replacement; 0 if nothing is left of it).
+ * At a node without an accepted child the round's last token is the first x
+ * whose running sum of R, in index order, exceeds u[0] times the whole.
+ * q = NULL: drafts without a distribution (looked up, or a drafter's
+ * argmax): S is 1 at x and 0 elsewhere, for each child its own.
+ *  parent, draft_ids: device int32 [n_seqs][T], parent as in stv_tree_accept;
+ *            a node whose id is outside [0, vocab) is not there.
+ *  p, q:     device, dtype (enum stv_dtype), row of node i of sequence s at p
+ *            + (s T + i) * p_stride elements: the target's, and the draft's
+ *            that i's children were drawn from, probabilities in [0, 1], used as
+ *            they are.  Strides >= vocab, any alignment of the type.
+ *  u:        device fp32 [n_seqs][T], in [0, 1).
+ *  n_commit, path, out_ids: as stv_tree_accept writes them; stv_kv_commit takes
+ *            them.
+ * R and its sums are 64-bit integers in units of 2^-56, so the result does not
+ * depend on the order of threads; u Z S(x) < R(x) is decided in 64 bits.
+ * A sequence with a bad tree gets n_commit 0 and -1 (STV_DEV_BAD_TREE); so does
+ * one whose walk reads a probability outside [0, 1] or NaN, a u outside
+ * [0, 1), or a node's row without any mass (STV_DEV_BAD_SAMPLE).
+ * 1 <= T <= 32, 1 <= vocab <= 524,288; n_seqs = 0 enqueues nothing.
+ */
+enum stv_drafts { STV_DRAFTS_REPLACED = 0, STV_DRAFTS_DISTINCT = 1 };
+int stv_tree_accept_probs(const int32_t* parent, const int32_t* draft_ids, const void* p, int64_t p_stride,
+                          const void* q, int64_t q_stride, int dtype, int vocab, int drafts, const float* u,
+                          int t_nodes, int n_seqs, int32_t* n_commit, int32_t* path, int32_t* out_ids,
+                          int32_t* dev_status, stv_stream_t stream);
 
 #ifdef __cplusplus
 }

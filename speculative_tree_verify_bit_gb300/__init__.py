@@ -34,6 +34,8 @@ STV_DEV_BAD_SEQ = 128
 
 STV_KV_BY_GROUP = 0  # group 32: the 3-bit cache; group 256: the int4 per-token-head cache
 STV_KV_K4V2 = 2      # the K 4 / V 2-bit cache (group 32)
+STV_KV_ROWS_F16 = 4  # the drafter's cache: rows as they are (group 0)
+STV_KV_ROWS_BF16 = 5
 
 STV_PATH_EXACT = 0
 STV_PATH_INT8 = 1
@@ -55,7 +57,8 @@ EXPORTS = (
     "stv_prefill_workspace_bytes", "stv_prefill_attn", "stv_verify_attn_timeout_test",
     "stv_prefill_attn_timeout_test", "stv_append_verify_combine", "stv_rope", "stv_sample",
     "stv_page_workspace_bytes", "stv_page_reserve", "stv_page_fork", "stv_page_free", "stv_page_compact",
-    "stv_page_copy",
+    "stv_page_copy", "stv_page_extend", "stv_kv_write", "stv_paged_attn_workspace_bytes", "stv_paged_attn",
+    "stv_tree_accept_probs",
 )
 
 
@@ -90,6 +93,11 @@ class stv_rope_spec(ctypes.Structure):
 class stv_rows(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("row_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
                 ("heads", ctypes.c_int32)]
+
+
+class stv_attn_spec(ctypes.Structure):
+    _fields_ = [("window", ctypes.c_int32), ("sinks", ctypes.c_int32), ("causal", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
 
 
 class stv_page_pool(ctypes.Structure):
@@ -160,6 +168,16 @@ def load() -> ctypes.CDLL:
         lib.stv_page_compact.argtypes = [P, P, I, P, P, P, P, ctypes.c_size_t, P, P]
         lib.stv_page_copy.restype = I
         lib.stv_page_copy.argtypes = [P, P, I, I, P, P, I, P, ctypes.c_size_t, P, P]
+        lib.stv_page_extend.restype = I
+        lib.stv_page_extend.argtypes = [P, P, I, P, P, P, P, P, P, I, P, P]
+        lib.stv_kv_write.restype = I
+        lib.stv_kv_write.argtypes = [P, P, P, P, P, I, P, P]
+        lib.stv_paged_attn_workspace_bytes.restype = I
+        lib.stv_paged_attn_workspace_bytes.argtypes = [P, I, P]
+        lib.stv_paged_attn.restype = I
+        lib.stv_paged_attn.argtypes = [P, P, P, P, P, I, P, P, I, P, P, I, P, ctypes.c_size_t, P, P]
+        lib.stv_tree_accept_probs.restype = I
+        lib.stv_tree_accept_probs.argtypes = [P, P, P, I64, P, I64, I, I, I, P, I, I, P, P, P, P, P]
         _lib = lib
     return _lib
 
@@ -734,3 +752,158 @@ def stv_page_copy(shape, layers, src, dst, workspace, dev_status=None, stream=No
         workspace.nbytes, _raw(dev_status, i32, dev, "dev_status"), _raw_stream(stream, dev))
     if rc:
         raise StvError("stv_page_copy", rc)
+
+
+# --------------------------------------------------------------------------
+# the drafter's side of a round: rows of a ragged batch, a 16-bit paged cache,
+# attention over it, acceptance by probabilities
+# --------------------------------------------------------------------------
+
+def make_row_shape(hq: int, hkv: int, head_dim: int, dtype) -> stv_shape:
+    """The drafter's cache: fp16 or bf16 rows of hkv heads of 64, 128 or 256 channels."""
+    torch = _t()
+    formats = {torch.float16: STV_KV_ROWS_F16, torch.bfloat16: STV_KV_ROWS_BF16}
+    if dtype not in formats:
+        raise TypeError(f"the cache's rows must be fp16 or bf16, got {dtype}")
+    return stv_shape(int(hq), int(hkv), int(head_dim), 0, PAGE_TOKENS, formats[dtype])
+
+
+class RowCache:
+    """One layer's pool of the drafter's cache: a contiguous CUDA tensor
+    [n_pages][hkv][2][256][head_dim] of fp16 or bf16 (K, then V, of each head).
+    The page calls take it in the place of a LayerCache."""
+
+    def __init__(self, pool):
+        torch = _t()
+        if not isinstance(pool, torch.Tensor) or pool.dim() != 5 or pool.shape[2] != 2 or pool.shape[3] != PAGE_TOKENS:
+            raise ValueError("the pool must be [n_pages][hkv][2][256][head_dim]")
+        if pool.dtype not in (torch.float16, torch.bfloat16):
+            raise TypeError(f"the pool must be fp16 or bf16, got {pool.dtype}")
+        self.pool = pool
+        self.n_pages, self.hkv, _, _, self.head_dim = pool.shape
+        self.page_bytes = self.hkv * 4 * PAGE_TOKENS * self.head_dim
+
+    @classmethod
+    def empty(cls, n_pages: int, hkv: int, head_dim: int, dtype, device="cuda"):
+        return cls(_t().zeros((n_pages, hkv, 2, PAGE_TOKENS, head_dim), dtype=dtype, device=device))
+
+    def c(self) -> stv_layer_cache:
+        return stv_layer_cache(_ptr(self.pool, name="pool").value, self.page_bytes, self.n_pages)
+
+
+def _row_cache(shape, layer, dev):
+    """The layer as the calls take it, and its type; the tensor must be what the shape says."""
+    pool, fmt = layer.pool, shape.kv_format
+    if not isinstance(pool, _torch.Tensor) or pool.get_device() != dev or not pool.is_contiguous():
+        raise ValueError(f"the layer's pool must be a contiguous CUDA tensor on cuda:{dev}")
+    if layer.hkv != shape.hkv or layer.head_dim != shape.head_dim:
+        raise ValueError(f"the shape has {shape.hkv} heads of {shape.head_dim}, the pool {layer.hkv} of {layer.head_dim}")
+    dt = pool.dtype
+    if fmt != (STV_KV_ROWS_F16 if dt == _torch.float16 else STV_KV_ROWS_BF16 if dt == _torch.bfloat16 else -1):
+        raise TypeError(f"the shape's cache format is {fmt}, the pool holds {dt}")
+    return struct.pack("@Pqi4x", pool.data_ptr(), layer.page_bytes, layer.n_pages), dt
+
+
+def make_attn(window: int = 0, sinks: int = 0, causal: bool = True, scale: float = 0.0) -> stv_attn_spec:
+    """Which keys a row sees (include/stv.h): window 0: all before it; sinks:
+    first tokens that stay visible; causal False: the rows of a block see one
+    another; scale 0: head_dim ** -0.5."""
+    return stv_attn_spec(int(window), int(sinks), int(bool(causal)), float(scale))
+
+
+def stv_page_extend(pool: PagePool, seqs, n_new, ctx, row_start, row_seq=None, row_pos=None, slots=None,
+                    dev_status=None, stream=None):
+    """Pages for n_new[i] more tokens of sequence seqs[i] (None: sequence i),
+    and the rows' places: row_start int32 [n + 1]; row_seq, row_pos and slots
+    int32 [max_rows], each or None (include/stv.h)."""
+    dev, i32 = pool._on_current(), _torch.int32
+    n = n_new.numel()
+    first = next((t for t in (row_seq, row_pos, slots) if t is not None), None)
+    rows = first.numel() if first is not None else 1 << 26
+    rc = load().stv_page_extend(
+        pool._ref, _raw(seqs, i32, dev, "seqs", n), n, _raw(n_new, i32, dev, "n_new"),
+        _raw(ctx, i32, dev, "ctx", pool._c.max_seqs), _raw(row_start, i32, dev, "row_start", n + 1),
+        _raw(row_seq, i32, dev, "row_seq", rows), _raw(row_pos, i32, dev, "row_pos", rows),
+        _raw(slots, i32, dev, "slots", rows), rows, _raw(dev_status, i32, dev, "dev_status"),
+        _raw_stream(stream, dev))
+    if rc:
+        raise StvError("stv_page_extend", rc)
+
+
+def stv_kv_write(shape, layer: RowCache, k, v, slots, dev_status=None, stream=None):
+    """Rows k, v [n_rows][hkv][head_dim] (any row and head strides) into the
+    cache at slots, int32 [n_rows] (-1: left out)."""
+    _t()
+    dev = _device_of(k, "k")
+    lc, dt = _row_cache(shape, layer, dev)
+    n, hd = slots.numel(), shape.head_dim
+    rc = load().stv_kv_write(
+        ctypes.byref(shape), lc, _rows(k, n, hd, dt, dev, "k"), _rows(v, n, hd, dt, dev, "v"),
+        _raw(slots, _torch.int32, dev, "slots"), n, _raw(dev_status, _torch.int32, dev, "dev_status"),
+        _raw_stream(stream, dev))
+    if rc:
+        raise StvError("stv_kv_write", rc)
+
+
+def stv_paged_attn_workspace_bytes(shape, max_new: int) -> int:
+    out = ctypes.c_size_t()
+    _check("stv_paged_attn_workspace_bytes", load().stv_paged_attn_workspace_bytes(
+        ctypes.byref(shape), int(max_new), ctypes.byref(out)))
+    return out.value
+
+
+def stv_paged_attn(shape, spec: stv_attn_spec, layer: RowCache, pool: PagePool, seqs, ctx, row_start, max_new: int, q,
+                   o, workspace, dev_status=None, stream=None):
+    """Attention of the new rows of n sequences over the drafter's cache.  q, o
+    [n_rows][hq][head_dim] (any row and head strides); entry i is sequence
+    seqs[i] (None: sequence i) with the rows row_start[i] .. row_start[i + 1] - 1
+    (int32 [n + 1]; None: one row each) at positions ctx[s] and on; no entry has
+    more than max_new rows (include/stv.h)."""
+    i32 = _t().int32
+    dev = pool._on_current()
+    lc, dt = _row_cache(shape, layer, dev)
+    n_rows, hd = q.shape[0], shape.head_dim
+    n = row_start.numel() - 1 if row_start is not None else seqs.numel() if seqs is not None else n_rows
+    rc = load().stv_paged_attn(
+        ctypes.byref(shape), ctypes.byref(spec), lc, pool._ref, _raw(seqs, i32, dev, "seqs", n), n,
+        _raw(ctx, i32, dev, "ctx", pool._c.max_seqs), _raw(row_start, i32, dev, "row_start"), int(max_new),
+        _rows(q, n_rows, hd, dt, dev, "q"), _rows(o, n_rows, hd, dt, dev, "o"), n_rows,
+        _raw(workspace, None, dev, "workspace"), workspace.nbytes, _raw(dev_status, i32, dev, "dev_status"),
+        _raw_stream(stream, dev))
+    if rc:
+        raise StvError("stv_paged_attn", rc)
+
+
+def stv_tree_accept_probs(parent, draft_ids, p, q, u, n_commit, path, out_ids, distinct: bool = False,
+                          dev_status=None, stream=None):
+    """Verification of drafted tokens against the target's probabilities:
+    parent, draft_ids int32 [n_seqs][T]; p and q [n_seqs * T][vocab] (fp32,
+    fp16 or bf16, rows any distance apart; q None: drafts without a
+    distribution); u fp32 [n_seqs][T]; distinct: a node's children were drawn
+    without replacement (include/stv.h)."""
+    torch = _t()
+    dev = _device_of(p, "p")
+    if parent.dim() != 2:
+        raise ValueError("parent must be [n_seqs][T]")
+    n, t = parent.shape
+    m = n * t
+    if p.dim() != 2 or p.shape[0] != m or (p.shape[1] > 1 and p.stride(1) != 1):
+        raise ValueError(f"p must be [{m}][vocab] with adjacent columns")
+    vocab, q_at, q_stride = p.shape[1], None, 0
+    if q is not None:
+        if not isinstance(q, torch.Tensor) or q.get_device() != dev:
+            raise ValueError(f"q must be a CUDA tensor on cuda:{dev}")
+        if q.dtype != p.dtype:
+            raise TypeError(f"q must be {p.dtype} as p is, got {q.dtype}")
+        if tuple(q.shape) != (m, vocab) or (vocab > 1 and q.stride(1) != 1):
+            raise ValueError(f"q must be [{m}][{vocab}] with adjacent columns")
+        q_at, q_stride = q.data_ptr(), q.stride(0) if m > 1 else vocab
+    i32 = torch.int32
+    rc = load().stv_tree_accept_probs(
+        _raw(parent, i32, dev, "parent"), _raw(draft_ids, i32, dev, "draft_ids", m), p.data_ptr(),
+        p.stride(0) if m > 1 else vocab, q_at, q_stride, _dtype_code(p.dtype, "p"), vocab, 1 if distinct else 0,
+        _raw(u, torch.float32, dev, "u", m), t, n, _raw(n_commit, i32, dev, "n_commit", n),
+        _raw(path, i32, dev, "path", m), _raw(out_ids, i32, dev, "out_ids", m),
+        _raw(dev_status, i32, dev, "dev_status"), _raw_stream(stream, dev))
+    if rc:
+        raise StvError("stv_tree_accept_probs", rc)

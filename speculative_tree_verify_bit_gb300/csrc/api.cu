@@ -38,6 +38,35 @@ int check_layer(const stv_layer_cache* l, const ShapeInfo& sh) {
   return STV_OK;
 }
 
+int check_row_shape(const stv_shape* sh, RowShape* out) {
+  if (!sh) return STV_ERR_INVALID_ARG;
+  if (!is_row_shape(sh) || sh->group != 0 || sh->page_tokens != kPageTok) return STV_ERR_SHAPE_UNSUPPORTED;
+  if (sh->head_dim != 64 && sh->head_dim != 128 && sh->head_dim != 256) return STV_ERR_SHAPE_UNSUPPORTED;
+  if (sh->hkv < 1 || sh->hkv > 1024 || sh->hq < sh->hkv || sh->hq % sh->hkv != 0 || sh->hq / sh->hkv > kMaxRows)
+    return STV_ERR_SHAPE_UNSUPPORTED;
+  out->hq = sh->hq;
+  out->hkv = sh->hkv;
+  out->G = sh->hq / sh->hkv;
+  out->hd = sh->head_dim;
+  out->bf16 = sh->kv_format == STV_KV_ROWS_BF16;
+  out->page_bytes = (int64_t)sh->hkv * 4 * kPageTok * sh->head_dim;
+  return STV_OK;
+}
+
+int check_row_layer(const stv_layer_cache* l, const RowShape& sh) {
+  if (!l || !l->pool || l->n_pages < 1 || (uintptr_t)l->pool % 16) return STV_ERR_INVALID_ARG;
+  if (l->page_bytes != sh.page_bytes || (int64_t)l->n_pages * sh.hkv >= 1 << 22) return STV_ERR_SHAPE_UNSUPPORTED;
+  return STV_OK;
+}
+
+bool rows_view_ok(const stv_rows* v, int head_dim, int n_rows) {
+  if (!v->data || v->heads < 1 || v->heads > 1 << 17 || v->head_stride < head_dim) return false;
+  // an extent of at most 2^50 bytes, so that no offset overflows
+  if (v->head_stride > ((int64_t)1 << 48) / v->heads || (n_rows > 1 && v->row_stride > ((int64_t)1 << 48) / n_rows))
+    return false;
+  return n_rows <= 1 || v->row_stride >= (v->heads - 1) * v->head_stride + head_dim;
+}
+
 // need_keys < 0: only the table pointer is checked (append: positions are on
 // the device); otherwise ctx + need_keys must fit in the sequence's pages.
 static int check_seqs(const stv_seq* seqs, int n_seqs, int need_keys) {
@@ -294,6 +323,13 @@ const char* stv_status_string(int status) {
 int stv_version(void) { return 3; }
 
 int stv_page_bytes(const stv_shape* shape, int64_t* bytes) {
+  if (is_row_shape(shape)) {
+    RowShape rs;
+    if (int rc = check_row_shape(shape, &rs)) return rc;
+    if (!bytes) return STV_ERR_INVALID_ARG;
+    *bytes = rs.page_bytes;
+    return STV_OK;
+  }
   int rc = check_shape(shape, -1, nullptr);
   if (rc) return rc;
   if (!bytes) return STV_ERR_INVALID_ARG;

@@ -1,0 +1,391 @@
+// paged_attn.cuh -- what the two kernels of stv_paged_attn share: parameters,
+// the cut of the work into equal shares, and the walk over a share.
+//
+// Work.  A unit is (entry, tokens_per consecutive new tokens of it, KV head):
+// at most 16 or 128 (256) rows of Q that read the same keys.  Its keys come in
+// tiles of 64: those of the first tokens (sinks) that lie before the window's
+// first tile, then the window's (or all up to the last visible key).  All tiles
+// of all units, in the order (entry, unit, head, tile), are cut into as many
+// equal runs as there are CTAs.  A unit inside one CTA's run is finished there;
+// a unit cut by the runs' borders leaves partials (O, and the running maximum and
+// sum of each row), at most two per CTA, which the join kernel puts together in
+// the runs' order.  So every CTA has the same number of tiles whatever the
+// lengths, a single long sequence is spread over all SMs, and the result
+// depends on the lengths alone.
+//
+// The lengths are on the device: each CTA works its own run out (a scan over the
+// entries, one over the units), which costs about as much as one dependent load
+// and saves a launch.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+
+#include "stv_device.cuh"
+#include "tc_util.cuh"
+
+namespace stv {
+
+constexpr int kAttnTile = 64;       // keys
+constexpr int kMaxEntries = 4096;
+constexpr int kMaxCtx = 1 << 30;
+constexpr int kSmallRows = 16;      // rows of Q per unit, single tokens
+constexpr int kJoinRows = 4;        // rows per block of the join kernel
+
+// A unit cut by the runs' borders: written by the CTA whose run it begins in.
+struct JoinRecord {
+  int row0, rows, h, last_cta;
+};
+
+struct AttnParams {
+  CUtensorMap map;  // the pool as [hd / 64][rows][64], 64 x 64 x (hd / 64) boxes
+  const void* q;
+  void* o;
+  int64_t q_row, q_head, o_row, o_head;  // strides in elements
+  const int32_t* tables;
+  const int32_t* counts;
+  int table_stride, max_seqs, n_pages;
+  const int32_t* seqs;
+  const int32_t* ctx;
+  const int32_t* row_start;
+  int n, n_rows, max_new;
+  int hkv, G;
+  int tokens_per;  // new tokens of a unit
+  int window, sinks, causal;
+  float scale2;  // scale * log2(e)
+  bool q_wide, o_wide;  // 16-byte loads of q, stores of o
+  // workspace
+  float* part;       // [2 * CTAs][part_rows][hd]
+  float2* ml;        // [2 * CTAs][part_rows]
+  JoinRecord* rec;   // [CTAs]
+  int part_rows;
+  int32_t* status;
+};
+
+namespace {
+
+struct Entry {
+  int s, ctx, L, row0;
+  int keys;  // tokens of its pages
+};
+
+// Entry i, with no rows where anything about it is wrong.
+__device__ __forceinline__ Entry entry_of(const AttnParams& p, int i) {
+  Entry e;
+  e.s = p.seqs ? __ldg(p.seqs + i) : i;
+  int r1;
+  if (p.row_start) {
+    e.row0 = __ldg(p.row_start + i);
+    r1 = __ldg(p.row_start + i + 1);
+  } else {
+    e.row0 = i;
+    r1 = i + 1;
+  }
+  e.L = e.ctx = e.keys = 0;
+  if (e.row0 < 0 || r1 < e.row0 || r1 > p.n_rows || r1 - e.row0 > p.max_new) {
+    report(p.status, STV_DEV_BAD_ROW);
+    return e;
+  }
+  if (e.s < 0 || e.s >= p.max_seqs) {
+    report(p.status, STV_DEV_BAD_SEQ);
+    return e;
+  }
+  e.ctx = __ldg(p.ctx + e.s);
+  if (e.ctx < 0 || e.ctx > kMaxCtx) {
+    report(p.status, STV_DEV_BAD_SEQ);
+    return e;
+  }
+  e.L = r1 - e.row0;
+  const int have = min(__ldg(p.counts + e.s), p.table_stride);
+  e.keys = max(0, min(have, kMaxCtx / kPageTok * 2 - 1)) * kPageTok;
+  if (e.L && e.ctx + e.L > e.keys) report(p.status, STV_DEV_BAD_PAGE);
+  return e;
+}
+
+// Unit u of an entry.
+struct AttnUnit {
+  int pos0, ntok, end;  // position of its first token, tokens, keys of the sequence that have a page
+  int hi, lo;           // keys some row sees: [lo, hi), and those before `sinks`
+  int n_sink, wt0;      // tiles of the first tokens; first tile of the window
+  int n_tiles;
+};
+
+__device__ __forceinline__ AttnUnit unit_of(const AttnParams& p, const Entry& e, int u) {
+  AttnUnit x;
+  x.pos0 = e.ctx + u * p.tokens_per;
+  x.ntok = min(p.tokens_per, e.L - u * p.tokens_per);
+  x.end = min(e.ctx + e.L, e.keys);
+  x.hi = p.causal ? min(x.pos0 + x.ntok, x.end) : x.end;
+  x.lo = p.window ? max(0, x.pos0 - p.window + 1) : 0;
+  x.wt0 = x.lo / kAttnTile;
+  const int up_to = (x.hi + kAttnTile - 1) / kAttnTile;
+  x.n_sink = p.window && p.sinks ? min((p.sinks - 1) / kAttnTile + 1, min(x.wt0, up_to)) : 0;
+  x.n_tiles = max(1, max(0, up_to - x.wt0) + x.n_sink);  // one tile at least: it writes the rows
+  return x;
+}
+// First key of its t-th tile.
+__device__ __forceinline__ int tile_key(const AttnUnit& x, int t) {
+  return (t < x.n_sink ? t : x.wt0 + t - x.n_sink) * kAttnTile;
+}
+// Whether some row may not see some key of the tile.
+__device__ __forceinline__ bool tile_edge(const AttnParams& p, const AttnUnit& x, int key0) {
+  const int last = key0 + kAttnTile - 1;
+  if (last >= x.end || (p.causal && last > x.pos0)) return true;
+  return p.window && key0 <= x.pos0 + x.ntok - 1 - p.window && last >= p.sinks;
+}
+// The keys of a tile (bit k: key0 + k) that the row at position pos sees.
+__device__ __forceinline__ uint64_t low_bits(int n) { return n >= 64 ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1; }
+__device__ __forceinline__ uint64_t row_sees(const AttnParams& p, int pos, int end, int key0) {
+  uint64_t m = low_bits((p.causal ? min(pos + 1, end) : end) - key0);
+  if (p.window) m &= ~low_bits(pos - p.window + 1 - key0) | low_bits(p.sinks - key0);
+  return m;
+}
+// Those that some row of the unit sees.
+__device__ __forceinline__ uint64_t unit_sees(const AttnParams& p, const AttnUnit& x, int key0) {
+  uint64_t m = low_bits(x.hi - key0);
+  if (p.window) m &= ~low_bits(x.lo - key0) | low_bits(p.sinks - key0);
+  return m;
+}
+
+// Exclusive scan of x over the CTA's kThreads threads; *total gets the sum.
+template <int kThreads>
+__device__ __forceinline__ long long cta_scan(long long x, long long* total) {
+  __shared__ long long warp_sum[kThreads / 32];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  long long incl = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  __syncthreads();  // warp_sum may still be read from a scan before
+  if (lane == 31) warp_sum[w] = incl;
+  __syncthreads();
+  long long before = 0, all = 0;
+#pragma unroll
+  for (int i = 0; i < kThreads / 32; ++i) {
+    if (i < w) before += warp_sum[i];
+    all += warp_sum[i];
+  }
+  *total = all;
+  return before + incl - x;
+}
+
+// Where a CTA's run begins, and its length in tiles.
+struct RunStart {
+  int e, u, h, t;         // entry, unit, head, tile
+  long long left, share;  // tiles of the run, of a full run
+};
+
+// Whole CTA; scratch: n + 1 ints of shared memory, free afterwards.  Ends with
+// a barrier.
+template <int kThreads>
+__device__ __forceinline__ RunStart run_of(const AttnParams& p, int* scratch) {
+  __shared__ RunStart start;
+  const int tid = threadIdx.x;
+  // units of the entries before
+  const int per = (p.n + kThreads - 1) / kThreads;
+  const int e0 = min(tid * per, p.n), e1 = min(e0 + per, p.n);
+  int mine = 0;
+  for (int e = e0; e < e1; ++e) {
+    const int nu = (entry_of(p, e).L + p.tokens_per - 1) / p.tokens_per;
+    scratch[e] = nu;
+    mine += nu;
+  }
+  long long all;
+  int at = (int)cta_scan<kThreads>(mine, &all);
+  const int n_units = (int)all;
+  for (int e = e0; e < e1; ++e) {
+    const int nu = scratch[e];
+    scratch[e] = at;
+    at += nu;
+  }
+  if (tid == 0) {
+    scratch[p.n] = n_units;
+    start.left = 0;
+    start.share = 1;
+  }
+  __syncthreads();
+  // tiles of the units of this thread's stretch
+  const int uper = (n_units + kThreads - 1) / kThreads;
+  const int g0 = min(tid * uper, n_units), g1 = min(g0 + uper, n_units);
+  int first = 0;  // the entry of unit g0
+  {
+    int lo = 0, hi = p.n;  // scratch[lo] <= g0 < scratch[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (scratch[mid] <= g0) lo = mid; else hi = mid;
+    }
+    first = lo;
+  }
+  long long tiles = 0;
+  auto walk = [&](auto&& f) {
+    int e = first;
+    Entry en = {};
+    bool have = false;
+    for (int g = g0; g < g1; ++g) {
+      while (scratch[e + 1] <= g) {
+        ++e;
+        have = false;
+      }
+      if (!have) {
+        en = entry_of(p, e);
+        have = true;
+      }
+      if (!f(e, g - scratch[e], unit_of(p, en, g - scratch[e]).n_tiles)) return;
+    }
+  };
+  walk([&](int, int, int n) {
+    tiles += n;
+    return true;
+  });
+  long long total;
+  const long long before = cta_scan<kThreads>(tiles, &total) * p.hkv;
+  total *= p.hkv;
+  const long long share = (total + gridDim.x - 1) / gridDim.x;
+  const long long f0 = share * blockIdx.x;
+  if (f0 < total && before <= f0 && f0 < before + tiles * p.hkv) {
+    long long f = before;
+    walk([&](int e, int u, int n) {
+      if (f0 < f + (long long)n * p.hkv) {
+        start.e = e;
+        start.u = u;
+        start.h = (int)((f0 - f) / n);
+        start.t = (int)((f0 - f) % n);
+        start.left = min(share, total - f0);
+        start.share = share;
+        return false;
+      }
+      f += (long long)n * p.hkv;
+      return true;
+    });
+  }
+  __syncthreads();
+  return start;
+}
+
+// Walks a run, one unit's part after the other.
+struct RunWalk {
+  const AttnParams& p;
+  RunStart at;
+  Entry en;
+  AttnUnit x;
+  int t0, t1;  // tiles of this part
+  bool any;
+
+  __device__ RunWalk(const AttnParams& p_, const RunStart& s) : p(p_), at(s), any(s.left > 0) {
+    if (any) {
+      en = entry_of(p, at.e);
+      open();
+    }
+  }
+  __device__ void open() {
+    x = unit_of(p, en, at.u);
+    t0 = at.t;
+    t1 = (int)min((long long)x.n_tiles, t0 + at.left);
+  }
+  // The workspace slot of this part's partials; -1: the unit is whole.
+  __device__ int slot() const {
+    const int b = 2 * (int)blockIdx.x;
+    return t0 ? b : t1 < x.n_tiles ? b + 1 : -1;
+  }
+  // The last CTA that has tiles of this unit, for a unit that begins here and
+  // does not end here.
+  __device__ int last_cta() const {
+    const int rest = x.n_tiles - t1;  // in runs after this one
+    return (int)(blockIdx.x + (rest + at.share - 1) / at.share);
+  }
+  __device__ bool next() {
+    at.left -= t1 - t0;
+    at.t = 0;
+    if (at.left <= 0) return any = false;
+    if (++at.h == p.hkv) {
+      at.h = 0;
+      if (++at.u * p.tokens_per >= en.L) {
+        at.u = 0;
+        do {
+          if (++at.e >= p.n) return any = false;
+          en = entry_of(p, at.e);
+        } while (en.L == 0);
+      }
+    }
+    open();
+    return true;
+  }
+};
+
+// Row of the map (a key's row of K; V's is 256 further) of the tile at key0, or
+// -1 where the sequence has no page there.
+__device__ __forceinline__ int tile_row(const AttnParams& p, int s, int h, int key0) {
+  const int lp = key0 / kPageTok;
+  const int have = min(__ldg(p.counts + s), p.table_stride);
+  const int page = lp < have ? __ldg(p.tables + (int64_t)s * p.table_stride + lp) : -1;
+  if (page < 0 || page >= p.n_pages) {
+    report(p.status, STV_DEV_BAD_PAGE);
+    return -1;
+  }
+  return (page * p.hkv + h) * (2 * kPageTok) + key0 % kPageTok;
+}
+
+__device__ __forceinline__ void tma_tile(void* dst, const CUtensorMap* map, int row, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+          su32(dst)),
+      "l"(map), "r"(0), "r"(row), "r"(0), "r"(su32(bar))
+      : "memory");
+}
+
+template <typename T>
+struct Pack;
+template <>
+struct Pack<__half> {
+  static __device__ __forceinline__ uint32_t two(float a, float b) {
+    __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<uint32_t*>(&h);
+  }
+  static __device__ __forceinline__ float2 floats(uint32_t v) { return __half22float2(*reinterpret_cast<__half2*>(&v)); }
+};
+template <>
+struct Pack<__nv_bfloat16> {
+  static __device__ __forceinline__ uint32_t two(float a, float b) {
+    __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<uint32_t*>(&h);
+  }
+  static __device__ __forceinline__ float2 floats(uint32_t v) {
+    return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+  }
+};
+
+enum TileFlags { kFirst = 1, kLast = 2, kEdge = 4, kAbsent = 8, kStop = 16 };
+
+// A tile as the producer hands it to the other warps.
+struct TileInfo {
+  int flags, key0;
+  int row0, rows, h, slot;  // the unit's first row of q, its rows of Q, KV head, workspace slot or -1
+  AttnUnit x;
+};
+
+// n (2, 4 or 8) adjacent outputs, as wide as o allows.
+template <typename T, int n>
+__device__ __forceinline__ void store_out(T* dst, const float* v, bool wide) {
+  uint32_t w[n / 2];
+#pragma unroll
+  for (int i = 0; i < n / 2; ++i) w[i] = Pack<T>::two(v[2 * i], v[2 * i + 1]);
+  if (wide) {
+    if constexpr (n == 8) *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+    else if constexpr (n == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+    else *reinterpret_cast<uint32_t*>(dst) = w[0];
+  } else {
+#pragma unroll
+    for (int i = 0; i < n; ++i) reinterpret_cast<uint16_t*>(dst)[i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
+  }
+}
+
+}  // namespace
+
+// Launchers (cudaError_t of the launch); grid: CTAs, as the workspace was cut.
+cudaError_t launch_attn_small(const AttnParams& p, int hd, bool bf16, int grid, cudaStream_t s);  // paged_attn.cu
+// paged_attn_tc.cu; q_tiles: tiles of 128 rows per unit (1 or 2)
+cudaError_t launch_attn_tiles(const AttnParams& p, int hd, bool bf16, int q_tiles, int grid, cudaStream_t s);
+
+}  // namespace stv

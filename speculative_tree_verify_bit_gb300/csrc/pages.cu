@@ -1,5 +1,5 @@
-// pages.cu -- the pages of the caches: reserve, fork, free, compact and copy
-// (include/stv.h, stv_page_*).
+// pages.cu -- the pages of the caches: reserve, extend, fork, free, compact and
+// copy (include/stv.h, stv_page_*).
 //
 // The books (refs, tables, counts) live on the device and one CTA changes
 // them: it checks the whole call first, so that a call with anything wrong
@@ -39,6 +39,11 @@ struct BookParams {
   int2* list;         // workspace: (source, destination)
   int32_t* map;
   int32_t* n_live;
+  // extend
+  const int32_t* n_new;
+  int32_t* row_start;
+  int32_t* maps[3];  // row_seq, row_pos, slots
+  int max_rows, map_rows;  // map_rows: 0 where no map is asked for
   int32_t* status;
 };
 
@@ -219,6 +224,112 @@ __global__ void __launch_bounds__(kBookThreads) page_reserve_kernel(const __grid
   __syncthreads();  // counts were read above
   for (int i = threadIdx.x; i < p.n; i += kBookThreads)
     if (off[i + 1] > off[i]) pool.counts[p.seqs[i]] += off[i + 1] - off[i];
+}
+
+// Rows [r0, r1) of extend's maps.  start is row_start (n + 1 entries).
+__device__ __forceinline__ void write_rows(const BookParams& p, const int* start, int r0, int r1, int step) {
+  const stv_page_pool& pool = p.pool;
+  const int total = start[p.n];
+  for (int r = r0; r < r1; r += step) {
+    int i = -1, pos = -1, slot = -1;
+    if (r < total) {
+      i = last_at_most([&](int k) { return start[k]; }, p.n, r);
+      const int s = p.seqs ? __ldg(p.seqs + i) : i;
+      pos = __ldg(p.ctx + s) + (r - start[i]);
+      if (p.maps[2]) {
+        const int page = pool.tables[(int64_t)s * pool.table_stride + pos / kPageTok];
+        if (page >= 0 && page < pool.n_pages) slot = page * kPageTok + pos % kPageTok;
+        else report(p.status, STV_DEV_BAD_PAGE);
+      }
+    }
+    if (p.maps[0]) p.maps[0][r] = i;
+    if (p.maps[1]) p.maps[1][r] = pos;
+    if (p.maps[2]) p.maps[2][r] = slot;
+  }
+}
+
+// Pages for n_new[i] more tokens of each sequence, and the rows' maps where one
+// CTA writes them (kRows).
+template <bool kRows>
+__global__ void __launch_bounds__(kBookThreads) page_extend_kernel(const __grid_constant__ BookParams p) {
+  extern __shared__ int smem[];
+  __shared__ uint32_t named[kMaxPoolSeqs / 32];
+  __shared__ unsigned long long all_rows;
+  int* off = smem;             // [n + 1]: new pages of the entries before
+  int* start = off + p.n + 1;  // [n + 1]: rows of the entries before
+  if (threadIdx.x < kMaxPoolSeqs / 32) named[threadIdx.x] = 0;
+  if (threadIdx.x == 0) all_rows = 0;
+  __syncthreads();
+  grid_dep_wait();
+  grid_dep_launch();
+  const stv_page_pool& pool = p.pool;
+  int bad = 0;
+  unsigned long long mine = 0;
+  for (int i = threadIdx.x; i < p.n; i += kBookThreads) {
+    const int s = p.seqs ? p.seqs[i] : i, more = p.n_new[i];
+    off[i] = start[i] = 0;
+    if (s < 0 || s >= pool.max_seqs || mark(named, s)) {
+      bad |= STV_DEV_BAD_SEQ;
+      continue;
+    }
+    if (more < 0) {
+      bad |= STV_DEV_BAD_ROW;
+      continue;
+    }
+    const int have = pool.counts[s], c = p.ctx[s];
+    const int64_t need = ((int64_t)c + more + kPageTok - 1) / kPageTok;
+    if (have < 0 || c < 0 || have > pool.table_stride || need > pool.table_stride)
+      bad |= STV_DEV_BAD_SEQ;
+    else if (need > have)
+      off[i] = (int)min(need - have, (int64_t)pool.n_pages + 1);
+    start[i] = more;
+    mine += (unsigned)more;
+  }
+  if (mine) atomicAdd(&all_rows, mine);
+  __syncthreads();
+  if (all_rows > (unsigned long long)p.max_rows) bad |= STV_DEV_BAD_ROW;
+  bool fails = call_fails(bad, p.status);
+  LiveMap lm;
+  int total = 0;
+  if (!fails) {
+    scan_array(off, p.n);
+    scan_array(start, p.n);
+    total = off[p.n];
+    if (total) {
+      lm.build(start + p.n + 1, pool.refs, pool.n_pages);
+      fails = call_fails(total > pool.n_pages - lm.live() ? STV_DEV_NO_PAGES : 0, p.status);
+    }
+  }
+  if (fails) {
+    __syncthreads();
+    for (int i = threadIdx.x; i <= p.n; i += kBookThreads) start[i] = 0;
+    total = 0;
+  }
+  for (int r = threadIdx.x; r < total; r += kBookThreads) {
+    const int page = lm.free_page(r);
+    const int i = last_at_most([&](int k) { return off[k]; }, p.n, r);
+    const int s = p.seqs ? p.seqs[i] : i;
+    pool.tables[(int64_t)s * pool.table_stride + pool.counts[s] + (r - off[i])] = page;
+    pool.refs[page] = 1;
+  }
+  __syncthreads();  // counts were read above, and the tables are read below
+  for (int i = threadIdx.x; i <= p.n; i += kBookThreads) {
+    p.row_start[i] = start[i];
+    if (total && i < p.n && off[i + 1] > off[i]) pool.counts[p.seqs ? p.seqs[i] : i] += off[i + 1] - off[i];
+  }
+  if (kRows) write_rows(p, start, threadIdx.x, p.map_rows, kBookThreads);
+}
+
+// The maps of many rows: a CTA writes kRowsPerCta of each.
+constexpr int kRowsPerCta = 1024;
+__global__ void __launch_bounds__(kCopyThreads) page_rows_kernel(const __grid_constant__ BookParams p) {
+  extern __shared__ int start[];
+  grid_dep_wait();
+  grid_dep_launch();
+  for (int i = threadIdx.x; i <= p.n; i += kCopyThreads) start[i] = p.row_start[i];
+  __syncthreads();
+  const int r0 = blockIdx.x * kRowsPerCta;
+  write_rows(p, start, r0 + threadIdx.x, min(p.map_rows, r0 + kRowsPerCta), kCopyThreads);
 }
 
 __global__ void __launch_bounds__(kBookThreads) page_free_kernel(const __grid_constant__ BookParams p) {
@@ -457,6 +568,9 @@ int check_pool(const stv_page_pool* pool) {
   return STV_OK;
 }
 
+constexpr int kMaxRowsOfCall = 1 << 26;
+constexpr int kRowsInOneCta = 4096;
+
 size_t workspace_need(int n_pages) { return kListOffset + (size_t)n_pages * sizeof(int2); }
 
 int check_workspace(void* workspace, size_t ws_bytes, int n_pages) {
@@ -472,12 +586,14 @@ void set_workspace(BookParams* b, void* workspace) {
 // The layers' pools as the copy kernel takes them; every pool holds n_pages.
 int fill_copy(const stv_shape* shape, const stv_layer_cache* layers, int n_layers, int n_pages, CopyParams* c) {
   ShapeInfo sh;
-  int rc = check_shape(shape, -1, &sh);
+  RowShape rs;
+  const bool rows = is_row_shape(shape);
+  int rc = rows ? check_row_shape(shape, &rs) : check_shape(shape, -1, &sh);
   if (rc) return rc;
   if (!layers || n_layers < 1 || n_layers > kMaxLayers) return STV_ERR_INVALID_ARG;
   memset(c, 0, sizeof(*c));
   for (int l = 0; l < n_layers; ++l) {
-    if ((rc = check_layer(&layers[l], sh))) return rc;
+    if ((rc = rows ? check_row_layer(&layers[l], rs) : check_layer(&layers[l], sh))) return rc;
     if (layers[l].n_pages < n_pages || (uintptr_t)layers[l].pool % 16) return STV_ERR_INVALID_ARG;
     c->pools[l] = layers[l].pool;
   }
@@ -557,6 +673,37 @@ int stv_page_reserve(const stv_page_pool* pool, const int32_t* seqs, int n, cons
   b.status = dev_status;
   const size_t smem = (size_t)(n + 1) * 4 + LiveMap::bytes(pool->n_pages);
   return launch_book(page_reserve_kernel, smem, b, (cudaStream_t)stream) == cudaSuccess ? STV_OK : STV_ERR_CUDA;
+}
+
+int stv_page_extend(const stv_page_pool* pool, const int32_t* seqs, int n, const int32_t* n_new, const int32_t* ctx,
+                    int32_t* row_start, int32_t* row_seq, int32_t* row_pos, int32_t* slots, int max_rows,
+                    int32_t* dev_status, stv_stream_t stream) {
+  if (int rc = check_pool(pool)) return rc;
+  if (n < 0 || n > pool->max_seqs || max_rows < 0 || !row_start || (n > 0 && (!n_new || !ctx)))
+    return STV_ERR_INVALID_ARG;
+  if (max_rows > kMaxRowsOfCall) return STV_ERR_SHAPE_UNSUPPORTED;
+  BookParams b;
+  memset(&b, 0, sizeof(b));
+  b.pool = *pool;
+  b.seqs = seqs;
+  b.ctx = const_cast<int32_t*>(ctx);
+  b.n = n;
+  b.n_new = n_new;
+  b.row_start = row_start;
+  b.maps[0] = row_seq;
+  b.maps[1] = row_pos;
+  b.maps[2] = slots;
+  b.max_rows = max_rows;
+  b.map_rows = row_seq || row_pos || slots ? max_rows : 0;
+  b.status = dev_status;
+  cudaStream_t st = (cudaStream_t)stream;
+  const size_t smem = (size_t)(n + 1) * 8 + LiveMap::bytes(pool->n_pages);
+  if (b.map_rows <= kRowsInOneCta)
+    return launch_book(page_extend_kernel<true>, smem, b, st) == cudaSuccess ? STV_OK : STV_ERR_CUDA;
+  if (launch_book(page_extend_kernel<false>, smem, b, st) != cudaSuccess) return STV_ERR_CUDA;
+  const int grid = (max_rows + kRowsPerCta - 1) / kRowsPerCta;
+  return launch_pdl(page_rows_kernel, grid, kCopyThreads, (size_t)(n + 1) * 4, st, b) == cudaSuccess ? STV_OK
+                                                                                                     : STV_ERR_CUDA;
 }
 
 int stv_page_free(const stv_page_pool* pool, const int32_t* seqs, int n, int32_t* dev_status, stv_stream_t stream) {

@@ -254,6 +254,19 @@ cudaError_t launch_pdl_coop(void (*kernel)(KArgs...), int grid, int block, size_
 // ---- host helpers (api.cu) ----
 int check_shape(const stv_shape* sh, int t_nodes, ShapeInfo* out);  // t_nodes < 0: no round
 int check_layer(const stv_layer_cache* l, const ShapeInfo& sh);
+// The drafter's 16-bit cache (STV_KV_ROWS_*).
+struct RowShape {
+  int hq, hkv, G, hd;
+  bool bf16;
+  int64_t page_bytes;
+};
+inline bool is_row_shape(const stv_shape* sh) {
+  return sh && (sh->kv_format == STV_KV_ROWS_F16 || sh->kv_format == STV_KV_ROWS_BF16);
+}
+int check_row_shape(const stv_shape* sh, RowShape* out);
+int check_row_layer(const stv_layer_cache* l, const RowShape& sh);
+// A view of rows of heads whose extents fit (api.cu).
+bool rows_view_ok(const stv_rows* v, int head_dim, int n_rows);
 int device_sm_count(int* n);
 int make_plan(const ShapeInfo& sh, const stv_seq* seqs, int n_seqs, int sm_count, Plan* plan, bool balance);
 WsLayout ws_layout(const ShapeInfo& sh, int n_seqs, const Plan& plan);
