@@ -786,11 +786,12 @@ int stv_paged_attn(const stv_shape* shape, const stv_attn_spec* spec, const stv_
  *  u:        device fp32 [n_seqs][T], in [0, 1).
  *  n_commit, path, out_ids: as stv_tree_accept writes them; stv_kv_commit takes
  *            them.
- * R and its sums are 64-bit integers in units of 2^-56, so the result does not
- * depend on the order of threads; u Z S(x) < R(x) is decided in 64 bits.
+ * R and its sums are 64-bit integers in units of 2^-60, so the result does not
+ * depend on the order of threads; u Z S(x) < R(x) is decided in 64 bits.  Z S(y)
+ * is off by less than 2^-46 of itself from the second rejection at a node on.
  * A sequence with a bad tree gets n_commit 0 and -1 (STV_DEV_BAD_TREE); so does
  * one whose walk reads a probability outside [0, 1] or NaN, a u outside
- * [0, 1), or a node's row without any mass (STV_DEV_BAD_SAMPLE).
+ * [0, 1), or a row that adds up to nothing or to 4 or more (STV_DEV_BAD_SAMPLE).
  * 1 <= T <= 32, 1 <= vocab <= 524,288; n_seqs = 0 enqueues nothing.
  */
 enum stv_drafts { STV_DRAFTS_REPLACED = 0, STV_DRAFTS_DISTINCT = 1 };

@@ -6,15 +6,22 @@
 // once, the target's and the draft's probability of i's token at i's parent:
 // the walk down the tree then needs no memory as long as drafts are accepted.
 // A rejection changes the node's whole row, R <- max(R - Z S, 0), and needs Z =
-// sum R: one pass over the vocabulary, split over the cluster's warps.  R is
-// not stored: after k rejections at a node it is computed again from p, q and
-// the k factors.  The last token comes from the same sums, kept per warp: the
-// CTA whose range holds it reads one warp's share again with all its threads.
+// sum R: one pass over the vocabulary, split over the cluster's warps.  Since
+// max(max(p - a, 0) - b, 0) = max(p - a - b, 0), the row after any number of
+// rejections is max(p - F q, 0) with one factor F, the sum of Z / sum S over
+// them: R is not stored, and a pass costs the same however many there were.
+// Tokens taken out of S (distinct) or of R (certain) are few and are put right
+// apart; without draft rows one pass per node gives every Z.  The last token
+// comes from the same sums, kept per warp: the CTA whose range holds it reads one
+// warp's share again with all its threads.
 //
-// R, Z and the running sums are integers in units of 2^-56 (an entry of at
-// least 2^-32 in fp32 is exact), so nothing depends on the order of threads.
-// The sums saturate at 64 instead of wrapping: rows of more mass than that are
-// refused.  Every CTA takes every decision from the same numbers.
+// R, Z and the running sums are integers in units of 2^-60, so nothing depends on
+// the order of threads.  A number becomes one in three steps of fp32 additions
+// (x + 2 leaves the first 22 bits in the sum's last places, and so on), whose bits
+// are added up in 32-bit registers: conversions to 64-bit integers run at the rate
+// of the fp64 units, 2 a clock and SM.  F q is a product of fp32 pairs, off by less than
+// 2^-46 of itself.  The sums saturate at 4 instead of wrapping: rows of more mass
+// than that are refused.  Every CTA takes every decision from the same numbers.
 //
 // Bounds: the launch, two dependent loads, a pass, two cluster barriers and the
 // second reading, one after the other, for few sequences; HBM for many.
@@ -34,10 +41,10 @@ namespace cg = cooperative_groups;
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 16;
 constexpr int kMaxVocab = 524288;
-constexpr uint64_t kFull = 1ull << 62;  // 64 in units of 2^-56
-constexpr float kUnit = 72057594037927936.f;  // 2^56
+constexpr uint64_t kFull = 1ull << 62;  // 4 in units of 2^-60
+constexpr double kOne = 1.0 / (1ull << 60);
 enum Drafts { kReplaced = 0, kDistinct = 1, kCertain = 2 };
 
 struct AcceptParams {
@@ -54,73 +61,83 @@ struct AcceptParams {
   int32_t* status;
 };
 
-// What a node's rejected children do to its row.
-struct Steps {
-  int k;             // rejections that count
-  int n_gone;        // tokens taken out of S (distinct) or R (certain)
-  uint64_t mul[kMaxT];  // Z over the sum of S (set_factor)
-  int shift[kMaxT];
-  int gone_before[kMaxT];
+// What a node's rejected children did to its row: max(p - F q, 0), F = f.x + f.y,
+// but for the tokens taken out, whose R is kept here.
+struct Rest {
+  float2 f;
+  int n_gone;
   int gone[kMaxT];
+  float gone_p[kMaxT], gone_q[kMaxT];
+  uint64_t gone_r[kMaxT];
 };
 
 __device__ __forceinline__ float to_f(float x) { return x; }
 __device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
 __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ uint64_t fixed(float x) { return __float2ull_rn(x * kUnit); }
 __device__ __forceinline__ bool is_prob(float x) { return x >= 0.f && x <= 1.f; }
 __device__ __forceinline__ uint64_t sat_add(uint64_t a, uint64_t b) { return min(a + b, kFull); }
 
-// f > 0 as mul / 2^64 * 2^e with mul's top bit set: s f = (s 2^6 mul / 2^64) / 2^(6 - e).
-__device__ __forceinline__ void set_factor(Steps& st, int j, double f) {
-  if (!(f > 0)) {
-    st.mul[j] = 0;
-    st.shift[j] = 6;
-    return;
-  }
-  int e;
-  const double fr = frexp(f, &e);
-  st.mul[j] = (uint64_t)(fr * 9007199254740992.0) << 11;  // 2^53, then 2^64
-  st.shift[j] = 6 - e;
+// A number in [0, 2) as h 2^-22 + l 2^-44 + s 2^-60, rounded to 2^-60; sums and
+// differences of a few of them stay in 32 bits.
+struct Parts {
+  int h, l, s;
+};
+__device__ __forceinline__ Parts parts_of(float x) {
+  const float t = x + 2.f, r = x - (t - 2.f);          // r exact, at most 2^-23
+  const float t2 = fmaf(r, 4194304.f, 3.f);            // 2^22 r
+  const float r2 = fmaf(t2 - 3.f, -2.384185791015625e-7f, r);  // exact, at most 2^-45
+  const float t3 = fmaf(r2, 274877906944.f, 3.f);      // 2^38 r2
+  return {__float_as_int(t) - 0x40000000, __float_as_int(t2) - 0x40400000, __float_as_int(t3) - 0x40400000};
 }
-__device__ __forceinline__ uint64_t times(uint64_t s, uint64_t mul, int shift) {
-  const uint64_t x = __umul64hi(s << 6, mul);
-  return shift >= 0 ? (shift < 64 ? x >> shift : 0) : x << min(-shift, 63);
+__device__ __forceinline__ uint64_t whole(const Parts& x) {
+  return (uint64_t)(((long long)x.h << 38) + ((long long)x.l << 16) + x.s);
 }
-
-// R of token y after the node's steps.
-template <int kDrafts>
-__device__ __forceinline__ uint64_t rest_of(float p, float q, int y, const Steps& st, int k) {
-  uint64_t r = fixed(p);
-  if constexpr (kDrafts == kCertain) {
-    for (int j = 0; j < k; ++j)
-      if (st.gone[st.gone_before[j]] == y) r = 0;
-  } else {
-    const uint64_t s0 = fixed(q);
-    for (int j = 0; j < k; ++j) {
-      uint64_t s = s0;
-      if constexpr (kDrafts == kDistinct)
-        for (int i = 0; i < st.gone_before[j]; ++i)
-          if (st.gone[i] == y) s = 0;
-      const uint64_t x = times(s, st.mul[j], st.shift[j]);
-      r = r > x ? r - x : 0;
-    }
-  }
-  return r;
+__device__ __forceinline__ uint64_t fixed(float x) { return whole(parts_of(x)); }
+__device__ __forceinline__ void add_to(Parts& a, const Parts& x) {
+  a.h += x.h;
+  a.l += x.l;
+  a.s += x.s;
 }
 
-// VE entries of a row from entry e on; zeros outside [0, vocab).
-template <typename T, int VE>
-__device__ __forceinline__ void load_entries(const T* row, int e, int vocab, bool wide, float (&x)[VE]) {
-  if (wide && e >= 0 && e + VE <= vocab) {
-    const uint4 v = __ldg(reinterpret_cast<const uint4*>(row + e));
-    const T* t = reinterpret_cast<const T*>(&v);
+// max(p - q, 0)
+__device__ __forceinline__ Parts above(float p, float q) {
+  const Parts a = parts_of(p), b = parts_of(q);
+  if (!(p > q)) return {0, 0, 0};
+  return {a.h - b.h, a.l - b.l, a.s - b.s};
+}
+// max(p - F q, 0).  F q = x + w, w at most 2^-23 x: (p - x) - w has the sign of the
+// difference, since p - x is exact where w could matter.
+__device__ __forceinline__ Parts above(float p, float q, float2 f) {
+  const float x = q * f.x, w = fmaf(q, f.y, fmaf(q, f.x, -x));
+  const Parts a = parts_of(p), b = parts_of(x);
+  const float t2 = fmaf(w, 4194304.f, 3.f), r2 = fmaf(t2 - 3.f, -2.384185791015625e-7f, w);
+  const float t3 = fmaf(r2, 274877906944.f, 3.f);
+  if (!((p - x) - w > 0.f)) return {0, 0, 0};
+  return {a.h - b.h, a.l - b.l - (__float_as_int(t2) - 0x40400000), a.s - b.s - (__float_as_int(t3) - 0x40400000)};
+}
+__device__ __forceinline__ uint64_t rest_of(float p, float q, float2 f) {
+  return f.x == 0.f ? fixed(p) : whole(above(p, q, f));
+}
+__device__ __forceinline__ float2 pair_of(double f) {
+  const float x = (float)f;
+  return make_float2(x, (float)(f - (double)x));
+}
+
+// VE entries of a row from entry e on, as they lie; zeros outside [0, vocab).
+template <typename T>
+__device__ __forceinline__ uint4 load_entries(const T* row, int e, int vocab, bool wide) {
+  constexpr int VE = 16 / (int)sizeof(T);
+  if (wide && e >= 0 && e + VE <= vocab) return __ldg(reinterpret_cast<const uint4*>(row + e));
+  uint4 v = make_uint4(0, 0, 0, 0);
+  T* t = reinterpret_cast<T*>(&v);
 #pragma unroll
-    for (int i = 0; i < VE; ++i) x[i] = to_f(t[i]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < VE; ++i) x[i] = e + i >= 0 && e + i < vocab ? to_f(row[e + i]) : 0.f;
-  }
+  for (int i = 0; i < VE; ++i)
+    if (e + i >= 0 && e + i < vocab) t[i] = row[e + i];
+  return v;
+}
+template <typename T>
+__device__ __forceinline__ float entry(const uint4& v, int i) {
+  return to_f(reinterpret_cast<const T*>(&v)[i]);
 }
 
 struct Share {
@@ -129,11 +146,11 @@ struct Share {
 };
 
 template <typename T, int kDrafts>
-__global__ void __launch_bounds__(kThreads) accept_probs_kernel(const __grid_constant__ AcceptParams p) {
+__global__ void __launch_bounds__(kThreads, 2) accept_probs_kernel(const __grid_constant__ AcceptParams p) {
   constexpr int VE = 16 / (int)sizeof(T);
   __shared__ int par[kMaxT], id[kMaxT], way[kMaxT];
   __shared__ float uu[kMaxT], pp[kMaxT], qq[kMaxT];
-  __shared__ Steps st;
+  __shared__ Rest st;
   __shared__ uint64_t warp_sum[kWarps], warp_draft[kWarps];
   __shared__ int warp_bad[kWarps];
   __shared__ Share share[2][kMaxCluster];
@@ -166,101 +183,124 @@ __global__ void __launch_bounds__(kThreads) accept_probs_kernel(const __grid_con
     else qq[tid] = 1.f;
     if (tid == 0) {
       bad_bits = any ? STV_DEV_BAD_TREE : 0;
-      st.k = st.n_gone = 0;
+      st.f = make_float2(0.f, 0.f);
+      st.n_gone = 0;
       node = 0;
     }
   }
   __syncthreads();
   cluster.barrier_wait(std::move(started));
 
-  // Thread 0's place in the walk.  z: Z (1 until a rejection counts); known:
-  // the warps' sums are those of R as it is now.
+  // Thread 0's place in the walk.  z: Z (1 until a rejection counts); factor: F;
+  // known: the warps' sums are those of the row as it is now, but for the tokens
+  // taken out (certain: of p).
   int c = 1, depth = 0, pass = 0;
-  double z = 1.0, draft_mass = 1.0;
+  double z = 1.0, factor = 0.0, before_f = 0.0, draft_mass = 1.0;
   uint64_t draft_all = 0;
   bool pending = false, known = false;
-  uint64_t total = 0;
+  uint64_t total = 0, left = 0;  // the last pass's sum; with the tokens taken out
   int v_per = 0;
   const T* prow = p_rows;
   const T* qrow = q_rows;
   int pre = 0;
   bool p_wide = false, q_wide = false;
+  // What the tokens taken out add to the sums (modulo 2^64).
+  auto gone_adds = [&]() {
+    uint64_t x = 0;
+    for (int i = 0; i < st.n_gone; ++i)
+      x += st.gone_r[i] - rest_of(st.gone_p[i], st.gone_q[i], st.f);
+    return x;
+  };
+  auto place_of = [&](int x) {
+    for (int i = 0; i < st.n_gone; ++i)
+      if (st.gone[i] == x) return i;
+    return -1;
+  };
 
   for (;;) {
     if (tid == 0) {
       way[0] = 0;
-      if (pending) {  // the sum after a rejection
-        const int j = st.k - 1;
-        if (total == 0) {
-          --st.k;  // nothing left: R and Z stay
-          known = false;
-        } else {
-          z = (double)total * (1.0 / 72057594037927936.0);
-          known = true;
-        }
-        if constexpr (kDrafts != kReplaced) {
-          const int x = id[c];
-          bool seen = false;
-          for (int i = 0; i < st.n_gone; ++i) seen |= st.gone[i] == x;
-          if constexpr (kDrafts == kDistinct) {
-            if (j == 0 && st.n_gone == 0) draft_all = share[pass & 1][0].draft;
-            if (!seen) {
-              const uint64_t out = fixed(qq[c]);
-              draft_all = draft_all > out ? draft_all - out : 0;
-            }
-            draft_mass = (double)draft_all * (1.0 / 72057594037927936.0);
-            if (!seen) st.gone[st.n_gone++] = x;
-          } else {
-            st.n_gone = st.k;  // the token of each rejection that counts, in turn
-          }
-        }
-        pending = false;
-        ++c;
-      }
       cmd = 0;
       while (!cmd && !bad_bits) {
+        if (pending) {  // a rejected child, and the sum after it (certain: of p)
+          const int x = id[c], at = place_of(x);
+          if constexpr (kDrafts == kCertain) {
+            const uint64_t px = fixed(pp[c]);
+            left = total + gone_adds();
+            if (at < 0 && left > px) {  // else nothing would be left
+              st.gone[st.n_gone] = x;
+              st.gone_p[st.n_gone] = pp[c];
+              st.gone_r[st.n_gone++] = 0;
+              left -= px;
+            }
+            if (st.n_gone) z = (double)left * kOne;
+          } else {
+            const uint64_t sum = total + gone_adds();
+            if (sum == 0) {  // nothing left: R and Z stay
+              factor = before_f;
+              st.f = pair_of(factor);
+              known = false;
+            } else {
+              z = (double)sum * kOne;
+              left = sum;
+              known = true;
+            }
+            if constexpr (kDrafts == kDistinct) {
+              if (st.n_gone == 0) draft_all = share[pass & 1][0].draft;
+              if (at < 0) {
+                const uint64_t qx = fixed(qq[c]);
+                draft_all = draft_all > qx ? draft_all - qx : 0;
+                st.gone[st.n_gone] = x;
+                st.gone_p[st.n_gone] = pp[c];
+                st.gone_q[st.n_gone] = qq[c];
+                st.gone_r[st.n_gone++] = rest_of(pp[c], qq[c], st.f);
+              }
+              draft_mass = (double)draft_all * kOne;
+            }
+          }
+          pending = false;
+          ++c;
+        }
         while (c < T_ && par[c] != node) ++c;
-        if (c >= T_) {
-          cmd = known ? 2 : 1;  // the last token: from the sums that there are, or a pass first
+        if (c >= T_) {  // the last token: from the sums that there are, or a pass first
+          cmd = known ? 2 : 1;
           known = true;
           break;
         }
-        const int x = id[c];
         if (!is_prob(pp[c]) || !is_prob(qq[c]) || !(uu[c] >= 0.f && uu[c] < 1.f)) {
           bad_bits = STV_DEV_BAD_SAMPLE;
           break;
         }
-        double share_d = qq[c];  // S(x)
-        if constexpr (kDrafts == kDistinct) {
-          for (int i = 0; i < st.n_gone; ++i)
-            if (st.gone[i] == x) share_d = 0;
-          if (st.n_gone) share_d = draft_mass > 0 ? share_d / draft_mass : 0;
-        }
-        const double r = st.k ? (double)rest_of<kDrafts>(pp[c], qq[c], x, st, st.k) * (1.0 / 72057594037927936.0)
-                              : (double)pp[c];
-        if ((double)uu[c] * share_d * z < r) {  // accepted
+        const int at = place_of(id[c]);
+        double s_x = qq[c], r_x = pp[c];  // S(x), R(x)
+        if constexpr (kDrafts == kDistinct)
+          if (st.n_gone) s_x = at < 0 && draft_mass > 0 ? s_x / draft_mass : 0;
+        if (at >= 0) r_x = (double)st.gone_r[at] * kOne;
+        else if (kDrafts != kCertain && factor > 0) r_x = (double)rest_of(pp[c], qq[c], st.f) * kOne;
+        if ((double)uu[c] * s_x * z < r_x) {  // accepted
           node = c;
           way[++depth] = c;
-          st.k = st.n_gone = 0;
+          st.n_gone = 0;
           z = draft_mass = 1.0;
+          factor = 0;
+          st.f = make_float2(0.f, 0.f);
           known = false;
           ++c;
           continue;
         }
-        const int j = st.k++;
+        pending = true;
         if constexpr (kDrafts == kCertain) {
-          st.gone[j] = x;
-          st.gone_before[j] = j;
+          cmd = known ? 0 : 1;
+          known = true;
         } else {
-          st.gone_before[j] = st.n_gone;
+          before_f = factor;
           double f = z;
           if constexpr (kDrafts == kDistinct)
             if (st.n_gone) f = draft_mass > 0 ? z / draft_mass : 0;
-          set_factor(st, j, f);
+          factor += f;
+          st.f = pair_of(factor);
+          cmd = 1;
         }
-        pending = true;
-        known = false;
-        cmd = 1;
       }
     }
     __syncthreads();
@@ -276,44 +316,62 @@ __global__ void __launch_bounds__(kThreads) accept_probs_kernel(const __grid_con
     const int n_vec = (V + pre + VE - 1) / VE;
     v_per = (n_vec + C * kWarps - 1) / (C * kWarps);
     const int v0 = (rank * kWarps + w) * v_per, v1 = min(n_vec, v0 + v_per);
-    const int k = st.k;
-    const bool plain = kDrafts != kCertain && k == 1 && st.mul[0] == 1ull << 63 && st.shift[0] == 5;
+    const float2 f = st.f;
+    const bool none = f.x == 0.f, plain = f.x == 1.f && f.y == 0.f;
     uint64_t sum = 0, draft = 0;
     bool bad = false;
-#pragma unroll 4
-    for (int v = v0 + lane; v < v1; v += 32) {
-      float a[VE], b[VE];
-      const int e = v * VE - pre;
-      load_entries<T, VE>(prow, e, V, p_wide, a);
-      if constexpr (kDrafts != kCertain) {
-        if (k || kDrafts == kDistinct) load_entries<T, VE>(qrow, e, V, q_wide, b);
-      }
-      uint64_t part = 0, part_q = 0;
+    constexpr int U = kDrafts == kCertain ? 4 : 2;  // vectors in flight
+    constexpr uint32_t kOneBits = 0x3f800000u;
+    for (int v = v0 + lane; v < v1; v += 32 * U) {
+      uint4 a[U], b[U];
 #pragma unroll
-      for (int i = 0; i < VE; ++i) {
-        bad |= !is_prob(a[i]);
-        if constexpr (kDrafts != kCertain) {
-          if (k || kDrafts == kDistinct) bad |= !is_prob(b[i]);
-        }
+      for (int j = 0; j < U; ++j) {
+        const bool in = v + 32 * j < v1;
+        const int e = in ? (v + 32 * j) * VE - pre : V;  // V: zeros
+        a[j] = load_entries(prow, e, V, p_wide);
+        if constexpr (kDrafts != kCertain)
+          if (!none) b[j] = load_entries(qrow, e, V, q_wide);
       }
-      if (!bad) {
-        if (k == 0) {
+      uint32_t most = 0;  // of the entries' bits: above 1's, they are looked at again
+      Parts part = {0, 0, 0}, part_q = {0, 0, 0};
 #pragma unroll
-          for (int i = 0; i < VE; ++i) part += fixed(a[i]);
+      for (int j = 0; j < U; ++j) {
+        if (kDrafts == kCertain || none) {
+#pragma unroll
+          for (int i = 0; i < VE; ++i) {
+            const float x = entry<T>(a[j], i);
+            most = max(most, __float_as_uint(x));
+            add_to(part, parts_of(x));
+          }
         } else if (plain) {
 #pragma unroll
           for (int i = 0; i < VE; ++i) {
-            const uint64_t x = fixed(a[i]), y = fixed(b[i]);
-            part += x > y ? x - y : 0;
-            if constexpr (kDrafts == kDistinct) part_q += y;
+            const float x = entry<T>(a[j], i), y = entry<T>(b[j], i);
+            most = max(most, max(__float_as_uint(x), __float_as_uint(y)));
+            add_to(part, above(x, y));
+            if constexpr (kDrafts == kDistinct) add_to(part_q, parts_of(y));
           }
         } else {
 #pragma unroll
-          for (int i = 0; i < VE; ++i) part += rest_of<kDrafts>(a[i], kDrafts == kCertain ? 0.f : b[i], e + i, st, k);
+          for (int i = 0; i < VE; ++i) {
+            const float x = entry<T>(a[j], i), y = entry<T>(b[j], i);
+            most = max(most, max(__float_as_uint(x), __float_as_uint(y)));
+            add_to(part, above(x, y, f));
+          }
         }
       }
-      sum = sat_add(sum, part);
-      if constexpr (kDrafts == kDistinct) draft = sat_add(draft, part_q);
+      sum = sat_add(sum, whole(part));
+      if constexpr (kDrafts == kDistinct) draft = sat_add(draft, whole(part_q));
+      if (most > kOneBits) {  // -0 is a probability
+#pragma unroll
+        for (int j = 0; j < U; ++j)
+#pragma unroll
+          for (int i = 0; i < VE; ++i) {
+            bad |= !is_prob(entry<T>(a[j], i));
+            if constexpr (kDrafts != kCertain)
+              if (!none) bad |= !is_prob(entry<T>(b[j], i));
+          }
+      }
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
@@ -332,7 +390,7 @@ __global__ void __launch_bounds__(kThreads) accept_probs_kernel(const __grid_con
       Share mine = {lane < kWarps ? warp_sum[lane] : 0, lane < kWarps ? warp_draft[lane] : 0,
                     lane < kWarps ? warp_bad[lane] : 0};
 #pragma unroll
-      for (int o = 8; o; o >>= 1) {
+      for (int o = kWarps / 2; o; o >>= 1) {
         mine.sum = sat_add(mine.sum, __shfl_xor_sync(0xffffffffu, mine.sum, o));
         mine.draft = sat_add(mine.draft, __shfl_xor_sync(0xffffffffu, mine.draft, o));
         mine.bad |= __shfl_xor_sync(0xffffffffu, mine.bad, o);
@@ -351,7 +409,7 @@ __global__ void __launch_bounds__(kThreads) accept_probs_kernel(const __grid_con
         found |= x.bad;
       }
       share[pass & 1][0].draft = all;
-      if (found || total >= kFull || all >= kFull || (!pending && total == 0) || !(uu[0] >= 0.f && uu[0] < 1.f))
+      if (found || total >= kFull || all >= kFull || ((kDrafts == kCertain || !pending) && total + gone_adds() == 0) || !(uu[0] >= 0.f && uu[0] < 1.f))
         bad_bits = STV_DEV_BAD_SAMPLE;
     }
     // (thread 0's next decisions are behind this loop's first barrier; it alone reads what it wrote)
@@ -372,12 +430,18 @@ __global__ void __launch_bounds__(kThreads) accept_probs_kernel(const __grid_con
     return;
   }
   // ---- the last token ----
-  // Thread 0's depth and total for all.
   __shared__ int depth_s;
-  __shared__ uint64_t total_s;
+  __shared__ uint64_t left_s;
   if (tid == 0) {
     depth_s = depth;
-    total_s = total;
+    // the row's whole mass, and what the tokens taken out add to their ranges
+    left_s = total + gone_adds();
+    for (int i = 0; i < st.n_gone; ++i) {
+      const int at = (st.gone[i] + pre) / VE / v_per;
+      const uint64_t x = st.gone_r[i] - rest_of(st.gone_p[i], st.gone_q[i], st.f);
+      share[pass & 1][at / kWarps].sum += x;
+      if (at / kWarps == rank) warp_sum[at % kWarps] += x;
+    }
   }
   __syncthreads();
   if (rank == 0 && tid < T_) {
@@ -385,8 +449,8 @@ __global__ void __launch_bounds__(kThreads) accept_probs_kernel(const __grid_con
     if (tid != depth_s) p.out_ids[out + tid] = tid < depth_s ? id[way[tid + 1]] : -1;
     if (tid == 0) p.n_commit[s] = depth_s + 1;
   }
-  // u total, rounded down: a whole running sum exceeds one iff it exceeds the other.
-  const uint64_t target = __umul64hi(__float2ull_rz(uu[0] * 18446744073709551616.f), total_s);
+  // u times the mass, rounded down: a whole running sum exceeds one iff it exceeds the other.
+  const uint64_t target = __umul64hi(__float2ull_rz(uu[0] * 18446744073709551616.f), left_s);
   uint64_t before = 0;
   for (int i = 0; i < rank; ++i) before += share[pass & 1][i].sum;
   if (target < before || target >= before + share[pass & 1][rank].sum) return;
@@ -399,15 +463,29 @@ __global__ void __launch_bounds__(kThreads) accept_probs_kernel(const __grid_con
   const int w0 = (rank * kWarps + from) * v_per, w1 = min(n_vec, w0 + v_per);
   const int m = (v_per + kThreads - 1) / kThreads;
   const int v0 = min(w1, w0 + tid * m), v1 = min(w1, v0 + m);
-  const int k = st.k;
-  uint64_t sum = 0;
-  for (int v = v0; v < v1; ++v) {
-    float a[VE], b[VE] = {};
-    load_entries<T, VE>(prow, v * VE - pre, V, p_wide, a);
+  const float2 f = st.f;
+  const int n_gone = st.n_gone;
+  // R of the entries of vector v.
+  auto rest_at = [&](int v, uint64_t (&r)[VE]) {
+    const int e = v * VE - pre;
+    const uint4 a = load_entries(prow, e, V, p_wide);
+    uint4 b = make_uint4(0, 0, 0, 0);
     if constexpr (kDrafts != kCertain)
-      if (k) load_entries<T, VE>(qrow, v * VE - pre, V, q_wide, b);
+      if (f.x != 0.f) b = load_entries(qrow, e, V, q_wide);
 #pragma unroll
-    for (int i = 0; i < VE; ++i) sum += rest_of<kDrafts>(a[i], b[i], v * VE - pre + i, st, k);
+    for (int i = 0; i < VE; ++i) r[i] = rest_of(entry<T>(a, i), entry<T>(b, i), f);
+    for (int g = 0; g < n_gone; ++g) {
+      const int i = st.gone[g] - e;
+#pragma unroll
+      for (int k = 0; k < VE; ++k)
+        if (k == i) r[k] = st.gone_r[g];
+    }
+  };
+  uint64_t sum = 0, r[VE];
+  for (int v = v0; v < v1; ++v) {
+    rest_at(v, r);
+#pragma unroll
+    for (int i = 0; i < VE; ++i) sum += r[i];
   }
   uint64_t incl = sum;
 #pragma unroll
@@ -421,15 +499,11 @@ __global__ void __launch_bounds__(kThreads) accept_probs_kernel(const __grid_con
   before += incl - sum;
   if (target < before || target >= before + sum) return;
   for (int v = v0; v < v1; ++v) {
-    float a[VE], b[VE] = {};
-    load_entries<T, VE>(prow, v * VE - pre, V, p_wide, a);
-    if constexpr (kDrafts != kCertain)
-      if (k) load_entries<T, VE>(qrow, v * VE - pre, V, q_wide, b);
+    if (v1 - v0 > 1) rest_at(v, r);  // else r still holds it
 #pragma unroll
     for (int i = 0; i < VE; ++i) {
-      const uint64_t r = rest_of<kDrafts>(a[i], b[i], v * VE - pre + i, st, k);
-      if (target >= before && target < before + r) p.out_ids[out + depth_s] = v * VE - pre + i;
-      before += r;
+      if (target >= before && target < before + r[i]) p.out_ids[out + depth_s] = v * VE - pre + i;
+      before += r[i];
     }
   }
 }
@@ -448,7 +522,10 @@ cudaError_t launch(const AcceptParams& p, int n_seqs, int cluster, cudaStream_t 
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, accept_probs_kernel<T, kDrafts>, p);
+  cudaError_t e = cudaSuccess;
+  if (cluster > 8)
+    e = cudaFuncSetAttribute(accept_probs_kernel<T, kDrafts>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, accept_probs_kernel<T, kDrafts>, p);
   if (e != cudaSuccess) (void)cudaGetLastError();
   return e;
 }
@@ -497,7 +574,7 @@ extern "C" int stv_tree_accept_probs(const int32_t* parent, const int32_t* draft
   int sm = 0;
   if (int rc = device_sm_count(&sm)) return rc;
   int cluster = kMaxCluster;
-  while (cluster > 1 && ((int64_t)n_seqs * cluster > 2 * sm || vocab < 4096 * cluster)) cluster /= 2;
+  while (cluster > 1 && ((int64_t)n_seqs * cluster > (cluster > 8 ? sm : 2 * sm) || vocab < 4096 * cluster)) cluster /= 2;
   cudaStream_t st = (cudaStream_t)stream;
   const cudaError_t e = dtype == STV_F32   ? launch_for<float>(a, drafts, n_seqs, cluster, st)
                         : dtype == STV_F16 ? launch_for<__half>(a, drafts, n_seqs, cluster, st)
