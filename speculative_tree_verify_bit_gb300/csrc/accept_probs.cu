@@ -44,7 +44,6 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 16;
 constexpr int kMaxVocab = 524288;
 constexpr uint64_t kFull = 1ull << 62;  // 4 in units of 2^-60
-constexpr double kOne = 1.0 / (1ull << 60);
 enum Drafts { kReplaced = 0, kDistinct = 1, kCertain = 2 };
 
 struct AcceptParams {
@@ -99,29 +98,69 @@ __device__ __forceinline__ void add_to(Parts& a, const Parts& x) {
   a.s += x.s;
 }
 
-// max(p - q, 0)
-__device__ __forceinline__ Parts above(float p, float q) {
-  const Parts a = parts_of(p), b = parts_of(q);
-  if (!(p > q)) return {0, 0, 0};
-  return {a.h - b.h, a.l - b.l, a.s - b.s};
-}
-// max(p - F q, 0).  F q = x + w, w at most 2^-23 x: (p - x) - w has the sign of the
-// difference, since p - x is exact where w could matter.
-__device__ __forceinline__ Parts above(float p, float q, float2 f) {
-  const float x = q * f.x, w = fmaf(q, f.y, fmaf(q, f.x, -x));
-  const Parts a = parts_of(p), b = parts_of(x);
-  const float t2 = fmaf(w, 4194304.f, 3.f), r2 = fmaf(t2 - 3.f, -2.384185791015625e-7f, w);
+// The same of a number of at most 2^-22, without h.
+__device__ __forceinline__ Parts small_parts_of(float x) {
+  const float t2 = fmaf(x, 4194304.f, 3.f), r2 = fmaf(t2 - 3.f, -2.384185791015625e-7f, x);
   const float t3 = fmaf(r2, 274877906944.f, 3.f);
-  if (!((p - x) - w > 0.f)) return {0, 0, 0};
-  return {a.h - b.h, a.l - b.l - (__float_as_int(t2) - 0x40400000), a.s - b.s - (__float_as_int(t3) - 0x40400000)};
+  return {0, __float_as_int(t2) - 0x40400000, __float_as_int(t3) - 0x40400000};
+}
+
+// a += max(p - F q, 0).  F q = x + w with w at most 2^-23 x; where p >= x, p - x = d + e
+// exactly; d + e - w has the sign of (p - x) - w, since d is exact where w matters.
+template <bool kOneF>
+__device__ __forceinline__ void add_above(Parts& a, float p, float q, float2 f) {
+  const float x = kOneF ? q : q * f.x;
+  const float d = p - x;
+  float e = (p - d) - x, sign = d;
+  if constexpr (!kOneF) {
+    const float w = fmaf(q, f.y, fmaf(q, f.x, -x));
+    e -= w;
+    sign = d - w;
+  }
+  const Parts y = parts_of(d), z = small_parts_of(e);
+  if (sign > 0.f) {
+    a.h += y.h;
+    a.l += y.l + z.l;
+    a.s += y.s + z.s;
+  }
 }
 __device__ __forceinline__ uint64_t rest_of(float p, float q, float2 f) {
-  return f.x == 0.f ? fixed(p) : whole(above(p, q, f));
+  if (f.x == 0.f) return fixed(p);
+  Parts a = {0, 0, 0};
+  if (f.x == 1.f && f.y == 0.f) add_above<true>(a, p, q, f);
+  else add_above<false>(a, p, q, f);
+  return whole(a);
 }
-__device__ __forceinline__ float2 pair_of(double f) {
-  const float x = (float)f;
-  return make_float2(x, (float)(f - (double)x));
+// The walk's own arithmetic, one thread's, in pairs of floats (x + y, y at most
+// half a place of x): about 2^-46, at a few cycles an operation where an fp64 one
+// takes a hundred.
+__device__ __forceinline__ float2 pair_sum(float a, float b) {  // |a| >= |b|
+  const float s = a + b;
+  return make_float2(s, b - (s - a));
 }
+__device__ __forceinline__ float2 pair_of(uint64_t x) {  // of x units
+  if (x == 0) return make_float2(0.f, 0.f);
+  const int s = __clzll((long long)x);
+  x <<= s;
+  const uint32_t top = (uint32_t)(x >> 40), rest = (uint32_t)(x >> 8);  // 24 bits, the next 32
+  const float unit = __int_as_float((127 - 36 + 16 - s) << 23);       // 2^(64 - 24 - 60 - s)
+  return pair_sum((float)top * unit, (float)rest * 2.3283064365386963e-10f * unit);
+}
+__device__ __forceinline__ float2 operator*(float2 a, float2 b) {
+  const float x = a.x * b.x;
+  return pair_sum(x, fmaf(a.x, b.x, -x) + fmaf(a.x, b.y, a.y * b.x));
+}
+__device__ __forceinline__ float2 operator/(float2 a, float2 b) {  // b > 0
+  const float r = 1.f / b.x, q = a.x * r;
+  const float2 back = b * make_float2(q, 0.f);
+  return pair_sum(q, ((a.x - back.x) + (a.y - back.y)) * r);
+}
+__device__ __forceinline__ float2 operator+(float2 a, float2 b) {  // both at least 0
+  const bool swap = b.x > a.x;
+  const float2 s = pair_sum(swap ? b.x : a.x, swap ? a.x : b.x);
+  return pair_sum(s.x, s.y + (a.y + b.y));
+}
+__device__ __forceinline__ bool operator<(float2 a, float2 b) { return a.x < b.x || (a.x == b.x && a.y < b.y); }
 
 // VE entries of a row from entry e on, as they lie; zeros outside [0, vocab).
 template <typename T>
@@ -191,12 +230,12 @@ __global__ void __launch_bounds__(kThreads, 2) accept_probs_kernel(const __grid_
   __syncthreads();
   cluster.barrier_wait(std::move(started));
 
-  // Thread 0's place in the walk.  z: Z (1 until a rejection counts); factor: F;
-  // known: the warps' sums are those of the row as it is now, but for the tokens
+  // Thread 0's place in the walk.  z: Z (1 until a rejection counts); known: the warps' sums are those of the row as it is now, but for the tokens
   // taken out (certain: of p).
   int c = 1, depth = 0, pass = 0;
-  double z = 1.0, factor = 0.0, before_f = 0.0, draft_mass = 1.0;
-  uint64_t draft_all = 0;
+  const float2 one = make_float2(1.f, 0.f), zero = make_float2(0.f, 0.f);
+  float2 z = one, before_f = zero, draft_mass = one;
+  uint64_t draft_all = 0, draft_sum = 0;  // what is left of the draft's mass; the last pass's sum
   bool pending = false, known = false;
   uint64_t total = 0, left = 0;  // the last pass's sum; with the tokens taken out
   int v_per = 0;
@@ -233,20 +272,19 @@ __global__ void __launch_bounds__(kThreads, 2) accept_probs_kernel(const __grid_
               st.gone_r[st.n_gone++] = 0;
               left -= px;
             }
-            if (st.n_gone) z = (double)left * kOne;
+            if (st.n_gone) z = pair_of(left);
           } else {
             const uint64_t sum = total + gone_adds();
             if (sum == 0) {  // nothing left: R and Z stay
-              factor = before_f;
-              st.f = pair_of(factor);
+              st.f = before_f;
               known = false;
             } else {
-              z = (double)sum * kOne;
+              z = pair_of(sum);
               left = sum;
               known = true;
             }
             if constexpr (kDrafts == kDistinct) {
-              if (st.n_gone == 0) draft_all = share[pass & 1][0].draft;
+              if (st.n_gone == 0) draft_all = draft_sum;
               if (at < 0) {
                 const uint64_t qx = fixed(qq[c]);
                 draft_all = draft_all > qx ? draft_all - qx : 0;
@@ -255,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, 2) accept_probs_kernel(const __grid_
                 st.gone_q[st.n_gone] = qq[c];
                 st.gone_r[st.n_gone++] = rest_of(pp[c], qq[c], st.f);
               }
-              draft_mass = (double)draft_all * kOne;
+              draft_mass = pair_of(draft_all);
             }
           }
           pending = false;
@@ -272,18 +310,22 @@ __global__ void __launch_bounds__(kThreads, 2) accept_probs_kernel(const __grid_
           break;
         }
         const int at = place_of(id[c]);
-        double s_x = qq[c], r_x = pp[c];  // S(x), R(x)
-        if constexpr (kDrafts == kDistinct)
-          if (st.n_gone) s_x = at < 0 && draft_mass > 0 ? s_x / draft_mass : 0;
-        if (at >= 0) r_x = (double)st.gone_r[at] * kOne;
-        else if (kDrafts != kCertain && factor > 0) r_x = (double)rest_of(pp[c], qq[c], st.f) * kOne;
-        if ((double)uu[c] * s_x * z < r_x) {  // accepted
+        float2 s_x = make_float2(qq[c], 0.f), r_x = make_float2(pp[c], 0.f);  // S(x), R(x), times the sum of S
+        if (at >= 0) r_x = pair_of(st.gone_r[at]);
+        else if (kDrafts != kCertain && st.f.x > 0.f) r_x = pair_of(rest_of(pp[c], qq[c], st.f));
+        if constexpr (kDrafts == kDistinct) {
+          if (st.n_gone) {
+            if (at >= 0 || draft_mass.x == 0.f) s_x = zero;
+            else r_x = r_x * draft_mass;
+          }
+        }
+        // exact at a node's first child: three 24-bit numbers
+        if (make_float2(uu[c], 0.f) * s_x * z < r_x) {  // accepted
           node = c;
           way[++depth] = c;
           st.n_gone = 0;
-          z = draft_mass = 1.0;
-          factor = 0;
-          st.f = make_float2(0.f, 0.f);
+          z = draft_mass = one;
+          st.f = zero;
           known = false;
           ++c;
           continue;
@@ -293,12 +335,11 @@ __global__ void __launch_bounds__(kThreads, 2) accept_probs_kernel(const __grid_
           cmd = known ? 0 : 1;
           known = true;
         } else {
-          before_f = factor;
-          double f = z;
+          before_f = st.f;
+          float2 f = z;
           if constexpr (kDrafts == kDistinct)
-            if (st.n_gone) f = draft_mass > 0 ? z / draft_mass : 0;
-          factor += f;
-          st.f = pair_of(factor);
+            if (st.n_gone) f = draft_mass.x > 0.f ? z / draft_mass : zero;
+          st.f = st.f + f;
           cmd = 1;
         }
       }
@@ -348,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, 2) accept_probs_kernel(const __grid_
           for (int i = 0; i < VE; ++i) {
             const float x = entry<T>(a[j], i), y = entry<T>(b[j], i);
             most = max(most, max(__float_as_uint(x), __float_as_uint(y)));
-            add_to(part, above(x, y));
+            add_above<true>(part, x, y, f);
             if constexpr (kDrafts == kDistinct) add_to(part_q, parts_of(y));
           }
         } else {
@@ -356,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, 2) accept_probs_kernel(const __grid_
           for (int i = 0; i < VE; ++i) {
             const float x = entry<T>(a[j], i), y = entry<T>(b[j], i);
             most = max(most, max(__float_as_uint(x), __float_as_uint(y)));
-            add_to(part, above(x, y, f));
+            add_above<false>(part, x, y, f);
           }
         }
       }
@@ -398,19 +439,21 @@ __global__ void __launch_bounds__(kThreads, 2) accept_probs_kernel(const __grid_
       if (lane < C) *cluster.map_shared_rank(&share[pass & 1][rank], lane) = mine;
     }
     cluster.sync();
-    if (tid == 0) {
-      total = 0;
-      uint64_t all = 0;
-      int found = 0;
-      for (int i = 0; i < C; ++i) {
-        const Share x = share[pass & 1][i];
-        total = sat_add(total, x.sum);
-        all = sat_add(all, x.draft);
-        found |= x.bad;
+    if (w == 0) {
+      Share x = lane < C ? share[pass & 1][lane] : Share{0, 0, 0};
+#pragma unroll
+      for (int o = kMaxCluster / 2; o; o >>= 1) {
+        x.sum = sat_add(x.sum, __shfl_xor_sync(0xffffffffu, x.sum, o));
+        x.draft = sat_add(x.draft, __shfl_xor_sync(0xffffffffu, x.draft, o));
+        x.bad |= __shfl_xor_sync(0xffffffffu, x.bad, o);
       }
-      share[pass & 1][0].draft = all;
-      if (found || total >= kFull || all >= kFull || ((kDrafts == kCertain || !pending) && total + gone_adds() == 0) || !(uu[0] >= 0.f && uu[0] < 1.f))
-        bad_bits = STV_DEV_BAD_SAMPLE;
+      if (lane == 0) {
+        total = x.sum;
+        draft_sum = x.draft;
+        if (x.bad || total >= kFull || draft_sum >= kFull || !(uu[0] >= 0.f && uu[0] < 1.f) ||
+            ((kDrafts == kCertain || !pending) && total + gone_adds() == 0))
+          bad_bits = STV_DEV_BAD_SAMPLE;
+      }
     }
     // (thread 0's next decisions are behind this loop's first barrier; it alone reads what it wrote)
   }
