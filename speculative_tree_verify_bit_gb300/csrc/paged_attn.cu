@@ -24,13 +24,22 @@ constexpr int kThreads = 32 * (kWorkers + 1);
 
 template <int HD>
 struct Small {
-  static constexpr int kTileBytes = kAttnTile * HD * 2;  // of K, and of V
+  static constexpr int kTileBytes = kSmallTile * HD * 2;  // of K, and of V
   static constexpr int kStages = HD == 256 ? 3 : 4;
   static constexpr int kCtasPerSm = HD == 256 ? 1 : HD == 128 ? 1 : 2;
   static constexpr int kQBytes = kSmallRows * HD * 2;
   static constexpr int kChunk = HD / 4;  // channels put together at a time
   static constexpr int kExchangeBytes = kWorkers * kSmallRows * kChunk * 4;
   static constexpr int kSmem = 1024 + kStages * 2 * kTileBytes + 2 * kQBytes + kExchangeBytes;
+};
+
+enum TileFlags { kFirst = 1, kLast = 2, kEdge = 4, kAbsent = 8, kStop = 16 };
+
+// A tile as the producer hands it to the workers.
+struct TileInfo {
+  int flags, key0;
+  int row0, rows, h, slot;  // the unit's first row of q, its rows of Q, KV head, workspace slot or -1
+  AttnUnit x;
 };
 
 template <int kStages>
@@ -109,7 +118,7 @@ __global__ void __launch_bounds__(kThreads, Small<HD>::kCtasPerSm)
       for (int t = run.t0; ok && t < run.t1; ++t, ++g) {
         const int st = g % kStages;
         if (!(ok = waitw<false>(&sh.empty[st], ((g / kStages) & 1) ^ 1, abort_flag))) break;
-        const int key0 = tile_key(run.x, t);
+        const int key0 = tile_key(p, run.x, t);
         const int row = tile_row(p, run.en.s, run.at.h, key0);
         if (lane == 0) {
           TileInfo& i = sh.info[st];
@@ -126,8 +135,8 @@ __global__ void __launch_bounds__(kThreads, Small<HD>::kCtasPerSm)
           } else {
             mbar_expect_tx(&sh.full[st], 2 * K::kTileBytes);
             uint8_t* dst = ring + st * 2 * K::kTileBytes;
-            tma_tile(dst, &p.map, row, &sh.full[st]);
-            tma_tile(dst + K::kTileBytes, &p.map, row + kPageTok, &sh.full[st]);
+            tma_box(dst, &p.map_k, row, 0, &sh.full[st]);
+            tma_box(dst + K::kTileBytes, &p.map_k, row + kPageTok, 0, &sh.full[st]);
           }
         }
         __syncwarp();
@@ -498,18 +507,33 @@ EncodeTiled encode_tiled() {
   return fn;
 }
 
-// The pool as tiles: [hd / 64][rows][64 channels], boxes of 64 rows of all channels.
-int make_map(const stv_layer_cache* layer, const RowShape& sh, CUtensorMap* map) {
+int encode(CUtensorMap* map, bool bf16, int rank, void* base, const cuuint64_t* dims, const cuuint64_t* strides,
+           const cuuint32_t* box) {
   const EncodeTiled fn = encode_tiled();
   if (!fn) return STV_ERR_CUDA;
-  const cuuint64_t rows = (cuuint64_t)layer->n_pages * sh.hkv * 2 * kPageTok;
-  const cuuint64_t dims[3] = {64, rows, (cuuint64_t)sh.hd / 64};
-  const cuuint64_t strides[2] = {(cuuint64_t)sh.hd * 2, 128};
-  const cuuint32_t box[3] = {64, kAttnTile, (cuuint32_t)sh.hd / 64}, step[3] = {1, 1, 1};
-  const CUresult r = fn(map, sh.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, layer->pool,
-                        dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+  const cuuint32_t step[4] = {1, 1, 1, 1};
+  const CUresult r = fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rank, base, dims,
+                        strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? STV_OK : STV_ERR_CUDA;
+}
+
+// The pool as [hd / 64][rows][64 channels], boxes of `keys` rows of `blocks` times 64 channels.
+int make_pool_map(const stv_layer_cache* layer, const RowShape& sh, int keys, int blocks, CUtensorMap* map) {
+  const cuuint64_t dims[3] = {64, (cuuint64_t)layer->n_pages * sh.hkv * 2 * kPageTok, (cuuint64_t)sh.hd / 64};
+  const cuuint64_t strides[2] = {(cuuint64_t)sh.hd * 2, 128};
+  const cuuint32_t box[3] = {64, (cuuint32_t)keys, (cuuint32_t)blocks};
+  return encode(map, sh.bf16, 3, layer->pool, dims, strides, box);
+}
+
+// q as [rows][heads][hd / 64][64 channels], boxes of 64 channels of `tokens` tokens' G heads.
+int make_q_map(const stv_rows* q, const RowShape& sh, int n_rows, int tokens, CUtensorMap* map) {
+  const cuuint64_t dims[4] = {64, (cuuint64_t)sh.hd / 64, (cuuint64_t)sh.hq, (cuuint64_t)n_rows};
+  // a stride that no step is taken along is the view's to choose: any that the map accepts
+  const cuuint64_t strides[3] = {128, sh.hq > 1 ? (cuuint64_t)q->head_stride * 2 : (cuuint64_t)sh.hd * 2,
+                                 n_rows > 1 ? (cuuint64_t)q->row_stride * 2 : (cuuint64_t)sh.hd * 2};
+  const cuuint32_t box[4] = {64, 1, (cuuint32_t)sh.G, (cuuint32_t)tokens};
+  return encode(map, sh.bf16, 4, q->data, dims, strides, box);
 }
 
 // Whether the bytes of a view and of another (or of a range) can meet, by their extents.
@@ -575,7 +599,6 @@ extern "C" int stv_paged_attn(const stv_shape* shape, const stv_attn_spec* spec,
 
   AttnParams p;
   memset(&p, 0, sizeof(p));
-  if ((rc = make_map(layer, sh, &p.map))) return rc;
   auto wide = [&](const stv_rows* v) {
     return (uintptr_t)v->data % 16 == 0 && (v->heads == 1 || v->head_stride % 8 == 0) &&
            (n_rows == 1 || v->row_stride % 8 == 0);
@@ -586,8 +609,17 @@ extern "C" int stv_paged_attn(const stv_shape* shape, const stv_attn_spec* spec,
   p.q_head = q->head_stride;
   p.o_row = o->row_stride;
   p.o_head = o->head_stride;
-  p.q_wide = wide(q);
+  // (2^40: what a tensor map's strides may be)
+  p.q_wide = wide(q) && q->row_stride < (int64_t)1 << 38;
   p.o_wide = wide(o);
+  if (a.small) {
+    if ((rc = make_pool_map(layer, sh, kSmallTile, sh.hd / 64, &p.map_k))) return rc;
+  } else {
+    if ((rc = make_pool_map(layer, sh, kBigTile, 1, &p.map_k))) return rc;
+    if ((rc = make_pool_map(layer, sh, 8192 / sh.hd, sh.hd / 64, &p.map_v))) return rc;
+    if (p.q_wide && (rc = make_q_map(q, sh, n_rows, kMaxRows / sh.G, &p.map_q))) return rc;
+  }
+  p.tile_bits = a.small ? 6 : 7;
   p.tables = pool->tables;
   p.counts = pool->counts;
   p.table_stride = pool->table_stride;

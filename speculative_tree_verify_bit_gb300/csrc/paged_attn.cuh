@@ -3,7 +3,7 @@
 //
 // Work.  A unit is (entry, tokens_per consecutive new tokens of it, KV head):
 // at most 16 or 128 (256) rows of Q that read the same keys.  Its keys come in
-// tiles of 64: those of the first tokens (sinks) that lie before the window's
+// tiles of 64 (single tokens) or 128: those of the first tokens (sinks) that lie before the window's
 // first tile, then the window's (or all up to the last visible key).  All tiles
 // of all units, in the order (entry, unit, head, tile), are cut into as many
 // equal runs as there are CTAs.  A unit inside one CTA's run is finished there;
@@ -26,7 +26,8 @@
 
 namespace stv {
 
-constexpr int kAttnTile = 64;       // keys
+constexpr int kSmallTile = 64;      // keys of a tile, single tokens
+constexpr int kBigTile = 128;       // blocks and prompts
 constexpr int kMaxEntries = 4096;
 constexpr int kMaxCtx = 1 << 30;
 constexpr int kSmallRows = 16;      // rows of Q per unit, single tokens
@@ -38,7 +39,10 @@ struct JoinRecord {
 };
 
 struct AttnParams {
-  CUtensorMap map;  // the pool as [hd / 64][rows][64], 64 x 64 x (hd / 64) boxes
+  // The pool as [hd / 64][rows][64 channels], in boxes of a tile of K and V
+  // (single tokens: the same map), or of a 16 KB piece of one; q as
+  // [rows][heads][hd / 64][64], in boxes of a row tile's 64 channels.
+  CUtensorMap map_k, map_v, map_q;
   const void* q;
   void* o;
   int64_t q_row, q_head, o_row, o_head;  // strides in elements
@@ -51,6 +55,7 @@ struct AttnParams {
   int n, n_rows, max_new;
   int hkv, G;
   int tokens_per;  // new tokens of a unit
+  int tile_bits;   // log2 of a tile's keys
   int window, sinks, causal;
   float scale2;  // scale * log2(e)
   bool q_wide, o_wide;  // 16-byte loads of q, stores of o
@@ -117,23 +122,23 @@ __device__ __forceinline__ AttnUnit unit_of(const AttnParams& p, const Entry& e,
   x.end = min(e.ctx + e.L, e.keys);
   x.hi = p.causal ? min(x.pos0 + x.ntok, x.end) : x.end;
   x.lo = p.window ? max(0, x.pos0 - p.window + 1) : 0;
-  x.wt0 = x.lo / kAttnTile;
-  const int up_to = (x.hi + kAttnTile - 1) / kAttnTile;
-  x.n_sink = p.window && p.sinks ? min((p.sinks - 1) / kAttnTile + 1, min(x.wt0, up_to)) : 0;
+  x.wt0 = x.lo >> p.tile_bits;
+  const int up_to = (x.hi + (1 << p.tile_bits) - 1) >> p.tile_bits;
+  x.n_sink = p.window && p.sinks ? min(((p.sinks - 1) >> p.tile_bits) + 1, min(x.wt0, up_to)) : 0;
   x.n_tiles = max(1, max(0, up_to - x.wt0) + x.n_sink);  // one tile at least: it writes the rows
   return x;
 }
 // First key of its t-th tile.
-__device__ __forceinline__ int tile_key(const AttnUnit& x, int t) {
-  return (t < x.n_sink ? t : x.wt0 + t - x.n_sink) * kAttnTile;
+__device__ __forceinline__ int tile_key(const AttnParams& p, const AttnUnit& x, int t) {
+  return (t < x.n_sink ? t : x.wt0 + t - x.n_sink) << p.tile_bits;
 }
 // Whether some row may not see some key of the tile.
 __device__ __forceinline__ bool tile_edge(const AttnParams& p, const AttnUnit& x, int key0) {
-  const int last = key0 + kAttnTile - 1;
+  const int last = key0 + (1 << p.tile_bits) - 1;
   if (last >= x.end || (p.causal && last > x.pos0)) return true;
   return p.window && key0 <= x.pos0 + x.ntok - 1 - p.window && last >= p.sinks;
 }
-// The keys of a tile (bit k: key0 + k) that the row at position pos sees.
+// Of 64 keys (bit k: key0 + k), those that the row at position pos sees.
 __device__ __forceinline__ uint64_t low_bits(int n) { return n >= 64 ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1; }
 __device__ __forceinline__ uint64_t row_sees(const AttnParams& p, int pos, int end, int key0) {
   uint64_t m = low_bits((p.causal ? min(pos + 1, end) : end) - key0);
@@ -327,11 +332,11 @@ __device__ __forceinline__ int tile_row(const AttnParams& p, int s, int h, int k
   return (page * p.hkv + h) * (2 * kPageTok) + key0 % kPageTok;
 }
 
-__device__ __forceinline__ void tma_tile(void* dst, const CUtensorMap* map, int row, uint64_t* bar) {
+__device__ __forceinline__ void tma_box(void* dst, const CUtensorMap* map, int row, int block, uint64_t* bar) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
           su32(dst)),
-      "l"(map), "r"(0), "r"(row), "r"(0), "r"(su32(bar))
+      "l"(map), "r"(0), "r"(row), "r"(block), "r"(su32(bar))
       : "memory");
 }
 
@@ -354,15 +359,6 @@ struct Pack<__nv_bfloat16> {
   static __device__ __forceinline__ float2 floats(uint32_t v) {
     return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
   }
-};
-
-enum TileFlags { kFirst = 1, kLast = 2, kEdge = 4, kAbsent = 8, kStop = 16 };
-
-// A tile as the producer hands it to the other warps.
-struct TileInfo {
-  int flags, key0;
-  int row0, rows, h, slot;  // the unit's first row of q, its rows of Q, KV head, workspace slot or -1
-  AttnUnit x;
 };
 
 // n (2, 4 or 8) adjacent outputs, as wide as o allows.
