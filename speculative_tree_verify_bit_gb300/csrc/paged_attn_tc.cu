@@ -37,9 +37,11 @@ struct Tiles {
   static constexpr int kPieces = HD / 64;        // of K's tile, and of V's
   static constexpr int kVKeys = 8192 / HD;       // keys of a piece of V
   static constexpr int kAhead = 2 / NQ;          // tiles of keys that S runs ahead
-  static constexpr int kRing = HD == 64 ? 8 : 10;
+  static constexpr int kStage = NQ * 16384;      // 32 rows x 128 bytes for each softmax warp: O on its way out
+  static constexpr int kRing = (232448 - 1024 - 2048 - NQ * kQTile - kStage) / kPiece < 10
+                                   ? (232448 - 1024 - 2048 - NQ * kQTile - kStage) / kPiece : 10;
   static_assert(kRing / kPieces / 2 + kAhead + 2 < kUnits, "units in flight");
-  static constexpr int kSmem = 1024 + NQ * kQTile + kRing * kPiece;
+  static constexpr int kSmem = 1024 + NQ * kQTile + kStage + kRing * kPiece;
   static constexpr int kThreads = 96 + 128 * NQ;
   // tensor memory: two S (P in their first halves), O of each row tile
   static constexpr uint32_t kColS = 0, kColO = 256;
@@ -103,6 +105,7 @@ __global__ void __launch_bounds__(Tiles<HD, NQ>::kThreads, 1)
   uint8_t* smem = smem_raw + ((1024 - (su32(smem_raw) & 1023)) & 1023);
   uint8_t* const qbuf = smem;
   uint8_t* const ring = smem + NQ * C::kQTile;
+  uint8_t* const stage = ring + R * kPiece;
   volatile int* abort_flag = &sh.abort;
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
@@ -212,77 +215,126 @@ __global__ void __launch_bounds__(Tiles<HD, NQ>::kThreads, 1)
     constexpr uint32_t kIdescQK = idesc<T>(kBigTile, false), kIdescPV = idesc<T>(HD, true);
     const uint64_t qdesc = desc_sw128(su32(qbuf)), kdesc = desc_sw128(su32(ring));
     const uint64_t vdesc = desc_mn_sw128(su32(ring), C::kVKeys * 128);
-    // The ring's pieces of K, then of V, of tile g (see the producer's order).
-    auto k_piece = [&](int g) { return (g + max(0, g - C::kAhead + 1)) * NP; };
-    auto v_piece = [&](int g) { return (g + min(g + C::kAhead, n_tiles)) * NP; };
-    int qk_unit = 0, qk_left = 0;          // units whose S has begun; tiles of the last one still to come
-    int pv_unit = 0, pv_left = 0;          // the same for P V
+    // Whatever the loop's course hangs on is read from lane 0, so that the compiler
+    // knows the warp to stay together: descriptors are then kept once for the warp
+    // (an MMA takes 140 cycles to issue otherwise).  What a step waits for is probed
+    // at once, ahead of the issue.
+    auto same = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
+    const int n_mine = same(n_tiles);
+    int qk_unit = 0, qk_left = 0;    // units whose S has begun; tiles of the last one still to come
+    int pv_unit = 0, pv_left = 0;    // the same for P V
     bool pv_first = false, ok = true;
-    auto issue_qk = [&](int n) -> bool {  // step n
-      const int g = n / NQ, qt = n % NQ, b = n & 1;
+    // A place in the ring, and the phase there.
+    struct Place {
+      int st;
+      uint32_t ph;
+    };
+    auto plus = [&](Place x, int i) -> Place {  // i < R
+      x.st += i;
+      if (x.st >= R) {
+        x.st -= R;
+        x.ph ^= 1u;
+      }
+      return x;
+    };
+    auto landed = [&](Place x) -> uint32_t {
+      uint32_t y = 1;
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        const Place z = plus(x, i);
+        y &= probe(&sh.full[z.st], z.ph);
+      }
+      return y;
+    };
+    auto wait_landed = [&](Place x) -> bool {
+      bool y = true;
+#pragma unroll 1
+      for (int i = 0; i < NP && y; ++i) {
+        const Place z = plus(x, i);
+        y = waitw<false>(&sh.full[z.st], z.ph, abort_flag);
+      }
+      return y;
+    };
+    // S of a step (K of its tile is at k and has landed).
+    auto issue_qk = [&](int qt, int b, Place k) -> bool {
       if (qt == 0) {
         if (qk_left == 0) {
           UnitInfo u;
           if (!unit_at(qk_unit, &u) || !waitw<false>(&sh.q_full, qk_unit & 1, abort_flag)) return false;
-          qk_left = u.t1 - u.t0;
+          qk_left = same(u.t1 - u.t0);
           ++qk_unit;
         }
         --qk_left;
       }
-      const int p0 = k_piece(g);
-      uint32_t seen[NP];
-#pragma unroll
-      for (int i = 0; i < NP; ++i) seen[i] = probe(&sh.full[(p0 + i) % R], ((p0 + i) / R) & 1);
+      tc_after();
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
-        const int st = (p0 + i) % R;
-        if (qt == 0 && !settle<false>(&sh.full[st], ((p0 + i) / R) & 1, seen[i], abort_flag)) return false;
-        tc_after();
-        const uint64_t kd = kdesc + (uint64_t)(st * (kPiece >> 4));
+        const Place z = plus(k, i);
+        const uint64_t kd = kdesc + (uint64_t)(z.st * (kPiece >> 4));
         const uint64_t qd = qdesc + (uint64_t)(qt * (C::kQTile >> 4) + i * (kPiece >> 4));
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
           mma_smem(tm + C::kColS + 128 * b, qd + 2 * kk, kd + 2 * kk, kIdescQK, i > 0 || kk > 0);
-        if (qt == NQ - 1) tc_commit(&sh.empty[st]);
+        if (qt == NQ - 1) tc_commit(&sh.empty[z.st]);
       }
       tc_commit(&sh.s_full[b]);
       if (qt == NQ - 1 && qk_left == 0) tc_commit(&sh.q_empty);
       return true;
     };
-    const int n_steps = n_tiles * NQ;
-    for (int n = 0; n < 2 && n < n_steps && ok; ++n) ok = issue_qk(n);
-    for (int n = 0; n < n_steps && ok; ++n) {
-      const int g = n / NQ, qt = n % NQ, b = n & 1;
-      if (qt == 0) {
-        if ((pv_first = pv_left == 0)) {
-          UnitInfo u;
-          if (!(ok = unit_at(pv_unit, &u))) break;
-          pv_left = u.t1 - u.t0;
-          ++pv_unit;
-        }
-        --pv_left;
+    // K of the tile `ahead` follows V of this one; before it, K of the first tiles.
+    Place v = {0, 0};
+    if (n_mine > 0) {
+      for (int i = 0; i < C::kAhead && i < n_mine && ok; ++i) {
+        if (!(ok = wait_landed(v))) break;
+        for (int qt = 0; qt < NQ && ok; ++qt) ok = issue_qk(qt, (i * NQ + qt) & 1, v);
+        v = plus(v, NP);
       }
-      const int p0 = v_piece(g);
-      // the unit's first P V restarts O: the previous unit's O has been read
-      if (pv_first && pv_unit > 1 && !(ok = waitw<false>(&sh.o_free[qt], (pv_unit - 2) & 1, abort_flag))) break;
+    }
+    uint32_t s_ph = 0;  // phase of both S buffers' steps
+    for (int g = 0; g < n_mine && ok; ++g) {
+      const Place k = plus(v, NP);
+      const bool more = g + C::kAhead < n_mine;
+      if ((pv_first = pv_left == 0)) {
+        UnitInfo u;
+        if (!(ok = unit_at(pv_unit, &u))) break;
+        pv_left = same(u.t1 - u.t0);
+        ++pv_unit;
+      }
+      --pv_left;
 #pragma unroll
-      for (int half = 0; half < 2 && ok; ++half) {
-        const uint32_t seen_p = probe(&sh.p_full[b][half], (n >> 1) & 1);
-        if (!(ok = settle<false>(&sh.p_full[b][half], (n >> 1) & 1, seen_p, abort_flag))) break;
+      for (int qt = 0; qt < NQ; ++qt) {
+        const int b = NQ == 2 ? qt : (g & 1);
+        if (NQ == 1 || qt == 0) s_ph = (NQ == 2 ? g : g >> 1) & 1;
+        const uint32_t seen_v = qt == 0 ? landed(v) : 1u, seen_k = qt == 0 && more ? landed(k) : 1u;
+        const uint32_t seen_0 = probe(&sh.p_full[b][0], s_ph);
+        const bool there_v = __all_sync(0xffffffffu, seen_v), there_k = __all_sync(0xffffffffu, seen_k);
+        if (!there_v && !(ok = wait_landed(v))) break;
+        // the unit's first P V restarts O: the previous unit's O has been read
+        if (pv_first && pv_unit > 1 && !(ok = waitw<false>(&sh.o_free[qt], (pv_unit - 2) & 1, abort_flag))) break;
+        if (!(ok = settle<false>(&sh.p_full[b][0], s_ph, seen_0, abort_flag))) break;
+        auto issue_pv = [&](int half) {
+          tc_after();
 #pragma unroll
-        for (int kk = 4 * half; kk < 4 * half + 4; ++kk) {  // 16 keys
-          const int i = kk * 16 / C::kVKeys, in = kk * 16 % C::kVKeys, st = (p0 + i) % R;
-          if (in == 0 && qt == 0 && !(ok = waitw<false>(&sh.full[st], ((p0 + i) / R) & 1, abort_flag))) break;
-          if (in == 0 || kk == 4 * half) tc_after();
-          mma_tmemA(tm + C::kColO + qt * HD, tm + C::kColS + 128 * b + 8 * kk,
-                    vdesc + (uint64_t)(st * (kPiece >> 4) + in * (128 >> 4)), kIdescPV, !pv_first || kk > 0);
-          if (in + 16 == C::kVKeys && qt == NQ - 1) tc_commit(&sh.empty[st]);
+          for (int kk = 4 * half; kk < 4 * half + 4; ++kk) {  // 16 keys
+            const int in = kk * 16 % C::kVKeys;
+            const Place z = plus(v, kk * 16 / C::kVKeys);
+            mma_tmemA(tm + C::kColO + qt * HD, tm + C::kColS + 128 * b + 8 * kk,
+                      vdesc + (uint64_t)(z.st * (kPiece >> 4) + in * (128 >> 4)), kIdescPV, !pv_first || kk > 0);
+            if (in + 16 == C::kVKeys && qt == NQ - 1) tc_commit(&sh.empty[z.st]);
+          }
+        };
+        issue_pv(0);
+        const uint32_t seen_1 = probe(&sh.p_full[b][1], s_ph);
+        if (!(ok = settle<false>(&sh.p_full[b][1], s_ph, seen_1, abort_flag))) break;
+        issue_pv(1);
+        tc_commit(&sh.pv_done[qt]);
+        if (pv_left == 0) tc_commit(&sh.o_ready[qt]);
+        if (more) {
+          if (!there_k && !(ok = wait_landed(k))) break;
+          if (!(ok = issue_qk(qt, b, k))) break;
         }
       }
-      if (!ok) break;
-      tc_commit(&sh.pv_done[qt]);
-      if (pv_left == 0) tc_commit(&sh.o_ready[qt]);
-      if (n + 2 < n_steps) ok = issue_qk(n + 2);
+      v = plus(v, more ? 2 * NP : NP);
     }
     // Every MMA issued here has finished before TMEM is freed.
     tc_commit(&sh.mma_done);
@@ -345,53 +397,63 @@ __global__ void __launch_bounds__(Tiles<HD, NQ>::kThreads, 1)
         if (!(ok = waitw<false>(&sh.s_full[b], (n >> 1) & 1, abort_flag))) break;
         tc_after();
         const uint32_t col_s = lane_addr + C::kColS + 128 * b;
-        uint32_t s[128];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) tmem_ld32(col_s + 32 * i, s + 32 * i);
         const bool absent = sh.absent[g % 32];
         const bool edge = absent || tile_edge(p, u.x, key0);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) tmem_wait_ld(s + 32 * i);
-        if (edge) {
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const int k0 = key0 + 64 * half;
-            const uint64_t vis = absent ? 0ull : row_sees(p, pos, u.x.end, k0);
+        // The row's maximum, 64 columns at a time; masked columns go back as -inf.
+        // (S is read twice: a step's code stays short, which is what the
+        // instruction cache asks for; a step with its 128 columns unrolled
+        // waited for instructions longer than for anything else.)
+        float mx = -INFINITY;
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          uint32_t s[64];
+          tmem_ld32(col_s + 64 * half, s);
+          tmem_ld32(col_s + 64 * half + 32, s + 32);
+          tmem_wait_ld(s);
+          tmem_wait_ld(s + 32);
+          if (edge) {
+            const uint64_t vis = absent ? 0ull : row_sees(p, pos, u.x.end, key0 + 64 * half);
             const uint32_t va = (uint32_t)vis, vb = (uint32_t)(vis >> 32);
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
-              s[64 * half + e] = ((va >> e) & 1u) ? s[64 * half + e] : 0xff800000u;
-              s[64 * half + 32 + e] = ((vb >> e) & 1u) ? s[64 * half + 32 + e] : 0xff800000u;
+              s[e] = ((va >> e) & 1u) ? s[e] : 0xff800000u;
+              s[32 + e] = ((vb >> e) & 1u) ? s[32 + e] : 0xff800000u;
             }
+            tmem_st32(col_s + 64 * half, s);
+            tmem_st32(col_s + 64 * half + 32, s + 32);
           }
+          // 3-input max, 8 independent chains
+          float mx8[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) mx8[e] = fmaxf(__uint_as_float(s[e]), __uint_as_float(s[8 + e]));
+#pragma unroll
+          for (int e = 16; e < 64; e += 2)
+            mx8[(e >> 1) & 7] = max3(mx8[(e >> 1) & 7], __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+          mx = max3(mx, fmaxf(mx8[0], mx8[1]), max3(max3(mx8[2], mx8[3], mx8[4]), mx8[5], fmaxf(mx8[6], mx8[7])));
+        }
+        if (edge) {
+          tmem_wait_st();
           // Keys that no row sees: zeros in V, by the first row tile's warps.
           if (qt == 0) {
-            const uint64_t some[2] = {absent ? 0ull : unit_sees(p, u.x, key0), absent ? 0ull : unit_sees(p, u.x, key0 + 64)};
-            if ((some[0] & some[1]) != ~0ull) {
+            const uint64_t some0 = absent ? 0ull : unit_sees(p, u.x, key0), some1 = absent ? 0ull : unit_sees(p, u.x, key0 + 64);
+            if ((some0 & some1) != ~0ull) {
               const int p0 = (g + min(g + C::kAhead, n_tiles)) * NP;
 #pragma unroll 1
-              for (int i = 0; i < NP && ok; ++i) {
-                const int st = (p0 + i) % R;
-                if (!(ok = waitw<false>(&sh.full[st], ((p0 + i) / R) & 1, abort_flag))) break;
-                const uint32_t base = su32(ring) + st * kPiece;
-                for (int e = r; e < kPiece / 16; e += 128) {
-                  const int key = i * C::kVKeys + (e >> 3) % C::kVKeys;
-                  if (!((some[key >> 6] >> (key & 63)) & 1)) st_shared_v4(base + e * 16, 0u, 0u, 0u, 0u);
-                }
+              for (int i = 0; i < NP && ok; ++i) ok = waitw<false>(&sh.full[(p0 + i) % R], ((p0 + i) / R) & 1, abort_flag);
+              if (!ok) break;
+              // thread: 16 bytes of keys r / 8, r / 8 + 16, ... in every block of 64 channels
+#pragma unroll 1
+              for (int m = 0; m < 8; ++m) {
+                const int key = (r >> 3) + 16 * m;
+                if (((m < 4 ? some0 : some1) >> (key & 63)) & 1) continue;
+                const uint32_t at = su32(ring) + (p0 + key / C::kVKeys) % R * kPiece + key % C::kVKeys * 128 + (r & 7) * 16;
+#pragma unroll
+                for (int cb = 0; cb < NP; ++cb) st_shared_v4(at + cb * (C::kVKeys * 128), 0u, 0u, 0u, 0u);
               }
               fence_async_smem();
-              if (!ok) break;
             }
           }
         }
-        // Row maximum: 3-input max, 8 independent chains.
-        float mx8[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) mx8[e] = fmaxf(__uint_as_float(s[e]), __uint_as_float(s[8 + e]));
-#pragma unroll
-        for (int e = 16; e < 128; e += 2)
-          mx8[(e >> 1) & 7] = max3(mx8[(e >> 1) & 7], __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
-        const float mx = fmaxf(max3(mx8[0], mx8[1], mx8[2]), max3(max3(mx8[3], mx8[4], mx8[5]), mx8[6], mx8[7]));
         const float m_tile = mx * c;
         float corr = 1.f;
         if (m_tile > m_ref + kRescaleThreshold) {
@@ -426,13 +488,17 @@ __global__ void __launch_bounds__(Tiles<HD, NQ>::kThreads, 1)
         const float mref = m_ref == -INFINITY ? 0.f : m_ref;
         const float2 c2 = make_float2(c, c), nm2 = make_float2(-mref, -mref);
         float2 sum4[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
+#pragma unroll 1
         for (int half = 0; half < 2; ++half) {
-          uint32_t pk[32];
+          uint32_t s[64], pk[32];
+          tmem_ld32(col_s + 64 * half, s);
+          tmem_ld32(col_s + 64 * half + 32, s + 32);
+          tmem_wait_ld(s);
+          tmem_wait_ld(s + 32);
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
-            const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[64 * half + 2 * e]),
-                                                    __uint_as_float(s[64 * half + 2 * e + 1])), c2, nm2);
+            const float2 x =
+                __ffma2_rn(make_float2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), c2, nm2);
             const float2 v = make_float2(ex2(x.x), ex2(x.y));
             sum4[e & 3] = __fadd2_rn(sum4[e & 3], v);
             pk[e] = Pack<T>::two(v.x, v.y);
@@ -450,43 +516,64 @@ __global__ void __launch_bounds__(Tiles<HD, NQ>::kThreads, 1)
       // ---- the unit's end ----
       if (!(ok = waitw<false>(&sh.o_ready[qt], n_units & 1, abort_flag))) break;
       tc_after();
+      // O leaves through shared memory, 32 columns of the warp's rows at a time (16-byte
+      // pieces swizzled), so that whole lines of several rows go out together:
+      // 64 bytes a row of o, 128 of the partials.
       const float inv = l > 0.f ? 1.f / l : 0.f;
-      float* part = nullptr;
-      T* dst = nullptr;
-      if (u.slot >= 0) {
-        part = p.part + ((int64_t)u.slot * p.part_rows + ru) * HD;
-        if (live) p.ml[(int64_t)u.slot * p.part_rows + ru] = make_float2(m_ref, l);
-      } else {
-        dst = static_cast<T*>(p.o) + (int64_t)(u.row0 + ru / p.G) * p.o_row + (int64_t)(u.h * p.G + ru % p.G) * p.o_head;
-      }
+      const bool cut = u.slot >= 0;
+      if (cut && live) p.ml[(int64_t)u.slot * p.part_rows + ru] = make_float2(m_ref, l);
+      const uint32_t mine = su32(stage) + (warp - 3) * 4096;
+      int64_t at = -1;  // where this thread's row goes, in elements
+      if (live)
+        at = cut ? ((int64_t)u.slot * p.part_rows + ru) * HD
+                 : (int64_t)(u.row0 + ru / p.G) * p.o_row + (int64_t)(u.h * p.G + ru % p.G) * p.o_head;
+      const int lanes = cut ? 8 : 4;  // of a row
 #pragma unroll 1
-      for (int chunk = 0; chunk < HD / 64; ++chunk) {
-        uint32_t o[64];
-        tmem_ld32(lane_addr + col_o + 64 * chunk, o);
-        tmem_ld32(lane_addr + col_o + 64 * chunk + 32, o + 32);
+      for (int col = 0; col < HD; col += 32) {
+        uint32_t o[32];
+        tmem_ld32(lane_addr + col_o + col, o);
         tmem_wait_ld(o);
-        tmem_wait_ld(o + 32);
-        if (chunk == HD / 64 - 1) {  // the next unit's P V may start O afresh
+        if (col == HD - 32) {  // the next unit's P V may start O afresh
           tc_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&sh.o_free[qt]);
         }
-        if (!live) continue;
-        if (part) {
+        if (cut) {
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
-            reinterpret_cast<float4*>(part + 64 * chunk)[e] =
-                make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]), __uint_as_float(o[4 * e + 2]),
-                            __uint_as_float(o[4 * e + 3]));
+          for (int e = 0; e < 8; ++e)
+            st_shared_v4(mine + lane * 128 + ((e ^ (lane & 7)) << 4), o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
         } else {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            float v[8];
+          for (int e = 0; e < 16; ++e) o[e] = Pack<T>::two(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] = __uint_as_float(o[8 * e + k]) * inv;
-            store_out<T, 8>(dst + 64 * chunk + 8 * e, v, p.o_wide);
+          for (int e = 0; e < 4; ++e)
+            st_shared_v4(mine + lane * 64 + ((e ^ ((lane >> 1) & 3)) << 4), o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+        }
+        __syncwarp();
+        const int piece = lane & (lanes - 1);
+#pragma unroll 2
+        for (int i = 0; i < lanes; ++i) {
+          const int row = i * (32 / lanes) + lane / lanes;
+          const int64_t to = __shfl_sync(0xffffffffu, at, row);
+          uint4 x;
+          const uint32_t from = cut ? mine + row * 128 + ((piece ^ (row & 7)) << 4) : mine + row * 64 + ((piece ^ ((row >> 1) & 3)) << 4);
+          asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(from)
+                       : "memory");
+          if (to < 0) continue;
+          if (cut) {
+            *reinterpret_cast<uint4*>(p.part + to + col + 4 * piece) = x;
+          } else {
+            T* dst = static_cast<T*>(p.o) + to + col + 8 * piece;
+            if (p.o_wide) {
+              *reinterpret_cast<uint4*>(dst) = x;
+            } else {
+              const uint32_t y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+              for (int k = 0; k < 8; ++k) reinterpret_cast<uint16_t*>(dst)[k] = (uint16_t)(y[k / 2] >> (16 * (k & 1)));
+            }
           }
         }
+        __syncwarp();
       }
     }
   }
