@@ -620,6 +620,7 @@ extern "C" int stv_paged_attn(const stv_shape* shape, const stv_attn_spec* spec,
     if (p.q_wide && (rc = make_q_map(q, sh, n_rows, kMaxRows / sh.G, &p.map_q))) return rc;
   }
   p.tile_bits = a.small ? 6 : 7;
+  p.unit_cost = a.small ? 1 : 2;
   p.tables = pool->tables;
   p.counts = pool->counts;
   p.table_stride = pool->table_stride;

@@ -5,11 +5,12 @@
 // at most 16 or 128 (256) rows of Q that read the same keys.  Its keys come in
 // tiles of 64 (single tokens) or 128: those of the first tokens (sinks) that lie before the window's
 // first tile, then the window's (or all up to the last visible key).  All tiles
-// of all units, in the order (entry, unit, head, tile), are cut into as many
-// equal runs as there are CTAs.  A unit inside one CTA's run is finished there;
+// of all units, in the order (entry, unit, head, tile), each unit's after a
+// few tiles' worth for its Q and its end, are cut into as many equal runs as there
+// are CTAs.  A unit inside one CTA's run is finished there;
 // a unit cut by the runs' borders leaves partials (O, and the running maximum and
 // sum of each row), at most two per CTA, which the join kernel puts together in
-// the runs' order.  So every CTA has the same number of tiles whatever the
+// the runs' order.  So every CTA has the same work whatever the
 // lengths, a single long sequence is spread over all SMs, and the result
 // depends on the lengths alone.
 //
@@ -56,6 +57,7 @@ struct AttnParams {
   int hkv, G;
   int tokens_per;  // new tokens of a unit
   int tile_bits;   // log2 of a tile's keys
+  int unit_cost;   // what a unit costs beside its tiles, in tiles
   int window, sinks, causal;
   float scale2;  // scale * log2(e)
   bool q_wide, o_wide;  // 16-byte loads of q, stores of o
@@ -178,8 +180,8 @@ __device__ __forceinline__ long long cta_scan(long long x, long long* total) {
 
 // Where a CTA's run begins, and its length in tiles.
 struct RunStart {
-  int e, u, h, t;         // entry, unit, head, tile
-  long long left, share;  // tiles of the run, of a full run
+  int e, u, h, off;       // entry, unit, head, and how far into that unit (its cost first, then its tiles)
+  long long left, share;  // length of the run, of a full run
 };
 
 // Whole CTA; scratch: n + 1 ints of shared memory, free afterwards.  Ends with
@@ -237,7 +239,7 @@ __device__ __forceinline__ RunStart run_of(const AttnParams& p, int* scratch) {
         en = entry_of(p, e);
         have = true;
       }
-      if (!f(e, g - scratch[e], unit_of(p, en, g - scratch[e]).n_tiles)) return;
+      if (!f(e, g - scratch[e], unit_of(p, en, g - scratch[e]).n_tiles + p.unit_cost)) return;
     }
   };
   walk([&](int, int, int n) {
@@ -256,7 +258,7 @@ __device__ __forceinline__ RunStart run_of(const AttnParams& p, int* scratch) {
         start.e = e;
         start.u = u;
         start.h = (int)((f0 - f) / n);
-        start.t = (int)((f0 - f) % n);
+        start.off = (int)((f0 - f) % n);
         start.left = min(share, total - f0);
         start.share = share;
         return false;
@@ -275,19 +277,21 @@ struct RunWalk {
   RunStart at;
   Entry en;
   AttnUnit x;
-  int t0, t1;  // tiles of this part
+  int t0, t1;  // tiles of this part, one at least
   bool any;
 
   __device__ RunWalk(const AttnParams& p_, const RunStart& s) : p(p_), at(s), any(s.left > 0) {
     if (any) {
       en = entry_of(p, at.e);
       open();
+      if (t0 == t1) next();
     }
   }
   __device__ void open() {
     x = unit_of(p, en, at.u);
-    t0 = at.t;
-    t1 = (int)min((long long)x.n_tiles, t0 + at.left);
+    const int from = at.off - p.unit_cost;
+    t0 = max(0, from);
+    t1 = (int)max((long long)t0, min((long long)x.n_tiles, from + at.left));
   }
   // The workspace slot of this part's partials; -1: the unit is whole.
   __device__ int slot() const {
@@ -301,20 +305,22 @@ struct RunWalk {
     return (int)(blockIdx.x + (rest + at.share - 1) / at.share);
   }
   __device__ bool next() {
-    at.left -= t1 - t0;
-    at.t = 0;
-    if (at.left <= 0) return any = false;
-    if (++at.h == p.hkv) {
-      at.h = 0;
-      if (++at.u * p.tokens_per >= en.L) {
-        at.u = 0;
-        do {
-          if (++at.e >= p.n) return any = false;
-          en = entry_of(p, at.e);
-        } while (en.L == 0);
+    do {
+      at.left -= x.n_tiles + p.unit_cost - at.off;
+      at.off = 0;
+      if (at.left <= p.unit_cost) return any = false;  // not a tile more
+      if (++at.h == p.hkv) {
+        at.h = 0;
+        if (++at.u * p.tokens_per >= en.L) {
+          at.u = 0;
+          do {
+            if (++at.e >= p.n) return any = false;
+            en = entry_of(p, at.e);
+          } while (en.L == 0);
+        }
       }
-    }
-    open();
+      open();
+    } while (t0 == t1);
     return true;
   }
 };

@@ -146,7 +146,6 @@ __global__ void __launch_bounds__(Tiles<HD, NQ>::kThreads, 1)
   __syncthreads();
   tc_after();
   const uint32_t tmem = sh.tmem_base;
-  const int n_tiles = (int)min(start.left, (long long)1 << 28);  // of the run (a CTA has far fewer keys to read)
 
   // The unit of the n-th entry, once it is known.
   auto unit_at = [&](int n, UnitInfo* u) -> bool {
@@ -198,7 +197,10 @@ __global__ void __launch_bounds__(Tiles<HD, NQ>::kThreads, 1)
           if (g + 1 >= C::kAhead && ok) issue(v_rows[C::kAhead - 1], true);
         }
       }
-      if (C::kAhead == 2 && g > 0 && ok) issue(v_rows[0], true);
+      if (C::kAhead == 2 && g > 0 && ok) {  // V of tile g is the (2 g + kAhead)-th, the last one too
+        issue(-1, false);
+        if (ok) issue(v_rows[0], true);
+      }
       if (ok) {
         // (the place of a unit kUnits ago, which is done with)
         sh.unit[n_units % kUnits].t0 = sh.unit[n_units % kUnits].t1 = 0;
@@ -220,7 +222,6 @@ __global__ void __launch_bounds__(Tiles<HD, NQ>::kThreads, 1)
     // (an MMA takes 140 cycles to issue otherwise).  What a step waits for is probed
     // at once, ahead of the issue.
     auto same = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
-    const int n_mine = same(n_tiles);
     int qk_unit = 0, qk_left = 0;    // units whose S has begun; tiles of the last one still to come
     int pv_unit = 0, pv_left = 0;    // the same for P V
     bool pv_first = false, ok = true;
@@ -255,17 +256,18 @@ __global__ void __launch_bounds__(Tiles<HD, NQ>::kThreads, 1)
       }
       return y;
     };
+    // Whether the run has another tile for S; at a unit's first, its Q is waited for.
+    auto more_qk = [&]() -> bool {
+      if (qk_left > 0) return true;
+      UnitInfo u;
+      if (!(ok = unit_at(qk_unit, &u))) return false;
+      qk_left = same(u.t1 - u.t0);
+      if (qk_left == 0) return false;  // the run has ended
+      return ok = waitw<false>(&sh.q_full, qk_unit++ & 1, abort_flag);
+    };
     // S of a step (K of its tile is at k and has landed).
-    auto issue_qk = [&](int qt, int b, Place k) -> bool {
-      if (qt == 0) {
-        if (qk_left == 0) {
-          UnitInfo u;
-          if (!unit_at(qk_unit, &u) || !waitw<false>(&sh.q_full, qk_unit & 1, abort_flag)) return false;
-          qk_left = same(u.t1 - u.t0);
-          ++qk_unit;
-        }
-        --qk_left;
-      }
+    auto issue_qk = [&](int qt, int b, Place k) {
+      if (qt == 0) --qk_left;
       tc_after();
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
@@ -279,21 +281,22 @@ __global__ void __launch_bounds__(Tiles<HD, NQ>::kThreads, 1)
       }
       tc_commit(&sh.s_full[b]);
       if (qt == NQ - 1 && qk_left == 0) tc_commit(&sh.q_empty);
-      return true;
     };
-    // K of the tile `ahead` follows V of this one; before it, K of the first tiles.
+    // In the ring: K of the first tiles, then V of a tile and K of the one kAhead further.
     Place v = {0, 0};
-    if (n_mine > 0) {
-      for (int i = 0; i < C::kAhead && i < n_mine && ok; ++i) {
-        if (!(ok = wait_landed(v))) break;
-        for (int qt = 0; qt < NQ && ok; ++qt) ok = issue_qk(qt, (i * NQ + qt) & 1, v);
-        v = plus(v, NP);
-      }
+    bool more = true;
+    for (int i = 0; i < C::kAhead && more; ++i) {
+      if (!(more = more_qk()) || !(ok = wait_landed(v))) break;
+      for (int qt = 0; qt < NQ; ++qt) issue_qk(qt, (i * NQ + qt) & 1, v);
+      v = plus(v, NP);
     }
-    uint32_t s_ph = 0;  // phase of both S buffers' steps
-    for (int g = 0; g < n_mine && ok; ++g) {
-      const Place k = plus(v, NP);
-      const bool more = g + C::kAhead < n_mine;
+    if (C::kAhead == 2 && qk_unit > 0 && !more && ok) v = plus(v, NP);  // a run of one tile
+    int tiles_left = 0;  // of those whose S has been issued
+    if (qk_unit > 0) tiles_left = C::kAhead == 2 && more ? 2 : 1;
+    // seen: what the next step waits for was there already when it was looked at.
+    uint32_t seen_vk = 0, seen_p = 0;
+    for (int g = 0; ok && tiles_left > 0; ++g) {
+      const Place k = plus(v, NP), v_next = plus(k, NP);
       if ((pv_first = pv_left == 0)) {
         UnitInfo u;
         if (!(ok = unit_at(pv_unit, &u))) break;
@@ -301,17 +304,17 @@ __global__ void __launch_bounds__(Tiles<HD, NQ>::kThreads, 1)
         ++pv_unit;
       }
       --pv_left;
+      --tiles_left;
 #pragma unroll
       for (int qt = 0; qt < NQ; ++qt) {
         const int b = NQ == 2 ? qt : (g & 1);
-        if (NQ == 1 || qt == 0) s_ph = (NQ == 2 ? g : g >> 1) & 1;
-        const uint32_t seen_v = qt == 0 ? landed(v) : 1u, seen_k = qt == 0 && more ? landed(k) : 1u;
-        const uint32_t seen_0 = probe(&sh.p_full[b][0], s_ph);
-        const bool there_v = __all_sync(0xffffffffu, seen_v), there_k = __all_sync(0xffffffffu, seen_k);
-        if (!there_v && !(ok = wait_landed(v))) break;
+        const uint32_t ph = (NQ == 2 ? g : g >> 1) & 1;
+        if (qt == 0 && !__all_sync(0xffffffffu, seen_vk) && !(ok = wait_landed(v))) break;
         // the unit's first P V restarts O: the previous unit's O has been read
         if (pv_first && pv_unit > 1 && !(ok = waitw<false>(&sh.o_free[qt], (pv_unit - 2) & 1, abort_flag))) break;
-        if (!(ok = settle<false>(&sh.p_full[b][0], s_ph, seen_0, abort_flag))) break;
+        if (!(ok = settle<false>(&sh.p_full[b][0], ph, seen_p, abort_flag))) break;
+        const uint32_t seen_1 = probe(&sh.p_full[b][1], ph);
+        const uint32_t seen_k = qt == 0 && more ? landed(k) : 1u;
         auto issue_pv = [&](int half) {
           tc_after();
 #pragma unroll
@@ -324,17 +327,25 @@ __global__ void __launch_bounds__(Tiles<HD, NQ>::kThreads, 1)
           }
         };
         issue_pv(0);
-        const uint32_t seen_1 = probe(&sh.p_full[b][1], s_ph);
-        if (!(ok = settle<false>(&sh.p_full[b][1], s_ph, seen_1, abort_flag))) break;
+        if (!(ok = settle<false>(&sh.p_full[b][1], ph, seen_1, abort_flag))) break;
         issue_pv(1);
         tc_commit(&sh.pv_done[qt]);
         if (pv_left == 0) tc_commit(&sh.o_ready[qt]);
-        if (more) {
-          if (!there_k && !(ok = wait_landed(k))) break;
-          if (!(ok = issue_qk(qt, b, k))) break;
+        // what the next step waits for, looked at while the next MMAs are issued
+        const int qn = NQ == 2 ? qt ^ 1 : 0, gn = g + (qn == 0);
+        seen_p = probe(&sh.p_full[NQ == 2 ? qn : (gn & 1)][0], (NQ == 2 ? gn : gn >> 1) & 1);
+        if (qn == 0) seen_vk = landed(v_next);
+        if (qt == 0 && more) {
+          more = more_qk();
+          if (!ok) break;
+          if (more) {
+            ++tiles_left;
+            if (!__all_sync(0xffffffffu, seen_k) && !(ok = wait_landed(k))) break;
+          }
         }
+        if (more) issue_qk(qt, b, k);
       }
-      v = plus(v, more ? 2 * NP : NP);
+      v = v_next;
     }
     // Every MMA issued here has finished before TMEM is freed.
     tc_commit(&sh.mma_done);
@@ -413,14 +424,16 @@ __global__ void __launch_bounds__(Tiles<HD, NQ>::kThreads, 1)
           tmem_wait_ld(s + 32);
           if (edge) {
             const uint64_t vis = absent ? 0ull : row_sees(p, pos, u.x.end, key0 + 64 * half);
-            const uint32_t va = (uint32_t)vis, vb = (uint32_t)(vis >> 32);
+            if (!__all_sync(0xffffffffu, vis == ~0ull)) {
+              const uint32_t va = (uint32_t)vis, vb = (uint32_t)(vis >> 32);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              s[e] = ((va >> e) & 1u) ? s[e] : 0xff800000u;
-              s[32 + e] = ((vb >> e) & 1u) ? s[32 + e] : 0xff800000u;
+              for (int e = 0; e < 32; ++e) {
+                s[e] = ((va >> e) & 1u) ? s[e] : 0xff800000u;
+                s[32 + e] = ((vb >> e) & 1u) ? s[32 + e] : 0xff800000u;
+              }
+              tmem_st32(col_s + 64 * half, s);
+              tmem_st32(col_s + 64 * half + 32, s + 32);
             }
-            tmem_st32(col_s + 64 * half, s);
-            tmem_st32(col_s + 64 * half + 32, s + 32);
           }
           // 3-input max, 8 independent chains
           float mx8[8];
@@ -437,7 +450,7 @@ __global__ void __launch_bounds__(Tiles<HD, NQ>::kThreads, 1)
           if (qt == 0) {
             const uint64_t some0 = absent ? 0ull : unit_sees(p, u.x, key0), some1 = absent ? 0ull : unit_sees(p, u.x, key0 + 64);
             if ((some0 & some1) != ~0ull) {
-              const int p0 = (g + min(g + C::kAhead, n_tiles)) * NP;
+              const int p0 = (2 * g + C::kAhead) * NP;
 #pragma unroll 1
               for (int i = 0; i < NP && ok; ++i) ok = waitw<false>(&sh.full[(p0 + i) % R], ((p0 + i) / R) & 1, abort_flag);
               if (!ok) break;
@@ -527,7 +540,7 @@ __global__ void __launch_bounds__(Tiles<HD, NQ>::kThreads, 1)
       if (live)
         at = cut ? ((int64_t)u.slot * p.part_rows + ru) * HD
                  : (int64_t)(u.row0 + ru / p.G) * p.o_row + (int64_t)(u.h * p.G + ru % p.G) * p.o_head;
-      const int lanes = cut ? 8 : 4;  // of a row
+      const int bits = cut ? 3 : 2;  // log2 of a row's lanes
 #pragma unroll 1
       for (int col = 0; col < HD; col += 32) {
         uint32_t o[32];
@@ -550,10 +563,10 @@ __global__ void __launch_bounds__(Tiles<HD, NQ>::kThreads, 1)
             st_shared_v4(mine + lane * 64 + ((e ^ ((lane >> 1) & 3)) << 4), o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
         }
         __syncwarp();
-        const int piece = lane & (lanes - 1);
+        const int piece = lane & ((1 << bits) - 1);
 #pragma unroll 2
-        for (int i = 0; i < lanes; ++i) {
-          const int row = i * (32 / lanes) + lane / lanes;
+        for (int i = 0; i < 1 << bits; ++i) {
+          const int row = (i << (5 - bits)) + (lane >> bits);
           const int64_t to = __shfl_sync(0xffffffffu, at, row);
           uint4 x;
           const uint32_t from = cut ? mine + row * 128 + ((piece ^ (row & 7)) << 4) : mine + row * 64 + ((piece ^ ((row >> 1) & 3)) << 4);
