@@ -109,6 +109,7 @@ __global__ void __launch_bounds__(kThreads, Small<HD>::kCtasPerSm)
     // =================== producer (whole warp; lane 0 issues) ===================
     RunWalk run(p, start);
     JoinRecord rec = {0, 0, 0, 0};
+    PageWalk pages;
     int g = 0, n_units = 0;
     bool ok = true;
     for (; ok && run.any; run.next(), ++n_units) {
@@ -119,7 +120,7 @@ __global__ void __launch_bounds__(kThreads, Small<HD>::kCtasPerSm)
         const int st = g % kStages;
         if (!(ok = waitw<false>(&sh.empty[st], ((g / kStages) & 1) ^ 1, abort_flag))) break;
         const int key0 = tile_key(p, run.x, t);
-        const int row = tile_row(p, run.en.s, run.at.h, key0);
+        const int row = pages.row(p, run.en, run.at.h, key0);
         if (lane == 0) {
           TileInfo& i = sh.info[st];
           i.flags = (t == run.t0 ? kFirst : 0) | (t + 1 == run.t1 ? kLast : 0) | (row < 0 ? kAbsent : 0) |
@@ -615,8 +616,8 @@ extern "C" int stv_paged_attn(const stv_shape* shape, const stv_attn_spec* spec,
   if (a.small) {
     if ((rc = make_pool_map(layer, sh, kSmallTile, sh.hd / 64, &p.map_k))) return rc;
   } else {
-    if ((rc = make_pool_map(layer, sh, kBigTile, 1, &p.map_k))) return rc;
-    if ((rc = make_pool_map(layer, sh, 8192 / sh.hd, sh.hd / 64, &p.map_v))) return rc;
+    if ((rc = make_pool_map(layer, sh, kBigTile, big_piece_bytes(sh.hd) / 16384, &p.map_k))) return rc;
+    if ((rc = make_pool_map(layer, sh, big_piece_bytes(sh.hd) / (2 * sh.hd), sh.hd / 64, &p.map_v))) return rc;
     if (p.q_wide && (rc = make_q_map(q, sh, n_rows, kMaxRows / sh.G, &p.map_q))) return rc;
   }
   p.tile_bits = a.small ? 6 : 7;

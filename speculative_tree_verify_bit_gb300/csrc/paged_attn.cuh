@@ -29,6 +29,9 @@ namespace stv {
 
 constexpr int kSmallTile = 64;      // keys of a tile, single tokens
 constexpr int kBigTile = 128;       // blocks and prompts
+// K and V of such a tile move in pieces: a copy's waits and issue take some 330
+// cycles, whatever its size, so 32 KB where a tile has as much.
+__host__ __device__ constexpr int big_piece_bytes(int hd) { return hd == 64 ? 16384 : 32768; }
 constexpr int kMaxEntries = 4096;
 constexpr int kMaxCtx = 1 << 30;
 constexpr int kSmallRows = 16;      // rows of Q per unit, single tokens
@@ -41,7 +44,7 @@ struct JoinRecord {
 
 struct AttnParams {
   // The pool as [hd / 64][rows][64 channels], in boxes of a tile of K and V
-  // (single tokens: the same map), or of a 16 KB piece of one; q as
+  // (single tokens: the same map), or of a piece of one; q as
   // [rows][heads][hd / 64][64], in boxes of a row tile's 64 channels.
   CUtensorMap map_k, map_v, map_q;
   const void* q;
@@ -325,18 +328,29 @@ struct RunWalk {
   }
 };
 
-// Row of the map (a key's row of K; V's is 256 further) of the tile at key0, or
-// -1 where the sequence has no page there.
-__device__ __forceinline__ int tile_row(const AttnParams& p, int s, int h, int key0) {
-  const int lp = key0 / kPageTok;
-  const int have = min(__ldg(p.counts + s), p.table_stride);
-  const int page = lp < have ? __ldg(p.tables + (int64_t)s * p.table_stride + lp) : -1;
-  if (page < 0 || page >= p.n_pages) {
-    report(p.status, STV_DEV_BAD_PAGE);
-    return -1;
+// Rows of the map where tiles begin (a key's row of K; V's is 256 further), or -1
+// where the sequence has no page; the next page's number is on its way ahead.
+struct PageWalk {
+  int s = -1, lp, page, next;
+
+  __device__ __forceinline__ int look(const AttnParams& p, const Entry& e, int at) const {
+    return at * kPageTok < e.keys ? __ldg(p.tables + (int64_t)e.s * p.table_stride + at) : -1;
   }
-  return (page * p.hkv + h) * (2 * kPageTok) + key0 % kPageTok;
-}
+  __device__ __forceinline__ int row(const AttnParams& p, const Entry& e, int head, int key0) {
+    const int at = key0 / kPageTok;
+    if (s != e.s || at != lp) {
+      page = s == e.s && at == lp + 1 ? next : look(p, e, at);
+      s = e.s;
+      lp = at;
+      next = look(p, e, at + 1);
+    }
+    if (page < 0 || page >= p.n_pages) {
+      report(p.status, STV_DEV_BAD_PAGE);
+      return -1;
+    }
+    return (page * p.hkv + head) * (2 * kPageTok) + key0 % kPageTok;
+  }
+};
 
 __device__ __forceinline__ void tma_box(void* dst, const CUtensorMap* map, int row, int block, uint64_t* bar) {
   asm volatile(

@@ -11,9 +11,8 @@
 // V as it lies in the cache (keys x channels: the MN-major operand).  Q is in
 // shared memory: tensor memory holds two S and O, 512 columns.
 //
-// K and V pass through one ring of 16 KB pieces (K: 128 keys of 64 channels, V:
-// 8,192 / head_dim keys of all channels) in the order in which the MMAs take
-// them.  A step is (tile of keys, row tile); S of step n + 2 is formed after P V
+// K and V pass through one ring of pieces (K: 128 keys of 64 or 128 channels, V:
+// 64 or 128 keys of all channels) in the order in which the MMAs take them.  A step is (tile of keys, row tile); S of step n + 2 is formed after P V
 // of step n, so the tensor pipe works while a softmax runs: with two row tiles
 // they take turns, with one the tiles of keys do.  P is handed over in halves.
 // The order runs on across units; only O waits to be read at a unit's end.
@@ -28,18 +27,21 @@ namespace stv {
 namespace {
 
 constexpr float kRescaleThreshold = 8.f;  // log2 units
-constexpr int kPiece = 16384;
 constexpr int kUnits = 16;  // units that the producer may be ahead; a unit has a tile at least
 
 template <int HD, int NQ>
 struct Tiles {
   static constexpr int kQTile = kMaxRows * HD * 2;
-  static constexpr int kPieces = HD / 64;        // of K's tile, and of V's
-  static constexpr int kVKeys = 8192 / HD;       // keys of a piece of V
+  static constexpr int kPiece = big_piece_bytes(HD);
+  static constexpr int kPieces = kBigTile * HD * 2 / kPiece;  // of K's tile, and of V's
+  static constexpr int kKBlocks = kPiece / 16384;             // blocks of 64 channels in a piece of K
+  static constexpr int kVKeys = kPiece / (2 * HD);            // keys of a piece of V
   static constexpr int kAhead = 2 / NQ;          // tiles of keys that S runs ahead
   static constexpr int kStage = NQ * 16384;      // 32 rows x 128 bytes for each softmax warp: O on its way out
-  static constexpr int kRing = (232448 - 1024 - 2048 - NQ * kQTile - kStage) / kPiece < 10
-                                   ? (232448 - 1024 - 2048 - NQ * kQTile - kStage) / kPiece : 10;
+  static constexpr int kFits = (232448 - 1024 - 2048 - NQ * kQTile - kStage) / kPiece;
+  static constexpr int kRing = kFits < 8 ? kFits : 8;
+  // (a step looks at a place's barrier up to two tiles ahead of the last that landed)
+  static_assert(kRing >= 2 * kPieces, "two tiles in the ring");
   static_assert(kRing / kPieces / 2 + kAhead + 2 < kUnits, "units in flight");
   static constexpr int kSmem = 1024 + NQ * kQTile + kStage + kRing * kPiece;
   static constexpr int kThreads = 96 + 128 * NQ;
@@ -99,7 +101,7 @@ template <typename T, int HD, int NQ>
 __global__ void __launch_bounds__(Tiles<HD, NQ>::kThreads, 1)
     attn_tiles_kernel(const __grid_constant__ AttnParams p) {
   using C = Tiles<HD, NQ>;
-  constexpr int R = C::kRing, NP = C::kPieces;
+  constexpr int R = C::kRing, NP = C::kPieces, kPiece = C::kPiece;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ TilesShared<HD, NQ> sh;
   uint8_t* smem = smem_raw + ((1024 - (su32(smem_raw) & 1023)) & 1023);
@@ -159,20 +161,27 @@ __global__ void __launch_bounds__(Tiles<HD, NQ>::kThreads, 1)
     if (lane == 0) {
       RunWalk run(p, start);
       JoinRecord rec = {0, 0, 0, 0};
-      int g = 0, piece = 0, n_units = 0;
+      PageWalk pages;
+      int g = 0, n_units = 0, st = 0, n_issued = 0;
+      uint32_t ph = 1;
       int v_rows[C::kAhead + 1];  // of tiles whose K is on its way
       bool ok = true;
       auto issue = [&](int row, bool v) {
-        for (int i = 0; ok && i < NP; ++i, ++piece) {
-          const int st = piece % R;
-          if (!(ok = wait1<false>(&sh.empty[st], ((piece / R) & 1) ^ 1, abort_flag))) return;
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+          if (!ok || !(ok = wait1<false>(&sh.empty[st], ph, abort_flag))) return;
           uint8_t* dst = ring + st * kPiece;
           if (row < 0) {
             mbar_arrive(&sh.full[st]);
           } else {
             mbar_expect_tx(&sh.full[st], kPiece);
             if (v) tma_box(dst, &p.map_v, row + kPageTok + i * C::kVKeys, 0, &sh.full[st]);
-            else tma_box(dst, &p.map_k, row, i, &sh.full[st]);
+            else tma_box(dst, &p.map_k, row, i * C::kKBlocks, &sh.full[st]);
+          }
+          ++n_issued;
+          if (++st == R) {
+            st = 0;
+            ph ^= 1u;
           }
         }
       };
@@ -188,7 +197,7 @@ __global__ void __launch_bounds__(Tiles<HD, NQ>::kThreads, 1)
         if (u.slot == 2 * (int)blockIdx.x + 1) rec = {u.row0, u.rows, u.h, run.last_cta()};
         mbar_arrive(&sh.unit_full[n_units % kUnits]);
         for (int t = run.t0; ok && t < run.t1; ++t, ++g) {
-          const int row = tile_row(p, run.en.s, run.at.h, tile_key(p, run.x, t));
+          const int row = pages.row(p, run.en, run.at.h, tile_key(p, run.x, t));
           sh.absent[g % 32] = row < 0;
           issue(row, false);
 #pragma unroll
@@ -209,7 +218,7 @@ __global__ void __launch_bounds__(Tiles<HD, NQ>::kThreads, 1)
       p.rec[blockIdx.x] = rec;
       // No copy may still be landing when the CTA exits.
       volatile int never = 0;
-      for (int j = max(0, piece - R); j < piece; ++j) wait1<false>(&sh.full[j % R], (j / R) & 1, &never);
+      for (int j = max(0, n_issued - R); j < n_issued; ++j) wait1<false>(&sh.full[j % R], (j / R) & 1, &never);
     }
   } else if (warp == 1) {
     // =================== MMA issuer (whole warp, one elected lane issues) ===================
@@ -275,8 +284,10 @@ __global__ void __launch_bounds__(Tiles<HD, NQ>::kThreads, 1)
         const uint64_t kd = kdesc + (uint64_t)(z.st * (kPiece >> 4));
         const uint64_t qd = qdesc + (uint64_t)(qt * (C::kQTile >> 4) + i * (kPiece >> 4));
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          mma_smem(tm + C::kColS + 128 * b, qd + 2 * kk, kd + 2 * kk, kIdescQK, i > 0 || kk > 0);
+        for (int kk = 0; kk < 4 * C::kKBlocks; ++kk) {
+          const int at = (kk >> 2) * (16384 >> 4) + (kk & 3) * 2;
+          mma_smem(tm + C::kColS + 128 * b, qd + at, kd + at, kIdescQK, i > 0 || kk > 0);
+        }
         if (qt == NQ - 1) tc_commit(&sh.empty[z.st]);
       }
       tc_commit(&sh.s_full[b]);
@@ -362,10 +373,10 @@ __global__ void __launch_bounds__(Tiles<HD, NQ>::kThreads, 1)
       if (n > 0 && !waitw<false>(&sh.q_empty, (n - 1) & 1, abort_flag)) break;
       if (p.q_wide) {
         if (lane == 0) {
-          mbar_expect_tx(&sh.q_full, NQ * NP * tile_rows * 128);
+          mbar_expect_tx(&sh.q_full, NQ * (HD / 64) * tile_rows * 128);
           for (int qt = 0; qt < NQ; ++qt)
-            for (int i = 0; i < NP; ++i)
-              tma_q(qbuf + qt * C::kQTile + i * kPiece, &p.map_q, i, u.h * p.G, u.row0 + qt * tile_tokens, &sh.q_full);
+            for (int i = 0; i < HD / 64; ++i)
+              tma_q(qbuf + qt * C::kQTile + i * 16384, &p.map_q, i, u.h * p.G, u.row0 + qt * tile_tokens, &sh.q_full);
         } else {
           mbar_arrive(&sh.q_full);
         }
@@ -377,7 +388,7 @@ __global__ void __launch_bounds__(Tiles<HD, NQ>::kThreads, 1)
           uint32_t w[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) w[k] = __ldg(src + 2 * k) | (uint32_t)__ldg(src + 2 * k + 1) << 16;
-          st_shared_v4(su32(qbuf) + qt * C::kQTile + (c >> 3) * kPiece + r * 128 + (((c & 7) ^ (r & 7)) << 4), w[0], w[1],
+          st_shared_v4(su32(qbuf) + qt * C::kQTile + (c >> 3) * 16384 + r * 128 + (((c & 7) ^ (r & 7)) << 4), w[0], w[1],
                        w[2], w[3]);
         }
         fence_async_smem();
@@ -461,7 +472,7 @@ __global__ void __launch_bounds__(Tiles<HD, NQ>::kThreads, 1)
                 if (((m < 4 ? some0 : some1) >> (key & 63)) & 1) continue;
                 const uint32_t at = su32(ring) + (p0 + key / C::kVKeys) % R * kPiece + key % C::kVKeys * 128 + (r & 7) * 16;
 #pragma unroll
-                for (int cb = 0; cb < NP; ++cb) st_shared_v4(at + cb * (C::kVKeys * 128), 0u, 0u, 0u, 0u);
+                for (int cb = 0; cb < HD / 64; ++cb) st_shared_v4(at + cb * (C::kVKeys * 128), 0u, 0u, 0u, 0u);
               }
               fence_async_smem();
             }
