@@ -14,8 +14,7 @@
 // K and V pass through one ring of pieces (K: 128 keys of 64 or 128 channels, V:
 // 64 or 128 keys of all channels) in the order in which the MMAs take them.  A step is (tile of keys, row tile); S of step n + 2 is formed after P V
 // of step n, so the tensor pipe works while a softmax runs: with two row tiles
-// they take turns, with one the tiles of keys do.  P is handed over in halves.
-// The order runs on across units; only O waits to be read at a unit's end.
+// they take turns, with one the tiles of keys do.  The order runs on across units; only O waits to be read at a unit's end.
 //
 // Keys that no row sees are cleared in V, since 0 times what a reused page holds
 // there could be NaN.  Every wait is bounded; a timeout sets a CTA abort flag,
@@ -38,10 +37,10 @@ struct Tiles {
   static constexpr int kVKeys = kPiece / (2 * HD);            // keys of a piece of V
   static constexpr int kAhead = 2 / NQ;          // tiles of keys that S runs ahead
   static constexpr int kStage = NQ * 16384;      // 32 rows x 128 bytes for each softmax warp: O on its way out
-  static constexpr int kFits = (232448 - 1024 - 2048 - NQ * kQTile - kStage) / kPiece;
-  static constexpr int kRing = kFits < 8 ? kFits : 8;
-  // (a step looks at a place's barrier up to two tiles ahead of the last that landed)
-  static_assert(kRing >= 2 * kPieces, "two tiles in the ring");
+  // Two tiles of K and V, or one where they are large: every place in the ring is
+  // known when the loop over two tiles is compiled.
+  static constexpr int kDeep = HD == 256 ? 1 : 2;
+  static constexpr int kRing = 2 * kPieces * kDeep;
   static_assert(kRing / kPieces / 2 + kAhead + 2 < kUnits, "units in flight");
   static constexpr int kSmem = 1024 + NQ * kQTile + kStage + kRing * kPiece;
   static constexpr int kThreads = 96 + 128 * NQ;
@@ -61,7 +60,7 @@ template <int HD, int NQ>
 struct TilesShared {
   uint64_t full[Tiles<HD, NQ>::kRing], empty[Tiles<HD, NQ>::kRing];
   uint64_t unit_full[kUnits];
-  uint64_t s_full[2], p_full[2][2], pv_done[NQ], q_full, q_empty, o_ready[NQ], o_free[NQ], mma_done;
+  uint64_t s_full[2], p_full[2], pv_done, q_full, q_empty, o_ready[NQ], o_free[NQ], mma_done;
   UnitInfo unit[kUnits];
   uint8_t absent[32];  // of tile g % 32: no page there
   uint32_t tmem_base;
@@ -120,14 +119,13 @@ __global__ void __launch_bounds__(Tiles<HD, NQ>::kThreads, 1)
     for (int i = 0; i < kUnits; ++i) mbar_init(&sh.unit_full[i], 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.s_full[i], 1);
-      mbar_init(&sh.p_full[i][0], 4);
-      mbar_init(&sh.p_full[i][1], 4);
+      mbar_init(&sh.p_full[i], 4);
     }
     for (int i = 0; i < NQ; ++i) {
-      mbar_init(&sh.pv_done[i], 1);
       mbar_init(&sh.o_ready[i], 1);
       mbar_init(&sh.o_free[i], 4);
     }
+    mbar_init(&sh.pv_done, 1);
     mbar_init(&sh.q_full, 32);
     mbar_init(&sh.q_empty, 1);
     mbar_init(&sh.mma_done, 1);
@@ -234,35 +232,17 @@ __global__ void __launch_bounds__(Tiles<HD, NQ>::kThreads, 1)
     int qk_unit = 0, qk_left = 0;    // units whose S has begun; tiles of the last one still to come
     int pv_unit = 0, pv_left = 0;    // the same for P V
     bool pv_first = false, ok = true;
-    // A place in the ring, and the phase there.
-    struct Place {
-      int st;
-      uint32_t ph;
-    };
-    auto plus = [&](Place x, int i) -> Place {  // i < R
-      x.st += i;
-      if (x.st >= R) {
-        x.st -= R;
-        x.ph ^= 1u;
-      }
-      return x;
-    };
-    auto landed = [&](Place x) -> uint32_t {
+    // K or V of a tile lies in pieces st, st + 1, ...; ph: their phase.
+    auto landed = [&](int st, uint32_t ph) -> uint32_t {
       uint32_t y = 1;
 #pragma unroll
-      for (int i = 0; i < NP; ++i) {
-        const Place z = plus(x, i);
-        y &= probe(&sh.full[z.st], z.ph);
-      }
+      for (int i = 0; i < NP; ++i) y &= probe(&sh.full[st + i], ph);
       return y;
     };
-    auto wait_landed = [&](Place x) -> bool {
+    auto wait_landed = [&](int st, uint32_t ph) -> bool {
       bool y = true;
 #pragma unroll 1
-      for (int i = 0; i < NP && y; ++i) {
-        const Place z = plus(x, i);
-        y = waitw<false>(&sh.full[z.st], z.ph, abort_flag);
-      }
+      for (int i = 0; i < NP && y; ++i) y = waitw<false>(&sh.full[st + i], ph, abort_flag);
       return y;
     };
     // Whether the run has another tile for S; at a unit's first, its Q is waited for.
@@ -274,89 +254,85 @@ __global__ void __launch_bounds__(Tiles<HD, NQ>::kThreads, 1)
       if (qk_left == 0) return false;  // the run has ended
       return ok = waitw<false>(&sh.q_full, qk_unit++ & 1, abort_flag);
     };
-    // S of a step (K of its tile is at k and has landed).
-    auto issue_qk = [&](int qt, int b, Place k) {
+    // S of a step (K of its tile is at st and has landed).
+    auto issue_qk = [&](int qt, int b, int st) {
       if (qt == 0) --qk_left;
-      tc_after();
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
-        const Place z = plus(k, i);
-        const uint64_t kd = kdesc + (uint64_t)(z.st * (kPiece >> 4));
+        const uint64_t kd = kdesc + (uint64_t)((st + i) * (kPiece >> 4));
         const uint64_t qd = qdesc + (uint64_t)(qt * (C::kQTile >> 4) + i * (kPiece >> 4));
 #pragma unroll
         for (int kk = 0; kk < 4 * C::kKBlocks; ++kk) {
           const int at = (kk >> 2) * (16384 >> 4) + (kk & 3) * 2;
           mma_smem(tm + C::kColS + 128 * b, qd + at, kd + at, kIdescQK, i > 0 || kk > 0);
         }
-        if (qt == NQ - 1) tc_commit(&sh.empty[z.st]);
+        if (qt == NQ - 1) tc_commit(&sh.empty[st + i]);
       }
       tc_commit(&sh.s_full[b]);
       if (qt == NQ - 1 && qk_left == 0) tc_commit(&sh.q_empty);
     };
-    // In the ring: K of the first tiles, then V of a tile and K of the one kAhead further.
-    Place v = {0, 0};
+    // In the ring: K of the first tiles, then V of tile g (the (2 g + A)-th) and K of
+    // tile g + A; A = kAhead.
+    constexpr int A = C::kAhead, D = C::kDeep;
     bool more = true;
-    for (int i = 0; i < C::kAhead && more; ++i) {
-      if (!(more = more_qk()) || !(ok = wait_landed(v))) break;
-      for (int qt = 0; qt < NQ; ++qt) issue_qk(qt, (i * NQ + qt) & 1, v);
-      v = plus(v, NP);
-    }
-    if (C::kAhead == 2 && qk_unit > 0 && !more && ok) v = plus(v, NP);  // a run of one tile
     int tiles_left = 0;  // of those whose S has been issued
-    if (qk_unit > 0) tiles_left = C::kAhead == 2 && more ? 2 : 1;
-    // seen: what the next step waits for was there already when it was looked at.
-    uint32_t seen_vk = 0, seen_p = 0;
-    for (int g = 0; ok && tiles_left > 0; ++g) {
-      const Place k = plus(v, NP), v_next = plus(k, NP);
-      if ((pv_first = pv_left == 0)) {
-        UnitInfo u;
-        if (!(ok = unit_at(pv_unit, &u))) break;
-        pv_left = same(u.t1 - u.t0);
-        ++pv_unit;
-      }
-      --pv_left;
-      --tiles_left;
 #pragma unroll
-      for (int qt = 0; qt < NQ; ++qt) {
-        const int b = NQ == 2 ? qt : (g & 1);
-        const uint32_t ph = (NQ == 2 ? g : g >> 1) & 1;
-        if (qt == 0 && !__all_sync(0xffffffffu, seen_vk) && !(ok = wait_landed(v))) break;
-        // the unit's first P V restarts O: the previous unit's O has been read
-        if (pv_first && pv_unit > 1 && !(ok = waitw<false>(&sh.o_free[qt], (pv_unit - 2) & 1, abort_flag))) break;
-        if (!(ok = settle<false>(&sh.p_full[b][0], ph, seen_p, abort_flag))) break;
-        const uint32_t seen_1 = probe(&sh.p_full[b][1], ph);
-        const uint32_t seen_k = qt == 0 && more ? landed(k) : 1u;
-        auto issue_pv = [&](int half) {
+    for (int i = 0; i < A; ++i) {
+      if (!more || !(more = more_qk()) || !(more = ok = wait_landed(i * NP, 0))) continue;
+      tc_after();
+#pragma unroll
+      for (int qt = 0; qt < NQ; ++qt) issue_qk(qt, (i * NQ + qt) & 1, i * NP);
+      ++tiles_left;
+    }
+    for (int g0 = 0; ok && tiles_left > 0; g0 += 2) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        if (!ok || tiles_left == 0) break;
+        const int g = g0 + j;
+        const int v_st = (2 * j + A) % (2 * D) * NP, k_st = (2 * j + A + 1) % (2 * D) * NP;
+        const uint32_t v_ph = ((2 * g + A) / (2 * D)) & 1, k_ph = ((2 * g + A + 1) / (2 * D)) & 1;
+        if ((pv_first = pv_left == 0)) {
+          UnitInfo u;
+          if (!(ok = unit_at(pv_unit, &u))) break;
+          pv_left = same(u.t1 - u.t0);
+          ++pv_unit;
+        }
+        --pv_left;
+        --tiles_left;
+#pragma unroll
+        for (int qt = 0; qt < NQ; ++qt) {
+          const int b = NQ == 2 ? qt : j;
+          const uint32_t ph = (NQ == 2 ? g : g >> 1) & 1;
+          // all that the step waits for, looked at once
+          const uint32_t seen_p = probe(&sh.p_full[b], ph);
+          const uint32_t seen_v = qt == 0 ? landed(v_st, v_ph) : 1u, seen_k = qt == 0 ? landed(k_st, k_ph) : 1u;
+          if (!__all_sync(0xffffffffu, seen_p & seen_v)) {
+            if (qt == 0 && !(ok = wait_landed(v_st, v_ph))) break;
+            if (!(ok = waitw<false>(&sh.p_full[b], ph, abort_flag))) break;
+          }
+          // the unit's first P V restarts O: the previous unit's O has been read
+          if (pv_first && pv_unit > 1 && !(ok = waitw<false>(&sh.o_free[qt], (pv_unit - 2) & 1, abort_flag))) break;
           tc_after();
 #pragma unroll
-          for (int kk = 4 * half; kk < 4 * half + 4; ++kk) {  // 16 keys
-            const int in = kk * 16 % C::kVKeys;
-            const Place z = plus(v, kk * 16 / C::kVKeys);
+          for (int kk = 0; kk < kBigTile / 16; ++kk) {  // 16 keys
+            const int st = v_st + kk * 16 / C::kVKeys, in = kk * 16 % C::kVKeys;
             mma_tmemA(tm + C::kColO + qt * HD, tm + C::kColS + 128 * b + 8 * kk,
-                      vdesc + (uint64_t)(z.st * (kPiece >> 4) + in * (128 >> 4)), kIdescPV, !pv_first || kk > 0);
-            if (in + 16 == C::kVKeys && qt == NQ - 1) tc_commit(&sh.empty[z.st]);
+                      vdesc + (uint64_t)(st * (kPiece >> 4) + in * (128 >> 4)), kIdescPV, !pv_first || kk > 0);
+            if (in + 16 == C::kVKeys && qt == NQ - 1) tc_commit(&sh.empty[st]);
           }
-        };
-        issue_pv(0);
-        if (!(ok = settle<false>(&sh.p_full[b][1], ph, seen_1, abort_flag))) break;
-        issue_pv(1);
-        tc_commit(&sh.pv_done[qt]);
-        if (pv_left == 0) tc_commit(&sh.o_ready[qt]);
-        // what the next step waits for, looked at while the next MMAs are issued
-        const int qn = NQ == 2 ? qt ^ 1 : 0, gn = g + (qn == 0);
-        seen_p = probe(&sh.p_full[NQ == 2 ? qn : (gn & 1)][0], (NQ == 2 ? gn : gn >> 1) & 1);
-        if (qn == 0) seen_vk = landed(v_next);
-        if (qt == 0 && more) {
-          more = more_qk();
-          if (!ok) break;
-          if (more) {
-            ++tiles_left;
-            if (!__all_sync(0xffffffffu, seen_k) && !(ok = wait_landed(k))) break;
+          if (NQ == 1) tc_commit(&sh.pv_done);
+          if (pv_left == 0) tc_commit(&sh.o_ready[qt]);
+          if (qt == 0 && more) {
+            more = more_qk();
+            if (!ok) break;
+            if (more) {
+              ++tiles_left;
+              if (!__all_sync(0xffffffffu, seen_k) && !(ok = wait_landed(k_st, k_ph))) break;
+            }
           }
+          if (more) issue_qk(qt, b, k_st);
         }
-        if (more) issue_qk(qt, b, k);
       }
-      v = v_next;
     }
     // Every MMA issued here has finished before TMEM is freed.
     tc_commit(&sh.mma_done);
@@ -485,13 +461,15 @@ __global__ void __launch_bounds__(Tiles<HD, NQ>::kThreads, 1)
           m_ref = m_tile;
           l *= corr;
         }
-        // O may be rescaled only once the row tile's previous P V has finished: the
-        // one before that has (this S followed it), and the next waits for this warp,
-        // so the phase is that one's or the one before.  At a unit's first tile O
-        // holds nothing to rescale.
+        // O may be rescaled only once the row tile's previous P V has finished.  With
+        // two row tiles this S followed it; with one, this S followed the P V before
+        // that, and the next waits for this warp, so the phase is that one's or the one
+        // before.  At a unit's first tile O holds nothing to rescale.
         if (t > u.t0 && __any_sync(0xffffffffu, corr != 1.f)) {
-          if (!(ok = waitw<false>(&sh.pv_done[qt], (g - 1) & 1, abort_flag))) break;
-          tc_after();
+          if (NQ == 1) {
+            if (!(ok = waitw<false>(&sh.pv_done, (g - 1) & 1, abort_flag))) break;
+            tc_after();
+          }
           const float2 corr2 = make_float2(corr, corr);
 #pragma unroll 1
           for (int chunk = 0; chunk < HD / 32; ++chunk) {
@@ -528,11 +506,11 @@ __global__ void __launch_bounds__(Tiles<HD, NQ>::kThreads, 1)
             pk[e] = Pack<T>::two(v.x, v.y);
           }
           tmem_st32(col_s + 32 * half, pk);
-          tmem_wait_st();
-          tc_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.p_full[b][half]);
         }
+        tmem_wait_st();
+        tc_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.p_full[b]);
         const float2 sum2 = __fadd2_rn(__fadd2_rn(sum4[0], sum4[1]), __fadd2_rn(sum4[2], sum4[3]));
         l += sum2.x + sum2.y;
       }
