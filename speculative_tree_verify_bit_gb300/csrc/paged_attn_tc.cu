@@ -384,54 +384,34 @@ __global__ void __launch_bounds__(Tiles<HD, NQ>::kThreads, 1)
     int g = 0;
     bool ok = true;
     for (int n_units = 0; ok; ++n_units) {
-      UnitInfo u;
-      if (!(ok = unit_at(n_units, &u)) || u.t1 == u.t0) break;
+      if (!(ok = waitw<false>(&sh.unit_full[n_units % kUnits], (n_units / kUnits) & 1, abort_flag))) break;
+      const UnitInfo& u = sh.unit[n_units % kUnits];  // stays as it is until the unit's end
+      const int t1 = u.t1;
+      if (t1 == u.t0) break;
       const bool live = r < tile_rows && ru < u.rows;
       const int pos = u.x.pos0 + ru / p.G;
       float m_ref = -INFINITY, l = 0.f;
-      for (int t = u.t0; t < u.t1; ++t, ++g) {
+      for (int t = u.t0; t < t1; ++t, ++g) {
         const int n = g * NQ + qt, b = n & 1;
         const int key0 = tile_key(p, u.x, t);
         if (!(ok = waitw<false>(&sh.s_full[b], (n >> 1) & 1, abort_flag))) break;
         tc_after();
         const uint32_t col_s = lane_addr + C::kColS + 128 * b;
         const bool absent = sh.absent[g % 32];
-        const bool edge = absent || tile_edge(p, u.x, key0);
-        // The row's maximum, 64 columns at a time; masked columns go back as -inf.
-        // (S is read twice: a step's code stays short, which is what the
-        // instruction cache asks for; a step with its 128 columns unrolled
-        // waited for instructions longer than for anything else.)
-        float mx = -INFINITY;
+        if (absent || tile_edge(p, u.x, key0)) {
+          // Columns that the row does not see go back as -inf, 32 at a time (a loop:
+          // this path is cold, and a long one waits for its instructions).
 #pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
-          uint32_t s[64];
-          tmem_ld32(col_s + 64 * half, s);
-          tmem_ld32(col_s + 64 * half + 32, s + 32);
-          tmem_wait_ld(s);
-          tmem_wait_ld(s + 32);
-          if (edge) {
-            const uint64_t vis = absent ? 0ull : row_sees(p, pos, u.x.end, key0 + 64 * half);
-            if (!__all_sync(0xffffffffu, vis == ~0ull)) {
-              const uint32_t va = (uint32_t)vis, vb = (uint32_t)(vis >> 32);
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t vis = absent ? 0u : (uint32_t)row_sees(p, pos, u.x.end, key0 + 32 * i);
+            if (__all_sync(0xffffffffu, vis == ~0u)) continue;
+            uint32_t x[32];
+            tmem_ld32(col_s + 32 * i, x);
+            tmem_wait_ld(x);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) {
-                s[e] = ((va >> e) & 1u) ? s[e] : 0xff800000u;
-                s[32 + e] = ((vb >> e) & 1u) ? s[32 + e] : 0xff800000u;
-              }
-              tmem_st32(col_s + 64 * half, s);
-              tmem_st32(col_s + 64 * half + 32, s + 32);
-            }
+            for (int e = 0; e < 32; ++e) x[e] = ((vis >> e) & 1u) ? x[e] : 0xff800000u;
+            tmem_st32(col_s + 32 * i, x);
           }
-          // 3-input max, 8 independent chains
-          float mx8[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) mx8[e] = fmaxf(__uint_as_float(s[e]), __uint_as_float(s[8 + e]));
-#pragma unroll
-          for (int e = 16; e < 64; e += 2)
-            mx8[(e >> 1) & 7] = max3(mx8[(e >> 1) & 7], __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
-          mx = max3(mx, fmaxf(mx8[0], mx8[1]), max3(max3(mx8[2], mx8[3], mx8[4]), mx8[5], fmaxf(mx8[6], mx8[7])));
-        }
-        if (edge) {
           tmem_wait_st();
           // Keys that no row sees: zeros in V, by the first row tile's warps.
           if (qt == 0) {
@@ -441,11 +421,14 @@ __global__ void __launch_bounds__(Tiles<HD, NQ>::kThreads, 1)
 #pragma unroll 1
               for (int i = 0; i < NP && ok; ++i) ok = waitw<false>(&sh.full[(p0 + i) % R], ((p0 + i) / R) & 1, abort_flag);
               if (!ok) break;
-              // thread: 16 bytes of keys r / 8, r / 8 + 16, ... in every block of 64 channels
+              // thread: 16 bytes of keys r / 8 + 16 m in every block of 64 channels
+              const uint32_t dead0 = (uint32_t)(~some0 >> (r >> 3)) & 0x00010001u, dead1 = (uint32_t)(~some0 >> (32 + (r >> 3))) & 0x00010001u;
+              const uint32_t dead2 = (uint32_t)(~some1 >> (r >> 3)) & 0x00010001u, dead3 = (uint32_t)(~some1 >> (32 + (r >> 3))) & 0x00010001u;
+              const uint32_t dead = dead0 | dead1 << 1 | dead2 << 2 | dead3 << 3;  // bit (m / 2) + 16 (m % 2)
 #pragma unroll 1
               for (int m = 0; m < 8; ++m) {
+                if (!((dead >> ((m >> 1) + 16 * (m & 1))) & 1u)) continue;
                 const int key = (r >> 3) + 16 * m;
-                if (((m < 4 ? some0 : some1) >> (key & 63)) & 1) continue;
                 const uint32_t at = su32(ring) + (p0 + key / C::kVKeys) % R * kPiece + key % C::kVKeys * 128 + (r & 7) * 16;
 #pragma unroll
                 for (int cb = 0; cb < HD / 64; ++cb) st_shared_v4(at + cb * (C::kVKeys * 128), 0u, 0u, 0u, 0u);
@@ -454,6 +437,19 @@ __global__ void __launch_bounds__(Tiles<HD, NQ>::kThreads, 1)
             }
           }
         }
+        uint32_t s[128];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tmem_ld32(col_s + 32 * i, s + 32 * i);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tmem_wait_ld(s + 32 * i);
+        // The row's maximum: 3-input max, 8 independent chains.
+        float mx8[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) mx8[e] = fmaxf(__uint_as_float(s[e]), __uint_as_float(s[8 + e]));
+#pragma unroll
+        for (int e = 16; e < 128; e += 2)
+          mx8[(e >> 1) & 7] = max3(mx8[(e >> 1) & 7], __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+        const float mx = fmaxf(max3(mx8[0], mx8[1], mx8[2]), max3(max3(mx8[3], mx8[4], mx8[5]), mx8[6], mx8[7]));
         const float m_tile = mx * c;
         float corr = 1.f;
         if (m_tile > m_ref + kRescaleThreshold) {
@@ -490,17 +486,13 @@ __global__ void __launch_bounds__(Tiles<HD, NQ>::kThreads, 1)
         const float mref = m_ref == -INFINITY ? 0.f : m_ref;
         const float2 c2 = make_float2(c, c), nm2 = make_float2(-mref, -mref);
         float2 sum4[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll 1
+#pragma unroll
         for (int half = 0; half < 2; ++half) {
-          uint32_t s[64], pk[32];
-          tmem_ld32(col_s + 64 * half, s);
-          tmem_ld32(col_s + 64 * half + 32, s + 32);
-          tmem_wait_ld(s);
-          tmem_wait_ld(s + 32);
+          uint32_t pk[32];
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
-            const float2 x =
-                __ffma2_rn(make_float2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), c2, nm2);
+            const float2 x = __ffma2_rn(
+                make_float2(__uint_as_float(s[64 * half + 2 * e]), __uint_as_float(s[64 * half + 2 * e + 1])), c2, nm2);
             const float2 v = make_float2(ex2(x.x), ex2(x.y));
             sum4[e & 3] = __fadd2_rn(sum4[e & 3], v);
             pk[e] = Pack<T>::two(v.x, v.y);
@@ -518,9 +510,9 @@ __global__ void __launch_bounds__(Tiles<HD, NQ>::kThreads, 1)
       // ---- the unit's end ----
       if (!(ok = waitw<false>(&sh.o_ready[qt], n_units & 1, abort_flag))) break;
       tc_after();
-      // O leaves through shared memory, 32 columns of the warp's rows at a time (16-byte
-      // pieces swizzled), so that whole lines of several rows go out together:
-      // 64 bytes a row of o, 128 of the partials.
+      // O leaves through shared memory, 128 bytes of each of the warp's rows at a time
+      // (64 columns of o, 32 of the partials; 16-byte pieces swizzled), so that whole
+      // lines of four rows go out together.
       const float inv = l > 0.f ? 1.f / l : 0.f;
       const bool cut = u.slot >= 0;
       if (cut && live) p.ml[(int64_t)u.slot * p.part_rows + ru] = make_float2(m_ref, l);
@@ -529,49 +521,60 @@ __global__ void __launch_bounds__(Tiles<HD, NQ>::kThreads, 1)
       if (live)
         at = cut ? ((int64_t)u.slot * p.part_rows + ru) * HD
                  : (int64_t)(u.row0 + ru / p.G) * p.o_row + (int64_t)(u.h * p.G + ru % p.G) * p.o_head;
-      const int bits = cut ? 3 : 2;  // log2 of a row's lanes
+      const int piece = lane & 7, step = cut ? 32 : 64;
+      int64_t to[8];  // of the rows that this thread stores a piece of
+#pragma unroll
+      for (int i = 0; i < 8; ++i) to[i] = __shfl_sync(0xffffffffu, at, 4 * i + (lane >> 3));
 #pragma unroll 1
-      for (int col = 0; col < HD; col += 32) {
-        uint32_t o[32];
+      for (int col = 0; col < HD; col += step) {
+        uint32_t o[64];
         tmem_ld32(lane_addr + col_o + col, o);
+        if (!cut) tmem_ld32(lane_addr + col_o + col + 32, o + 32);
         tmem_wait_ld(o);
-        if (col == HD - 32) {  // the next unit's P V may start O afresh
+        if (col + step >= HD) {  // the next unit's P V may start O afresh
           tc_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&sh.o_free[qt]);
         }
-        if (cut) {
+        if (!cut) {
+          tmem_wait_ld(o + 32);
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            st_shared_v4(mine + lane * 128 + ((e ^ (lane & 7)) << 4), o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 16; ++e) o[e] = Pack<T>::two(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            st_shared_v4(mine + lane * 64 + ((e ^ ((lane >> 1) & 3)) << 4), o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          for (int e = 0; e < 32; ++e) o[e] = Pack<T>::two(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
         }
-        __syncwarp();
-        const int piece = lane & ((1 << bits) - 1);
-#pragma unroll 2
-        for (int i = 0; i < 1 << bits; ++i) {
-          const int row = (i << (5 - bits)) + (lane >> bits);
-          const int64_t to = __shfl_sync(0xffffffffu, at, row);
-          uint4 x;
-          const uint32_t from = cut ? mine + row * 128 + ((piece ^ (row & 7)) << 4) : mine + row * 64 + ((piece ^ ((row >> 1) & 3)) << 4);
-          asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(from)
-                       : "memory");
-          if (to < 0) continue;
-          if (cut) {
-            *reinterpret_cast<uint4*>(p.part + to + col + 4 * piece) = x;
-          } else {
-            T* dst = static_cast<T*>(p.o) + to + col + 8 * piece;
-            if (p.o_wide) {
-              *reinterpret_cast<uint4*>(dst) = x;
-            } else {
-              const uint32_t y[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-              for (int k = 0; k < 8; ++k) reinterpret_cast<uint16_t*>(dst)[k] = (uint16_t)(y[k / 2] >> (16 * (k & 1)));
+        for (int e = 0; e < 8; ++e)
+          st_shared_v4(mine + lane * 128 + ((e ^ (lane & 7)) << 4), o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+        __syncwarp();
+        uint4 x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int row = 4 * i + (lane >> 3);
+          asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(x[i].x), "=r"(x[i].y), "=r"(x[i].z), "=r"(x[i].w)
+                       : "r"(mine + row * 128 + ((piece ^ (row & 7)) << 4)) : "memory");
+        }
+        if (cut) {
+          float* dst = p.part + col + 4 * piece;
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (to[i] >= 0) *reinterpret_cast<uint4*>(dst + to[i]) = x[i];
+        } else if (p.o_wide) {
+          uint16_t* dst = static_cast<uint16_t*>(p.o) + col + 8 * piece;
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (to[i] >= 0) *reinterpret_cast<uint4*>(dst + to[i]) = x[i];
+        } else {
+          uint16_t* dst = static_cast<uint16_t*>(p.o) + col + 8 * piece;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            if (to[i] < 0) continue;
+            uint32_t y[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll 1
+            for (int k = 0; k < 8; ++k) {
+              dst[to[i] + k] = (uint16_t)y[0];
+              y[0] = __funnelshift_r(y[0], y[1], 16);
+              y[1] = __funnelshift_r(y[1], y[2], 16);
+              y[2] = __funnelshift_r(y[2], y[3], 16);
+              y[3] >>= 16;
             }
           }
         }
