@@ -5,7 +5,7 @@
 // A unit's rows (tokens x the G heads of its KV head) fill one tile of 128 rows,
 // or two that share every tile of keys (head_dim 64 and 128: O of both fits
 // tensor memory).  Per CTA: warp 0 produces K and V, warp 1 issues the MMAs,
-// warp 2 brings Q, and four warps per row tile do the softmax, thread = row =
+// warp 2 brings Q, and from warp 4 on four warps per row tile do the softmax, thread = row =
 // TMEM lane.  A tile of 128 keys makes S = Q K^T of N = 128 (an MMA of N = 64
 // takes two thirds of one of N = 128); P takes S's place in 16 bits and O += P V reads
 // V as it lies in the cache (keys x channels: the MN-major operand).  Q is in
@@ -43,7 +43,12 @@ struct Tiles {
   static constexpr int kRing = 2 * kPieces * kDeep;
   static_assert(kRing / kPieces / 2 + kAhead + 2 < kUnits, "units in flight");
   static constexpr int kSmem = 1024 + NQ * kQTile + kStage + kRing * kPiece;
-  static constexpr int kThreads = 96 + 128 * NQ;
+  static constexpr int kThreads = 128 + 128 * NQ;
+  // Registers: with two row tiles the block starts with 168 a thread; the first
+  // four warps give up 80 of theirs, 40 more for each softmax thread, which holds a
+  // row of S (128 columns) at once.
+  static constexpr int kLaunchRegs = 168, kFewRegs = 88, kSoftmaxRegs = 208;
+  static_assert(kFewRegs + 2 * kSoftmaxRegs == 3 * kLaunchRegs, "registers of the block");
   // tensor memory: two S (P in their first halves), O of each row tile
   static constexpr uint32_t kColS = 0, kColO = 256;
   static constexpr uint32_t kCols = 512;
@@ -154,6 +159,8 @@ __global__ void __launch_bounds__(Tiles<HD, NQ>::kThreads, 1)
     return true;
   };
 
+  if (warp < 4) {
+  if (NQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kFewRegs));
   if (warp == 0) {
     // =================== producer of K and V ===================
     if (lane == 0) {
@@ -371,9 +378,11 @@ __global__ void __launch_bounds__(Tiles<HD, NQ>::kThreads, 1)
         mbar_arrive(&sh.q_full);
       }
     }
+  }
   } else {
+    if (NQ == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftmaxRegs));
     // =================== softmax (thread = row = TMEM lane) ===================
-    const int qt = (warp - 3) >> 2;
+    const int qt = (warp - 4) >> 2;
     const int quad = warp & 3;
     const int r = quad * 32 + lane;
     const int tile_rows = p.tokens_per / NQ * p.G;  // rows of a row tile
@@ -516,7 +525,7 @@ __global__ void __launch_bounds__(Tiles<HD, NQ>::kThreads, 1)
       const float inv = l > 0.f ? 1.f / l : 0.f;
       const bool cut = u.slot >= 0;
       if (cut && live) p.ml[(int64_t)u.slot * p.part_rows + ru] = make_float2(m_ref, l);
-      const uint32_t mine = su32(stage) + (warp - 3) * 4096;
+      const uint32_t mine = su32(stage) + (warp - 4) * 4096;
       int64_t at = -1;  // where this thread's row goes, in elements
       if (live)
         at = cut ? ((int64_t)u.slot * p.part_rows + ru) * HD
