@@ -143,18 +143,18 @@ __device__ __forceinline__ bool tile_edge(const AttnParams& p, const AttnUnit& x
   if (last >= x.end || (p.causal && last > x.pos0)) return true;
   return p.window && key0 <= x.pos0 + x.ntok - 1 - p.window && last >= p.sinks;
 }
-// Of 64 keys (bit k: key0 + k), those that the row at position pos sees.
-__device__ __forceinline__ uint64_t low_bits(int n) { return n >= 64 ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1; }
-__device__ __forceinline__ uint64_t row_sees(const AttnParams& p, int pos, int end, int key0) {
-  uint64_t m = low_bits((p.causal ? min(pos + 1, end) : end) - key0);
-  if (p.window) m &= ~low_bits(pos - p.window + 1 - key0) | low_bits(p.sinks - key0);
-  return m;
+// The keys that a row (or some row of a unit) sees: [lo, hi) and, before hi, those
+// below `sinks`.
+struct Seen {
+  int lo, hi;
+};
+__device__ __forceinline__ Seen row_sees(const AttnParams& p, const AttnUnit& x, int pos) {
+  return {p.window ? max(0, pos - p.window + 1) : 0, p.causal ? min(pos + 1, x.end) : x.end};
 }
-// Those that some row of the unit sees.
-__device__ __forceinline__ uint64_t unit_sees(const AttnParams& p, const AttnUnit& x, int key0) {
-  uint64_t m = low_bits(x.hi - key0);
-  if (p.window) m &= ~low_bits(x.lo - key0) | low_bits(p.sinks - key0);
-  return m;
+__device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u; }
+// Of 32 keys from key0 on, as bits.
+__device__ __forceinline__ uint32_t bits_of(const Seen& s, int sinks, int key0) {
+  return low_bits(s.hi - key0) & (~low_bits(s.lo - key0) | low_bits(sinks - key0));
 }
 
 // Exclusive scan of x over the CTA's kThreads threads; *total gets the sum.

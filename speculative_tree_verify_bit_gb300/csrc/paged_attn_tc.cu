@@ -14,7 +14,8 @@
 // K and V pass through one ring of pieces (K: 128 keys of 64 or 128 channels, V:
 // 64 or 128 keys of all channels) in the order in which the MMAs take them.  A step is (tile of keys, row tile); S of step n + 2 is formed after P V
 // of step n, so the tensor pipe works while a softmax runs: with two row tiles
-// they take turns, with one the tiles of keys do.  The order runs on across units; only O waits to be read at a unit's end.
+// they take turns, with one the tiles of keys do.  The order runs on across units: a unit's first P is
+// formed before the last unit's O is read, so that little waits for it.
 //
 // Keys that no row sees are cleared in V, since 0 times what a reused page holds
 // there could be NaN.  Every wait is bounded; a timeout sets a CTA abort flag,
@@ -390,29 +391,132 @@ __global__ void __launch_bounds__(Tiles<HD, NQ>::kThreads, 1)
     const uint32_t lane_addr = tmem + ((uint32_t)(quad * 32) << 16);
     const uint32_t col_o = C::kColO + qt * HD;
     const float c = p.scale2;
+    // A unit's end: its O is ready, or about to be.
+    struct Ended {
+      bool any = false, cut;
+      float l;
+      int64_t at;  // where this thread's row goes, in elements; -1: nowhere
+    } ended;
+    int n_ended = 0;
+    // Writes O of the unit that has ended.  It is taken out of tensor memory at once,
+    // so that the next unit's P V may start, and leaves through shared memory, 128
+    // bytes of each of the warp's rows at a time (64 columns of o, 32 of the
+    // partials; 16-byte pieces swizzled), so that whole lines of four rows go out
+    // together.
+    auto write_out = [&]() -> bool {
+      if (!waitw<false>(&sh.o_ready[qt], n_ended & 1, abort_flag)) return false;
+      ++n_ended;
+      tc_after();
+      const uint32_t mine = su32(stage) + (warp - 4) * 4096;
+      const int piece = lane & 7;
+      int64_t to[8];  // of the rows that this thread stores a piece of
+#pragma unroll
+      for (int i = 0; i < 8; ++i) to[i] = __shfl_sync(0xffffffffu, ended.at, 4 * i + (lane >> 3));
+      // 128 bytes of the warp's rows: w, a thread's row's.  put(i, x): 16 bytes of row to[i].
+      auto through = [&](const uint32_t* w, auto&& put) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          st_shared_v4(mine + lane * 128 + ((e ^ (lane & 7)) << 4), w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+        __syncwarp();
+        uint4 x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int row = 4 * i + (lane >> 3);
+          asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(x[i].x), "=r"(x[i].y), "=r"(x[i].z), "=r"(x[i].w)
+                       : "r"(mine + row * 128 + ((piece ^ (row & 7)) << 4)) : "memory");
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (to[i] >= 0) put(i, x[i]);
+        __syncwarp();
+      };
+      auto free_o = [&]() {
+        tc_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.o_free[qt]);
+      };
+      if (ended.cut) {
+#pragma unroll 1
+        for (int col = 0; col < HD; col += 32) {
+          uint32_t o[32];
+          tmem_ld32(lane_addr + col_o + col, o);
+          tmem_wait_ld(o);
+          if (col + 32 == HD) free_o();
+          float* dst = p.part + col + 4 * piece;
+          through(o, [&](int i, const uint4& x) { *reinterpret_cast<uint4*>(dst + to[i]) = x; });
+        }
+        return true;
+      }
+      const float inv = ended.l > 0.f ? 1.f / ended.l : 0.f;
+      // (of 256 channels the registers hold a quarter at a time)
+      constexpr int kHold = HD == 256 ? 128 : HD;
+#pragma unroll 1
+      for (int col = 0; col < HD; col += kHold) {
+        uint32_t out[kHold / 2];
+#pragma unroll
+        for (int i = 0; i < kHold / 32; ++i) {
+          uint32_t o[32];
+          tmem_ld32(lane_addr + col_o + col + 32 * i, o);
+          tmem_wait_ld(o);
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            out[16 * i + e] = Pack<T>::two(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+        }
+        if (col + kHold == HD) free_o();
+#pragma unroll
+        for (int i = 0; i < kHold / 64; ++i) {
+          uint16_t* dst = static_cast<uint16_t*>(p.o) + col + 64 * i + 8 * piece;
+          if (p.o_wide) {
+            through(out + 32 * i, [&](int j, const uint4& x) { *reinterpret_cast<uint4*>(dst + to[j]) = x; });
+          } else {
+            through(out + 32 * i, [&](int j, const uint4& x) {
+              uint32_t y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll 1
+              for (int k = 0; k < 8; ++k) {
+                dst[to[j] + k] = (uint16_t)y[0];
+                y[0] = __funnelshift_r(y[0], y[1], 16);
+                y[1] = __funnelshift_r(y[1], y[2], 16);
+                y[2] = __funnelshift_r(y[2], y[3], 16);
+                y[3] >>= 16;
+              }
+            });
+          }
+        }
+      }
+      return true;
+    };
+
     int g = 0;
     bool ok = true;
     for (int n_units = 0; ok; ++n_units) {
       if (!(ok = waitw<false>(&sh.unit_full[n_units % kUnits], (n_units / kUnits) & 1, abort_flag))) break;
       const UnitInfo& u = sh.unit[n_units % kUnits];  // stays as it is until the unit's end
-      const int t1 = u.t1;
-      if (t1 == u.t0) break;
+      const int t0 = u.t0, t1 = u.t1;
+      if (t1 == t0) break;
       const bool live = r < tile_rows && ru < u.rows;
-      const int pos = u.x.pos0 + ru / p.G;
+      const Seen sees = row_sees(p, u.x, u.x.pos0 + ru / p.G), some = {u.x.lo, u.x.hi};
+      // Some row may not see some key of a tile that goes on to `full_to` or further,
+      // or begins at `full_from` or before (and is not all among the first tokens).
+      const int full_to = p.causal ? min(u.x.pos0 + 1, u.x.end) : u.x.end;
+      const int full_from = p.window ? u.x.pos0 + u.x.ntok - 1 - p.window : -1;
+      const int n_sink = u.x.n_sink, skip = u.x.wt0 - n_sink;
       float m_ref = -INFINITY, l = 0.f;
-      for (int t = u.t0; t < t1; ++t, ++g) {
+      for (int t = t0; t < t1; ++t, ++g) {
         const int n = g * NQ + qt, b = n & 1;
-        const int key0 = tile_key(p, u.x, t);
+        const int key0 = (t < n_sink ? t : t + skip) * kBigTile;
         if (!(ok = waitw<false>(&sh.s_full[b], (n >> 1) & 1, abort_flag))) break;
         tc_after();
         const uint32_t col_s = lane_addr + C::kColS + 128 * b;
         const bool absent = sh.absent[g % 32];
-        if (absent || tile_edge(p, u.x, key0)) {
+        bool all_seen = true;  // by some row each
+        if (absent || key0 + kBigTile > full_to || (key0 <= full_from && key0 + kBigTile > p.sinks)) {
           // Columns that the row does not see go back as -inf, 32 at a time (a loop:
           // this path is cold, and a long one waits for its instructions).
+          uint32_t all = ~0u;
 #pragma unroll 1
           for (int i = 0; i < 4; ++i) {
-            const uint32_t vis = absent ? 0u : (uint32_t)row_sees(p, pos, u.x.end, key0 + 32 * i);
+            const uint32_t vis = absent ? 0u : bits_of(sees, p.sinks, key0 + 32 * i);
+            all &= absent ? 0u : bits_of(some, p.sinks, key0 + 32 * i);
             if (__all_sync(0xffffffffu, vis == ~0u)) continue;
             uint32_t x[32];
             tmem_ld32(col_s + 32 * i, x);
@@ -422,29 +526,7 @@ __global__ void __launch_bounds__(Tiles<HD, NQ>::kThreads, 1)
             tmem_st32(col_s + 32 * i, x);
           }
           tmem_wait_st();
-          // Keys that no row sees: zeros in V, by the first row tile's warps.
-          if (qt == 0) {
-            const uint64_t some0 = absent ? 0ull : unit_sees(p, u.x, key0), some1 = absent ? 0ull : unit_sees(p, u.x, key0 + 64);
-            if ((some0 & some1) != ~0ull) {
-              const int p0 = (2 * g + C::kAhead) * NP;
-#pragma unroll 1
-              for (int i = 0; i < NP && ok; ++i) ok = waitw<false>(&sh.full[(p0 + i) % R], ((p0 + i) / R) & 1, abort_flag);
-              if (!ok) break;
-              // thread: 16 bytes of keys r / 8 + 16 m in every block of 64 channels
-              const uint32_t dead0 = (uint32_t)(~some0 >> (r >> 3)) & 0x00010001u, dead1 = (uint32_t)(~some0 >> (32 + (r >> 3))) & 0x00010001u;
-              const uint32_t dead2 = (uint32_t)(~some1 >> (r >> 3)) & 0x00010001u, dead3 = (uint32_t)(~some1 >> (32 + (r >> 3))) & 0x00010001u;
-              const uint32_t dead = dead0 | dead1 << 1 | dead2 << 2 | dead3 << 3;  // bit (m / 2) + 16 (m % 2)
-#pragma unroll 1
-              for (int m = 0; m < 8; ++m) {
-                if (!((dead >> ((m >> 1) + 16 * (m & 1))) & 1u)) continue;
-                const int key = (r >> 3) + 16 * m;
-                const uint32_t at = su32(ring) + (p0 + key / C::kVKeys) % R * kPiece + key % C::kVKeys * 128 + (r & 7) * 16;
-#pragma unroll
-                for (int cb = 0; cb < HD / 64; ++cb) st_shared_v4(at + cb * (C::kVKeys * 128), 0u, 0u, 0u, 0u);
-              }
-              fence_async_smem();
-            }
-          }
+          all_seen = all == ~0u;
         }
         uint32_t s[128];
 #pragma unroll
@@ -460,34 +542,37 @@ __global__ void __launch_bounds__(Tiles<HD, NQ>::kThreads, 1)
           mx8[(e >> 1) & 7] = max3(mx8[(e >> 1) & 7], __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
         const float mx = fmaxf(max3(mx8[0], mx8[1], mx8[2]), max3(max3(mx8[3], mx8[4], mx8[5]), mx8[6], mx8[7]));
         const float m_tile = mx * c;
-        float corr = 1.f;
-        if (m_tile > m_ref + kRescaleThreshold) {
-          if (m_ref != -INFINITY) corr = ex2(m_ref - m_tile);
-          m_ref = m_tile;
-          l *= corr;
-        }
-        // O may be rescaled only once the row tile's previous P V has finished.  With
-        // two row tiles this S followed it; with one, this S followed the P V before
-        // that, and the next waits for this warp, so the phase is that one's or the one
-        // before.  At a unit's first tile O holds nothing to rescale.
-        if (t > u.t0 && __any_sync(0xffffffffu, corr != 1.f)) {
-          if (NQ == 1) {
-            if (!(ok = waitw<false>(&sh.pv_done, (g - 1) & 1, abort_flag))) break;
-            tc_after();
+        const bool grows = m_tile > m_ref + kRescaleThreshold;
+        if (__any_sync(0xffffffffu, grows)) {
+          float corr = 1.f;
+          if (grows) {
+            if (m_ref != -INFINITY) corr = ex2(m_ref - m_tile);
+            m_ref = m_tile;
+            l *= corr;
           }
-          const float2 corr2 = make_float2(corr, corr);
-#pragma unroll 1
-          for (int chunk = 0; chunk < HD / 32; ++chunk) {
-            uint32_t o[32];
-            tmem_ld32(lane_addr + col_o + 32 * chunk, o);
-            tmem_wait_ld(o);
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float2 x = __fmul2_rn(make_float2(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1])), corr2);
-              o[2 * e] = __float_as_uint(x.x);
-              o[2 * e + 1] = __float_as_uint(x.y);
+          // O may be rescaled only once the row tile's previous P V has finished.  With
+          // two row tiles this S followed it; with one, this S followed the P V before
+          // that, and the next waits for this warp, so the phase is that one's or the
+          // one before.  At a unit's first tile O holds nothing to rescale.
+          if (t > t0) {
+            if (NQ == 1) {
+              if (!(ok = waitw<false>(&sh.pv_done, (g - 1) & 1, abort_flag))) break;
+              tc_after();
             }
-            tmem_st32(lane_addr + col_o + 32 * chunk, o);
+            const float2 corr2 = make_float2(corr, corr);
+#pragma unroll 1
+            for (int chunk = 0; chunk < HD / 32; ++chunk) {
+              uint32_t o[32];
+              tmem_ld32(lane_addr + col_o + 32 * chunk, o);
+              tmem_wait_ld(o);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                const float2 x = __fmul2_rn(make_float2(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1])), corr2);
+                o[2 * e] = __float_as_uint(x.x);
+                o[2 * e + 1] = __float_as_uint(x.y);
+              }
+              tmem_st32(lane_addr + col_o + 32 * chunk, o);
+            }
           }
         }
         // P = 2^(S c - m_ref), rounded to the cache's type, packed in key pairs into
@@ -508,88 +593,58 @@ __global__ void __launch_bounds__(Tiles<HD, NQ>::kThreads, 1)
           }
           tmem_st32(col_s + 32 * half, pk);
         }
+        // Keys that no row sees: zeros in V, by the first row tile's warps.  (V comes
+        // late, so this is the last thing before P is handed over.)
+        if (qt == 0 && !all_seen) {
+          const int p0 = (2 * g + C::kAhead) * NP;
+#pragma unroll 1
+          for (int i = 0; i < NP && ok; ++i) ok = waitw<false>(&sh.full[(p0 + i) % R], ((p0 + i) / R) & 1, abort_flag);
+          if (!ok) break;
+          // thread: 16 bytes of keys r / 8 + 16 m in every block of 64 channels
+          constexpr int kPer = C::kVKeys / 16;  // of those keys in a piece
+#pragma unroll
+          for (int i = 0; i < NP; ++i) {
+            const uint32_t at = su32(ring) + (p0 + i) % R * kPiece + r * 16;
+#pragma unroll
+            for (int m = 0; m < kPer; ++m) {
+              const int k = key0 + (r >> 3) + 16 * (i * kPer + m);
+              if (!absent && k < some.hi && (k >= some.lo || k < p.sinks)) continue;
+#pragma unroll
+              for (int cb = 0; cb < HD / 64; ++cb) st_shared_v4(at + m * 2048 + cb * (C::kVKeys * 128), 0u, 0u, 0u, 0u);
+            }
+          }
+          fence_async_smem();
+        }
         tmem_wait_st();
         tc_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.p_full[b]);
         const float2 sum2 = __fadd2_rn(__fadd2_rn(sum4[0], sum4[1]), __fadd2_rn(sum4[2], sum4[3]));
         l += sum2.x + sum2.y;
+        // With two row tiles the unit before is written once this one's first P is on
+        // its way (an 8,192-token prompt takes 4 % less); with one, whose MMAs have a step
+        // more at hand, at once (2 % less).
+        if (ended.any) {
+          if (!(ok = write_out())) break;
+          ended.any = false;
+        }
       }
       if (!ok) break;
-      // ---- the unit's end ----
-      if (!(ok = waitw<false>(&sh.o_ready[qt], n_units & 1, abort_flag))) break;
-      tc_after();
-      // O leaves through shared memory, 128 bytes of each of the warp's rows at a time
-      // (64 columns of o, 32 of the partials; 16-byte pieces swizzled), so that whole
-      // lines of four rows go out together.
-      const float inv = l > 0.f ? 1.f / l : 0.f;
-      const bool cut = u.slot >= 0;
-      if (cut && live) p.ml[(int64_t)u.slot * p.part_rows + ru] = make_float2(m_ref, l);
-      const uint32_t mine = su32(stage) + (warp - 4) * 4096;
-      int64_t at = -1;  // where this thread's row goes, in elements
-      if (live)
-        at = cut ? ((int64_t)u.slot * p.part_rows + ru) * HD
-                 : (int64_t)(u.row0 + ru / p.G) * p.o_row + (int64_t)(u.h * p.G + ru % p.G) * p.o_head;
-      const int piece = lane & 7, step = cut ? 32 : 64;
-      int64_t to[8];  // of the rows that this thread stores a piece of
-#pragma unroll
-      for (int i = 0; i < 8; ++i) to[i] = __shfl_sync(0xffffffffu, at, 4 * i + (lane >> 3));
-#pragma unroll 1
-      for (int col = 0; col < HD; col += step) {
-        uint32_t o[64];
-        tmem_ld32(lane_addr + col_o + col, o);
-        if (!cut) tmem_ld32(lane_addr + col_o + col + 32, o + 32);
-        tmem_wait_ld(o);
-        if (col + step >= HD) {  // the next unit's P V may start O afresh
-          tc_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.o_free[qt]);
-        }
-        if (!cut) {
-          tmem_wait_ld(o + 32);
-#pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = Pack<T>::two(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          st_shared_v4(mine + lane * 128 + ((e ^ (lane & 7)) << 4), o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-        __syncwarp();
-        uint4 x[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int row = 4 * i + (lane >> 3);
-          asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(x[i].x), "=r"(x[i].y), "=r"(x[i].z), "=r"(x[i].w)
-                       : "r"(mine + row * 128 + ((piece ^ (row & 7)) << 4)) : "memory");
-        }
-        if (cut) {
-          float* dst = p.part + col + 4 * piece;
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (to[i] >= 0) *reinterpret_cast<uint4*>(dst + to[i]) = x[i];
-        } else if (p.o_wide) {
-          uint16_t* dst = static_cast<uint16_t*>(p.o) + col + 8 * piece;
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (to[i] >= 0) *reinterpret_cast<uint4*>(dst + to[i]) = x[i];
-        } else {
-          uint16_t* dst = static_cast<uint16_t*>(p.o) + col + 8 * piece;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            if (to[i] < 0) continue;
-            uint32_t y[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-#pragma unroll 1
-            for (int k = 0; k < 8; ++k) {
-              dst[to[i] + k] = (uint16_t)y[0];
-              y[0] = __funnelshift_r(y[0], y[1], 16);
-              y[1] = __funnelshift_r(y[1], y[2], 16);
-              y[2] = __funnelshift_r(y[2], y[3], 16);
-              y[3] >>= 16;
-            }
-          }
-        }
-        __syncwarp();
+      ended.any = true;
+      ended.cut = u.slot >= 0;
+      ended.l = l;
+      ended.at = -1;
+      if (live) {
+        if (ended.cut) p.ml[(int64_t)u.slot * p.part_rows + ru] = make_float2(m_ref, l);
+        ended.at = ended.cut ? ((int64_t)u.slot * p.part_rows + ru) * HD
+                             : (int64_t)(u.row0 + ru / p.G) * p.o_row + (int64_t)(u.h * p.G + ru % p.G) * p.o_head;
+      }
+      if (NQ == 1) {
+        if (!(ok = write_out())) break;
+        ended.any = false;
       }
     }
+    if (ok && ended.any) write_out();
   }
 
   // ---- teardown ----
