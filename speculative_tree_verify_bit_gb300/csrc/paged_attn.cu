@@ -14,6 +14,8 @@
 // barriers.  Bound by HBM; the ring holds what the SM needs in flight.
 #include <string.h>
 
+#include <algorithm>
+
 #include "paged_attn.cuh"
 
 namespace stv {
@@ -201,9 +203,12 @@ __global__ void __launch_bounds__(kThreads, Small<HD>::kCtasPerSm)
     auto meet = [&]() -> bool {
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.met);
-      const bool ok = waitw<false>(&sh.met, met & 1, abort_flag);
+      // (a poll: the others are about to come, and a suspended warp wakes up late)
+      bool ok = false;
+      for (uint32_t it = 0; it < kSpinLimit && !ok; ++it) ok = probe(&sh.met, met & 1);
+      if (!ok) ok = wait_suspend(&sh.met, met & 1, abort_flag);
       ++met;
-      return ok;
+      return __all_sync(0xffffffffu, ok);
     };
     for (int g = 0;; ++g) {
       const int st = g % kStages;
@@ -387,33 +392,79 @@ __global__ void __launch_bounds__(kThreads, Small<HD>::kCtasPerSm)
 }
 
 // Units cut by the runs' borders: M = max m, o = sum 2^(m - M) O / sum 2^(m - M) l
-// over their parts, in the runs' order.  Block (b, j): rows 4 j .. of the unit
-// that begins in CTA b's run and goes on after it.
-template <typename T, int HD>
-__global__ void __launch_bounds__(HD) attn_join_kernel(const __grid_constant__ AttnParams p) {
+// over their parts, in the runs' order.  Block (b, j) takes rows of the unit that
+// begins in CTA b's run and goes on after it; HD / 4 threads take a part of a row, so
+// there are kSlots at a time: of one row (kParts: single tokens, whose parts may be
+// as many as CTAs), put together through shared memory, or of as many rows.  A
+// thread asks for the next kBatch parts at once.
+constexpr int kJoinThreads = 256;
+template <typename T, int HD, bool kParts>
+__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_constant__ AttnParams p) {
+  constexpr int kPer = 4, kTeam = HD / kPer, kSlots = kJoinThreads / kTeam, kBatch = 8;
   grid_dep_wait();
   grid_dep_launch();
   const JoinRecord rec = p.rec[blockIdx.x];
-  constexpr int kPer = 4;  // channels of a thread
-  const int r = blockIdx.y * kJoinRows + threadIdx.x / (HD / kPer), ch = threadIdx.x % (HD / kPer) * kPer;
-  if (r >= rec.rows) return;
-  const int first = blockIdx.x;
-  auto slot_of = [&](int c) { return (int64_t)(2 * c + (c == first)) * p.part_rows + r; };
-  float M = -INFINITY;
-  for (int c = first; c <= rec.last_cta; ++c) M = fmaxf(M, __ldg(&p.ml[slot_of(c)].x));
-  const float ref = M == -INFINITY ? 0.f : M;
-  float L = 0.f, v[kPer] = {};
-#pragma unroll 4
-  for (int c = first; c <= rec.last_cta; ++c) {
-    const float2 x = __ldg(p.ml + slot_of(c));
-    const float4 a = __ldg(reinterpret_cast<const float4*>(p.part + slot_of(c) * HD + ch));
-    const float f = ex2(x.x - ref);
-    L += f * x.y;
-    v[0] += f * a.x;
-    v[1] += f * a.y;
-    v[2] += f * a.z;
-    v[3] += f * a.w;
+  const int slot = threadIdx.x / kTeam, ch = threadIdx.x % kTeam * kPer;
+  const int r = kParts ? blockIdx.y : blockIdx.y * kSlots + slot;
+  if ((kParts ? (int)blockIdx.y : (int)blockIdx.y * kSlots) >= rec.rows) return;
+  const int first = blockIdx.x, n = r < rec.rows ? rec.last_cta - first + 1 : 0, step = kParts ? kSlots : 1;
+  float M = -INFINITY, L = 0.f, v[kPer] = {};
+  for (int i0 = kParts ? slot : 0; i0 < n; i0 += step * kBatch) {
+    float2 x[kBatch];
+    float4 a[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int c = first + i0 + k * step;
+      x[k] = make_float2(-INFINITY, 0.f);
+      if (i0 + k * step < n) {
+        const int64_t at = (int64_t)(2 * c + (c == first)) * p.part_rows + r;
+        x[k] = __ldg(p.ml + at);
+        a[k] = __ldg(reinterpret_cast<const float4*>(p.part + at * HD + ch));
+      }
+    }
+    float m = M;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) m = fmaxf(m, x[k].x);
+    const float ref = m == -INFINITY ? 0.f : m, f0 = ex2(M - ref);
+    M = m;
+    L *= f0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) v[j] *= f0;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      if (x[k].x == -INFINITY) continue;  // not there, or without keys
+      const float f = ex2(x[k].x - ref);
+      L += f * x[k].y;
+      v[0] += f * a[k].x;
+      v[1] += f * a[k].y;
+      v[2] += f * a[k].z;
+      v[3] += f * a[k].w;
+    }
   }
+  if constexpr (kParts) {
+    __shared__ float2 ml[kSlots];
+    __shared__ float4 part[kSlots][kTeam];
+    if (threadIdx.x % kTeam == 0) ml[slot] = make_float2(M, L);
+    part[slot][threadIdx.x % kTeam] = make_float4(v[0], v[1], v[2], v[3]);
+    __syncthreads();
+    if (slot > 0) return;
+    M = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < kSlots; ++k) M = fmaxf(M, ml[k].x);
+    const float ref = M == -INFINITY ? 0.f : M;
+    L = v[0] = v[1] = v[2] = v[3] = 0.f;
+#pragma unroll
+    for (int k = 0; k < kSlots; ++k) {
+      const float f = ex2(ml[k].x - ref);
+      const float4 a = part[k][threadIdx.x];
+      L += f * ml[k].y;
+      v[0] += f * a.x;
+      v[1] += f * a.y;
+      v[2] += f * a.z;
+      v[3] += f * a.w;
+    }
+  }
+  if (r >= rec.rows) return;
   const float inv = L > 0.f ? 1.f / L : 0.f;
 #pragma unroll
   for (int k = 0; k < kPer; ++k) v[k] *= inv;
@@ -433,17 +484,20 @@ cudaError_t launch_small(const AttnParams& p, int grid, cudaStream_t s) {
 }
 
 template <typename T, int HD>
-cudaError_t launch_join(const AttnParams& p, int grid, cudaStream_t s) {
+cudaError_t launch_join(const AttnParams& p, bool small, int grid, cudaStream_t s) {
+  const int rows = (int)std::min<int64_t>(p.part_rows, (int64_t)p.max_new * p.G);  // of a unit, at most
+  const int slots = kJoinThreads / (HD / 4);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)grid, (unsigned)((p.part_rows + kJoinRows - 1) / kJoinRows));
-  cfg.blockDim = dim3(HD);
+  cfg.gridDim = dim3((unsigned)grid, (unsigned)(small ? rows : (rows + slots - 1) / slots));
+  cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, attn_join_kernel<T, HD>, p);
+  cudaError_t e = small ? cudaLaunchKernelEx(&cfg, attn_join_kernel<T, HD, true>, p)
+                        : cudaLaunchKernelEx(&cfg, attn_join_kernel<T, HD, false>, p);
   if (e != cudaSuccess) (void)cudaGetLastError();
   return e;
 }
@@ -455,8 +509,8 @@ cudaError_t launch_join(const AttnParams& p, int grid, cudaStream_t s) {
         : (hd == 256 ? f<__half, 256>(__VA_ARGS__) : hd == 128 ? f<__half, 128>(__VA_ARGS__)             \
                                                               : f<__half, 64>(__VA_ARGS__)))
 
-cudaError_t launch_attn_join(const AttnParams& p, int hd, bool bf16, int grid, cudaStream_t s) {
-  return STV_BY_TYPE(launch_join, p, grid, s);
+cudaError_t launch_attn_join(const AttnParams& p, int hd, bool bf16, bool small, int grid, cudaStream_t s) {
+  return STV_BY_TYPE(launch_join, p, small, grid, s);
 }
 
 // How a call is cut: which kernel, its CTAs, and the workspace.
@@ -651,6 +705,6 @@ extern "C" int stv_paged_attn(const stv_shape* shape, const stv_attn_spec* spec,
   cudaStream_t st = (cudaStream_t)stream;
   cudaError_t e = a.small ? launch_attn_small(p, sh.hd, sh.bf16, a.grid, st)
                           : launch_attn_tiles(p, sh.hd, sh.bf16, a.q_tiles, a.grid, st);
-  if (e == cudaSuccess) e = launch_attn_join(p, sh.hd, sh.bf16, a.grid, st);
+  if (e == cudaSuccess) e = launch_attn_join(p, sh.hd, sh.bf16, a.small, a.grid, st);
   return e == cudaSuccess ? STV_OK : STV_ERR_CUDA;
 }

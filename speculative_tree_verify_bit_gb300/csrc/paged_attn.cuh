@@ -35,7 +35,6 @@ __host__ __device__ constexpr int big_piece_bytes(int hd) { return hd == 64 ? 16
 constexpr int kMaxEntries = 4096;
 constexpr int kMaxCtx = 1 << 30;
 constexpr int kSmallRows = 16;      // rows of Q per unit, single tokens
-constexpr int kJoinRows = 4;        // rows per block of the join kernel
 
 // A unit cut by the runs' borders: written by the CTA whose run it begins in.
 struct JoinRecord {
@@ -79,36 +78,24 @@ struct Entry {
   int keys;  // tokens of its pages
 };
 
-// Entry i, with no rows where anything about it is wrong.
+// Entry i, with no rows where anything about it is wrong.  (All loads first: two
+// trips to memory, one without seqs.)
 __device__ __forceinline__ Entry entry_of(const AttnParams& p, int i) {
   Entry e;
   e.s = p.seqs ? __ldg(p.seqs + i) : i;
-  int r1;
-  if (p.row_start) {
-    e.row0 = __ldg(p.row_start + i);
-    r1 = __ldg(p.row_start + i + 1);
-  } else {
-    e.row0 = i;
-    r1 = i + 1;
-  }
-  e.L = e.ctx = e.keys = 0;
-  if (e.row0 < 0 || r1 < e.row0 || r1 > p.n_rows || r1 - e.row0 > p.max_new) {
-    report(p.status, STV_DEV_BAD_ROW);
-    return e;
-  }
-  if (e.s < 0 || e.s >= p.max_seqs) {
-    report(p.status, STV_DEV_BAD_SEQ);
-    return e;
-  }
-  e.ctx = __ldg(p.ctx + e.s);
-  if (e.ctx < 0 || e.ctx > kMaxCtx) {
-    report(p.status, STV_DEV_BAD_SEQ);
-    return e;
-  }
-  e.L = r1 - e.row0;
-  const int have = min(__ldg(p.counts + e.s), p.table_stride);
+  e.row0 = p.row_start ? __ldg(p.row_start + i) : i;
+  const int r1 = p.row_start ? __ldg(p.row_start + i + 1) : i + 1;
+  const int s = min(max(e.s, 0), p.max_seqs - 1);
+  e.ctx = __ldg(p.ctx + s);
+  const int have = min(__ldg(p.counts + s), p.table_stride);
   e.keys = max(0, min(have, kMaxCtx / kPageTok * 2 - 1)) * kPageTok;
-  if (e.L && e.ctx + e.L > e.keys) report(p.status, STV_DEV_BAD_PAGE);
+  int bad = 0;
+  if (e.row0 < 0 || r1 < e.row0 || r1 > p.n_rows || r1 - e.row0 > p.max_new) bad = STV_DEV_BAD_ROW;
+  else if (e.s != s || e.ctx < 0 || e.ctx > kMaxCtx) bad = STV_DEV_BAD_SEQ;
+  e.L = bad ? 0 : r1 - e.row0;
+  if (e.L && e.ctx + e.L > e.keys) bad = STV_DEV_BAD_PAGE;
+  if (bad) report(p.status, bad);
+  if (!e.L) e.ctx = e.keys = 0;
   return e;
 }
 
@@ -187,6 +174,11 @@ struct RunStart {
   long long left, share;  // length of the run, of a full run
 };
 
+// a / b; a 64-bit division takes a third of a microsecond.
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  return a >> 31 == 0 && b >> 31 == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
 // Whole CTA; scratch: n + 1 ints of shared memory, free afterwards.  Ends with
 // a barrier.
 template <int kThreads>
@@ -252,7 +244,7 @@ __device__ __forceinline__ RunStart run_of(const AttnParams& p, int* scratch) {
   long long total;
   const long long before = cta_scan<kThreads>(tiles, &total) * p.hkv;
   total *= p.hkv;
-  const long long share = (total + gridDim.x - 1) / gridDim.x;
+  const long long share = quotient(total + gridDim.x - 1, gridDim.x);
   const long long f0 = share * blockIdx.x;
   if (f0 < total && before <= f0 && f0 < before + tiles * p.hkv) {
     long long f = before;
@@ -260,8 +252,8 @@ __device__ __forceinline__ RunStart run_of(const AttnParams& p, int* scratch) {
       if (f0 < f + (long long)n * p.hkv) {
         start.e = e;
         start.u = u;
-        start.h = (int)((f0 - f) / n);
-        start.off = (int)((f0 - f) % n);
+        start.h = (int)quotient(f0 - f, n);
+        start.off = (int)(f0 - f - (long long)start.h * n);
         start.left = min(share, total - f0);
         start.share = share;
         return false;
@@ -305,7 +297,7 @@ struct RunWalk {
   // does not end here.
   __device__ int last_cta() const {
     const int rest = x.n_tiles - t1;  // in runs after this one
-    return (int)(blockIdx.x + (rest + at.share - 1) / at.share);
+    return (int)(blockIdx.x + quotient(rest + at.share - 1, at.share));
   }
   __device__ bool next() {
     do {
