@@ -30,6 +30,7 @@
 #include <math.h>
 #include <string.h>
 
+#include <type_traits>
 #include <utility>
 
 #include "stv_device.cuh"
@@ -92,12 +93,6 @@ __device__ __forceinline__ uint64_t whole(const Parts& x) {
   return (uint64_t)(((long long)x.h << 38) + ((long long)x.l << 16) + x.s);
 }
 __device__ __forceinline__ uint64_t fixed(float x) { return whole(parts_of(x)); }
-__device__ __forceinline__ void add_to(Parts& a, const Parts& x) {
-  a.h += x.h;
-  a.l += x.l;
-  a.s += x.s;
-}
-
 // The same of a number of at most 2^-22, without h.
 __device__ __forceinline__ Parts small_parts_of(float x) {
   const float t2 = fmaf(x, 4194304.f, 3.f), r2 = fmaf(t2 - 3.f, -2.384185791015625e-7f, x);
@@ -178,6 +173,65 @@ template <typename T>
 __device__ __forceinline__ float entry(const uint4& v, int i) {
   return to_f(reinterpret_cast<const T*>(&v)[i]);
 }
+// Entries i and i + 1, i even.
+template <typename T>
+__device__ __forceinline__ float2 entries(const uint4& v, int i) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  if constexpr (sizeof(T) == 4) return make_float2(__uint_as_float(w[i]), __uint_as_float(w[i + 1]));
+  else if constexpr (std::is_same<T, __half>::value) return __half22float2(*reinterpret_cast<const __half2*>(&w[i / 2]));
+  else return make_float2(__uint_as_float(w[i / 2] << 16), __uint_as_float(w[i / 2] & 0xffff0000u));
+}
+// The largest of the bit patterns so far; whether one is above 1's (or negative).
+template <typename T>
+__device__ __forceinline__ uint32_t most_of(uint32_t most, const uint4& v) {
+  if constexpr (sizeof(T) == 4) return max(max(most, max(v.x, v.y)), max(v.z, v.w));
+  else return __vmaxu2(__vmaxu2(most, __vmaxu2(v.x, v.y)), __vmaxu2(v.z, v.w));
+}
+template <typename T>
+__device__ __forceinline__ bool above_one(uint32_t most) {
+  if constexpr (sizeof(T) == 4) return most > 0x3f800000u;
+  constexpr uint32_t one = std::is_same<T, __half>::value ? 0x3c00u : 0x3f80u;
+  return (most & 0xffffu) > one || (most >> 16) > one;
+}
+
+// Sums of parts, two numbers an instruction (paired fp32): the bits of the sums as
+// they are, their constants taken off at the end.  The steps are parts_of's and
+// add_above's, so that each number counts as it does there.
+struct Sums {
+  uint32_t h = 0, l = 0, s = 0;
+  __device__ __forceinline__ void low(float2 r) {
+    const float2 three = make_float2(3.f, 3.f);
+    const float2 t2 = __ffma2_rn(r, make_float2(4194304.f, 4194304.f), three);
+    const float2 r2 = __ffma2_rn(__fadd2_rn(t2, make_float2(-3.f, -3.f)),
+                                 make_float2(-2.384185791015625e-7f, -2.384185791015625e-7f), r);
+    const float2 t3 = __ffma2_rn(r2, make_float2(274877906944.f, 274877906944.f), three);
+    l += __float_as_uint(t2.x) + __float_as_uint(t2.y);
+    s += __float_as_uint(t3.x) + __float_as_uint(t3.y);
+  }
+  __device__ __forceinline__ void add(float2 x) {
+    const float2 t = __fadd2_rn(x, make_float2(2.f, 2.f)), u = __fadd2_rn(t, make_float2(-2.f, -2.f));
+    h += __float_as_uint(t.x) + __float_as_uint(t.y);
+    low(__ffma2_rn(u, make_float2(-1.f, -1.f), x));
+  }
+  // of n numbers, m of them (n, or with their errors 2 n) with low parts
+  __device__ __forceinline__ uint64_t whole_of(int n, int m) const {
+    return whole(Parts{(int)(h - (uint32_t)n * 0x40000000u), (int)(l - (uint32_t)m * 0x40400000u),
+                       (int)(s - (uint32_t)m * 0x40400000u)});
+  }
+};
+template <bool kOneF>
+__device__ __forceinline__ void add_above2(Sums& a, float2 p, float2 q, float2 f) {
+  const float2 neg = make_float2(-1.f, -1.f);
+  const float2 x = kOneF ? q : __fmul2_rn(q, make_float2(f.x, f.x));
+  float2 d = __ffma2_rn(x, neg, p), e = __ffma2_rn(x, neg, __ffma2_rn(d, neg, p)), w = make_float2(0.f, 0.f);
+  if constexpr (!kOneF) {
+    w = __ffma2_rn(q, make_float2(f.y, f.y), __ffma2_rn(q, make_float2(f.x, f.x), __fmul2_rn(x, neg)));
+    e = __ffma2_rn(w, neg, e);
+  }
+  const bool kx = d.x > w.x, ky = d.y > w.y;
+  a.add(make_float2(kx ? d.x : 0.f, ky ? d.y : 0.f));
+  a.low(make_float2(kx ? e.x : 0.f, ky ? e.y : 0.f));
+}
 
 struct Share {
   uint64_t sum, draft;  // of R, of q
@@ -185,9 +239,10 @@ struct Share {
 };
 
 template <typename T, int kDrafts>
-__global__ void __launch_bounds__(kThreads, 2) accept_probs_kernel(const __grid_constant__ AcceptParams p) {
+__global__ void __launch_bounds__(kThreads, kDrafts == kCertain ? 2 : 1) accept_probs_kernel(const __grid_constant__ AcceptParams p) {
   constexpr int VE = 16 / (int)sizeof(T);
-  __shared__ int par[kMaxT], id[kMaxT], way[kMaxT];
+  __shared__ int id[kMaxT], way[kMaxT];
+  __shared__ uint32_t kids[kMaxT], fine, taken;  // nodes' children; nodes with good numbers; taken if nothing was rejected before
   __shared__ float uu[kMaxT], pp[kMaxT], qq[kMaxT];
   __shared__ Rest st;
   __shared__ uint64_t warp_sum[kWarps], warp_draft[kWarps];
@@ -214,42 +269,49 @@ __global__ void __launch_bounds__(kThreads, 2) accept_probs_kernel(const __grid_
     const bool bad = act && (tid == 0 ? pa != -1 : (pa < 0 || pa >= tid));
     const int any = __any_sync(0xffffffffu, bad);
     const bool there = act && tid > 0 && !any && x >= 0 && x < V;
-    par[tid] = there ? pa : -1;
+    const float px = there ? to_f(p_rows[pa * p.p_stride + x]) : 0.f;
+    float qx = 1.f;
+    if constexpr (kDrafts != kCertain) qx = there ? to_f(q_rows[pa * p.q_stride + x]) : 0.f;
     id[tid] = x;
     uu[tid] = u;
-    pp[tid] = there ? to_f(p_rows[pa * p.p_stride + x]) : 0.f;
-    if constexpr (kDrafts != kCertain) qq[tid] = there ? to_f(q_rows[pa * p.q_stride + x]) : 0.f;
-    else qq[tid] = 1.f;
+    pp[tid] = px;
+    qq[tid] = qx;
+    kids[tid] = 0;
+    __syncwarp();
+    const uint32_t with = __match_any_sync(0xffffffffu, there ? pa : -1);
+    if (there && lane == __ffs(with) - 1) kids[pa] = with;
+    const uint32_t good = __ballot_sync(0xffffffffu, is_prob(px) && is_prob(qx) && u >= 0.f && u < 1.f);
+    // u q < p, exactly: two 24-bit numbers, and one
+    const uint32_t take = __ballot_sync(0xffffffffu, make_float2(u, 0.f) * make_float2(qx, 0.f) < make_float2(px, 0.f));
     if (tid == 0) {
       bad_bits = any ? STV_DEV_BAD_TREE : 0;
       st.f = make_float2(0.f, 0.f);
       st.n_gone = 0;
       node = 0;
+      fine = good;
+      taken = take;
     }
   }
   __syncthreads();
   cluster.barrier_wait(std::move(started));
 
-  // Thread 0's place in the walk.  z: Z (1 until a rejection counts); known: the warps' sums are those of the row as it is now, but for the tokens
-  // taken out (certain: of p).
-  int c = 1, depth = 0, pass = 0;
+  // Thread 0's place in the walk.  todo: the node's children not tried yet; z: Z (1
+  // until a rejection counts); known: the warps' sums are those of the row as it is
+  // now, but for the tokens taken out (certain: of p); left: R's sum, with them.
+  int c = 0, depth = 0, pass = 0;
+  uint32_t todo = kids[0];
   const float2 one = make_float2(1.f, 0.f), zero = make_float2(0.f, 0.f);
   float2 z = one, before_f = zero, draft_mass = one;
   uint64_t draft_all = 0, draft_sum = 0;  // what is left of the draft's mass; the last pass's sum
-  bool pending = false, known = false;
-  uint64_t total = 0, left = 0;  // the last pass's sum; with the tokens taken out
+  bool pending = false, known = false, fresh = true;  // fresh: nothing was rejected at this node
+  uint64_t left = 0;
   int v_per = 0;
   const T* prow = p_rows;
   const T* qrow = q_rows;
   int pre = 0;
   bool p_wide = false, q_wide = false;
-  // What the tokens taken out add to the sums (modulo 2^64).
-  auto gone_adds = [&]() {
-    uint64_t x = 0;
-    for (int i = 0; i < st.n_gone; ++i)
-      x += st.gone_r[i] - rest_of(st.gone_p[i], st.gone_q[i], st.f);
-    return x;
-  };
+  // What a token taken out adds to the sums (modulo 2^64).
+  auto gone_adds = [&](int i) { return st.gone_r[i] - rest_of(st.gone_p[i], st.gone_q[i], st.f); };
   auto place_of = [&](int x) {
     for (int i = 0; i < st.n_gone; ++i)
       if (st.gone[i] == x) return i;
@@ -265,7 +327,6 @@ __global__ void __launch_bounds__(kThreads, 2) accept_probs_kernel(const __grid_
           const int x = id[c], at = place_of(x);
           if constexpr (kDrafts == kCertain) {
             const uint64_t px = fixed(pp[c]);
-            left = total + gone_adds();
             if (at < 0 && left > px) {  // else nothing would be left
               st.gone[st.n_gone] = x;
               st.gone_p[st.n_gone] = pp[c];
@@ -274,13 +335,11 @@ __global__ void __launch_bounds__(kThreads, 2) accept_probs_kernel(const __grid_
             }
             if (st.n_gone) z = pair_of(left);
           } else {
-            const uint64_t sum = total + gone_adds();
-            if (sum == 0) {  // nothing left: R and Z stay
+            if (left == 0) {  // R and Z stay
               st.f = before_f;
               known = false;
             } else {
-              z = pair_of(sum);
-              left = sum;
+              z = pair_of(left);
               known = true;
             }
             if constexpr (kDrafts == kDistinct) {
@@ -297,39 +356,46 @@ __global__ void __launch_bounds__(kThreads, 2) accept_probs_kernel(const __grid_
             }
           }
           pending = false;
-          ++c;
         }
-        while (c < T_ && par[c] != node) ++c;
-        if (c >= T_) {  // the last token: from the sums that there are, or a pass first
+        if (!todo) {  // the last token: from the sums that there are, or a pass first
           cmd = known ? 2 : 1;
           known = true;
           break;
         }
-        if (!is_prob(pp[c]) || !is_prob(qq[c]) || !(uu[c] >= 0.f && uu[c] < 1.f)) {
+        c = __ffs(todo) - 1;
+        todo &= todo - 1;
+        if (!((fine >> c) & 1u)) {
           bad_bits = STV_DEV_BAD_SAMPLE;
           break;
         }
-        const int at = place_of(id[c]);
-        float2 s_x = make_float2(qq[c], 0.f), r_x = make_float2(pp[c], 0.f);  // S(x), R(x), times the sum of S
-        if (at >= 0) r_x = pair_of(st.gone_r[at]);
-        else if (kDrafts != kCertain && st.f.x > 0.f) r_x = pair_of(rest_of(pp[c], qq[c], st.f));
-        if constexpr (kDrafts == kDistinct) {
-          if (st.n_gone) {
-            if (at >= 0 || draft_mass.x == 0.f) s_x = zero;
-            else r_x = r_x * draft_mass;
+        bool take = (taken >> c) & 1u;
+        if (!fresh) {
+          const int at = place_of(id[c]);
+          float2 s_x = make_float2(qq[c], 0.f), r_x = make_float2(pp[c], 0.f);  // S(x), R(x), times the sum of S
+          if (at >= 0) r_x = pair_of(st.gone_r[at]);
+          else if (kDrafts != kCertain && st.f.x > 0.f) r_x = pair_of(rest_of(pp[c], qq[c], st.f));
+          if constexpr (kDrafts == kDistinct) {
+            if (st.n_gone) {
+              if (at >= 0 || draft_mass.x == 0.f) s_x = zero;
+              else r_x = r_x * draft_mass;
+            }
           }
+          take = make_float2(uu[c], 0.f) * s_x * z < r_x;
         }
-        // exact at a node's first child: three 24-bit numbers
-        if (make_float2(uu[c], 0.f) * s_x * z < r_x) {  // accepted
+        if (take) {
           node = c;
+          todo = kids[c];
           way[++depth] = c;
-          st.n_gone = 0;
-          z = draft_mass = one;
-          st.f = zero;
+          if (!fresh) {
+            st.n_gone = 0;
+            z = draft_mass = one;
+            st.f = zero;
+          }
+          fresh = true;
           known = false;
-          ++c;
           continue;
         }
+        fresh = false;
         pending = true;
         if constexpr (kDrafts == kCertain) {
           cmd = known ? 0 : 1;
@@ -361,8 +427,7 @@ __global__ void __launch_bounds__(kThreads, 2) accept_probs_kernel(const __grid_
     const bool none = f.x == 0.f, plain = f.x == 1.f && f.y == 0.f;
     uint64_t sum = 0, draft = 0;
     bool bad = false;
-    constexpr int U = kDrafts == kCertain ? 4 : 2;  // vectors in flight
-    constexpr uint32_t kOneBits = 0x3f800000u;
+    constexpr int U = 4;  // vectors in flight
     for (int v = v0 + lane; v < v1; v += 32 * U) {
       uint4 a[U], b[U];
 #pragma unroll
@@ -374,36 +439,33 @@ __global__ void __launch_bounds__(kThreads, 2) accept_probs_kernel(const __grid_
           if (!none) b[j] = load_entries(qrow, e, V, q_wide);
       }
       uint32_t most = 0;  // of the entries' bits: above 1's, they are looked at again
-      Parts part = {0, 0, 0}, part_q = {0, 0, 0};
+      Sums part, part_q;
+      const bool one_sum = kDrafts == kCertain || none;
 #pragma unroll
       for (int j = 0; j < U; ++j) {
-        if (kDrafts == kCertain || none) {
+        most = most_of<T>(most, a[j]);
+        if (one_sum) {
 #pragma unroll
-          for (int i = 0; i < VE; ++i) {
-            const float x = entry<T>(a[j], i);
-            most = max(most, __float_as_uint(x));
-            add_to(part, parts_of(x));
-          }
-        } else if (plain) {
-#pragma unroll
-          for (int i = 0; i < VE; ++i) {
-            const float x = entry<T>(a[j], i), y = entry<T>(b[j], i);
-            most = max(most, max(__float_as_uint(x), __float_as_uint(y)));
-            add_above<true>(part, x, y, f);
-            if constexpr (kDrafts == kDistinct) add_to(part_q, parts_of(y));
-          }
+          for (int i = 0; i < VE; i += 2) part.add(entries<T>(a[j], i));
         } else {
+          most = most_of<T>(most, b[j]);
+          if (plain) {
 #pragma unroll
-          for (int i = 0; i < VE; ++i) {
-            const float x = entry<T>(a[j], i), y = entry<T>(b[j], i);
-            most = max(most, max(__float_as_uint(x), __float_as_uint(y)));
-            add_above<false>(part, x, y, f);
+            for (int i = 0; i < VE; i += 2) {
+              const float2 y = entries<T>(b[j], i);
+              add_above2<true>(part, entries<T>(a[j], i), y, f);
+              if constexpr (kDrafts == kDistinct) part_q.add(y);
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < VE; i += 2) add_above2<false>(part, entries<T>(a[j], i), entries<T>(b[j], i), f);
           }
         }
       }
-      sum = sat_add(sum, whole(part));
-      if constexpr (kDrafts == kDistinct) draft = sat_add(draft, whole(part_q));
-      if (most > kOneBits) {  // -0 is a probability
+      sum = sat_add(sum, part.whole_of(U * VE, one_sum ? U * VE : 2 * U * VE));
+      if constexpr (kDrafts == kDistinct)
+        if (plain) draft = sat_add(draft, part_q.whole_of(U * VE, U * VE));
+      if (above_one<T>(most)) {  // -0 is a probability
 #pragma unroll
         for (int j = 0; j < U; ++j)
 #pragma unroll
@@ -447,11 +509,17 @@ __global__ void __launch_bounds__(kThreads, 2) accept_probs_kernel(const __grid_
         x.draft = sat_add(x.draft, __shfl_xor_sync(0xffffffffu, x.draft, o));
         x.bad |= __shfl_xor_sync(0xffffffffu, x.bad, o);
       }
+      uint64_t more = 0;
+      if (kDrafts == kDistinct && st.n_gone) {
+        if (lane < st.n_gone) more = gone_adds(lane);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) more += __shfl_xor_sync(0xffffffffu, more, o);
+      }
       if (lane == 0) {
-        total = x.sum;
+        left = x.sum + more;
         draft_sum = x.draft;
-        if (x.bad || total >= kFull || draft_sum >= kFull || !(uu[0] >= 0.f && uu[0] < 1.f) ||
-            ((kDrafts == kCertain || !pending) && total + gone_adds() == 0))
+        if (x.bad || x.sum >= kFull || draft_sum >= kFull || !(fine & 1u) ||
+            ((kDrafts == kCertain || !pending) && left == 0))
           bad_bits = STV_DEV_BAD_SAMPLE;
       }
     }
@@ -477,14 +545,13 @@ __global__ void __launch_bounds__(kThreads, 2) accept_probs_kernel(const __grid_
   __shared__ uint64_t left_s;
   if (tid == 0) {
     depth_s = depth;
-    // the row's whole mass, and what the tokens taken out add to their ranges
-    left_s = total + gone_adds();
-    for (int i = 0; i < st.n_gone; ++i) {
-      const int at = (st.gone[i] + pre) / VE / v_per;
-      const uint64_t x = st.gone_r[i] - rest_of(st.gone_p[i], st.gone_q[i], st.f);
-      share[pass & 1][at / kWarps].sum += x;
-      if (at / kWarps == rank) warp_sum[at % kWarps] += x;
-    }
+    left_s = left;  // the row's whole mass
+  }
+  if (tid < st.n_gone) {  // what the tokens taken out add to their ranges
+    const int at = (st.gone[tid] + pre) / VE / v_per;
+    const unsigned long long x = gone_adds(tid);
+    atomicAdd(reinterpret_cast<unsigned long long*>(&share[pass & 1][at / kWarps].sum), x);
+    if (at / kWarps == rank) atomicAdd(reinterpret_cast<unsigned long long*>(&warp_sum[at % kWarps]), x);
   }
   __syncthreads();
   if (rank == 0 && tid < T_) {
@@ -613,11 +680,14 @@ extern "C" int stv_tree_accept_probs(const int32_t* parent, const int32_t* draft
   a.path = path;
   a.out_ids = out_ids;
   a.status = dev_status;
-  // As many CTAs for a sequence as have 4,096 entries each, while the grid stays within one wave.
+  // As many CTAs for a sequence as have 4,096 entries each, while the grid stays
+  // within one wave (two CTAs on an SM without draft rows, by registers; 16 in a
+  // cluster find room only where there are few).
   int sm = 0;
   if (int rc = device_sm_count(&sm)) return rc;
   int cluster = kMaxCluster;
-  while (cluster > 1 && ((int64_t)n_seqs * cluster > (cluster > 8 ? sm : 2 * sm) || vocab < 4096 * cluster)) cluster /= 2;
+  auto fits = [&](int c) { return (int64_t)n_seqs * c <= (c > 8 || q ? sm : 2 * sm) && vocab >= 4096 * c; };
+  while (cluster > 1 && !fits(cluster)) cluster /= 2;
   cudaStream_t st = (cudaStream_t)stream;
   const cudaError_t e = dtype == STV_F32   ? launch_for<float>(a, drafts, n_seqs, cluster, st)
                         : dtype == STV_F16 ? launch_for<__half>(a, drafts, n_seqs, cluster, st)
