@@ -664,15 +664,15 @@ extern "C" int stv_paged_attn(const stv_shape* shape, const stv_attn_spec* spec,
   p.q_head = q->head_stride;
   p.o_row = o->row_stride;
   p.o_head = o->head_stride;
-  // (2^40: what a tensor map's strides may be)
-  p.q_wide = wide(q) && q->row_stride < (int64_t)1 << 38;
+  p.q_wide = wide(q);
   p.o_wide = wide(o);
   if (a.small) {
     if ((rc = make_pool_map(layer, sh, kSmallTile, sh.hd / 64, &p.map_k))) return rc;
   } else {
     if ((rc = make_pool_map(layer, sh, kBigTile, big_piece_bytes(sh.hd) / 16384, &p.map_k))) return rc;
     if ((rc = make_pool_map(layer, sh, big_piece_bytes(sh.hd) / (2 * sh.hd), sh.hd / 64, &p.map_v))) return rc;
-    if (p.q_wide && (rc = make_q_map(q, sh, n_rows, kMaxRows / sh.G, &p.map_q))) return rc;
+    // (strides that a tensor map does not take: plain loads)
+    if (p.q_wide && make_q_map(q, sh, n_rows, kMaxRows / sh.G, &p.map_q)) p.q_wide = false;
   }
   p.tile_bits = a.small ? 6 : 7;
   // Measured: 64 ragged single tokens of 128 channels take 82, 78, 69 and 66 us at 0, 1,
