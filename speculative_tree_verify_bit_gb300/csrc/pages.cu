@@ -320,8 +320,9 @@ __global__ void __launch_bounds__(kBookThreads) page_extend_kernel(const __grid_
   if (kRows) write_rows(p, start, threadIdx.x, p.map_rows, kBookThreads);
 }
 
-// The maps of many rows: a CTA writes kRowsPerCta of each.
-constexpr int kRowsPerCta = 1024;
+// The maps of many rows: a row a thread, since a row is three dependent trips to
+// memory.
+constexpr int kRowsPerCta = kCopyThreads;
 __global__ void __launch_bounds__(kCopyThreads) page_rows_kernel(const __grid_constant__ BookParams p) {
   extern __shared__ int start[];
   grid_dep_wait();
