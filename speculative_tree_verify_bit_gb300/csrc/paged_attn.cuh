@@ -1,18 +1,17 @@
 // paged_attn.cuh -- what the two kernels of stv_paged_attn share: parameters,
 // the cut of the work into equal shares, and the walk over a share.
 //
-// Work.  A unit is (entry, tokens_per consecutive new tokens of it, KV head):
-// at most 16 or 128 (256) rows of Q that read the same keys.  Its keys come in
-// tiles of 64 (single tokens) or 128: those of the first tokens (sinks) that lie before the window's
-// first tile, then the window's (or all up to the last visible key).  All tiles
-// of all units, in the order (entry, unit, head, tile), each unit's after a
-// few tiles' worth for its Q and its end, are cut into as many equal runs as there
-// are CTAs.  A unit inside one CTA's run is finished there;
-// a unit cut by the runs' borders leaves partials (O, and the running maximum and
-// sum of each row), at most two per CTA, which the join kernel puts together in
-// the runs' order.  So every CTA has the same work whatever the
-// lengths, a single long sequence is spread over all SMs, and the result
-// depends on the lengths alone.
+// Work.  A unit is (entry, tokens_per consecutive new tokens of it, KV head): at
+// most 16 or 128 (256) rows of Q that read the same keys.  Its keys come in tiles
+// of 64 (single tokens) or 128: those of the first tokens (sinks) that lie before
+// the window's first tile, then the window's (or all up to the last visible key).
+// All tiles of all units, in the order (entry, unit, head, tile), each unit's after
+// a few tiles' worth for its Q and its end, are cut into as many equal runs as there
+// are CTAs.  A unit inside one CTA's run is finished there; a unit cut by the runs'
+// borders leaves partials (O, and the running maximum and sum of each row), at most
+// two per CTA, which the join kernel puts together in the runs' order.  So every
+// CTA has the same work whatever the lengths, a single long sequence is spread over
+// all SMs, and the result depends on the lengths alone.
 //
 // The lengths are on the device: each CTA works its own run out (a scan over the
 // entries, one over the units), which costs about as much as one dependent load
