@@ -437,7 +437,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
     for (int j = 0; j < kPer; ++j) v[j] *= f0;
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
-      if (x[k].x == -INFINITY) continue;  // not there, or without keys
+      if (x[k].x == -INFINITY && x[k].y == 0.f) continue;  // not there, or without keys (NaN scores count)
       const float f = ex2(x[k].x - ref);
       L += f * x[k].y;
       v[0] += f * a[k].x;
@@ -470,7 +470,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
     }
   }
   if (r >= rec.rows) return;
-  const float inv = L > 0.f ? 1.f / L : 0.f;
+  const float inv = L == 0.f ? 0.f : 1.f / L;
 #pragma unroll
   for (int k = 0; k < kPer; ++k) v[k] *= inv;
   T* dst = static_cast<T*>(p.o) + (int64_t)(rec.row0 + r / p.G) * p.o_row + (int64_t)(rec.h * p.G + r % p.G) * p.o_head;

@@ -293,6 +293,30 @@ def test_offsets_past_32_bits(gpu):
     check(d, q[:1], [(0, n - 1, 0, 1)], call(d, q[:1].clone(), [(0, n - 1, 0, 1)]))
 
 
+@pytest.mark.parametrize("n,ctx", [(1, 40), (1, 9000), (30, 40), (30, 9000)])
+@pytest.mark.parametrize("hd", [64, 256])
+def test_nan_goes_where_it_is_seen(gpu, n, ctx, hd):
+    """A head of q that is NaN, and a key that is: the rows that see them and no others, whether
+    or not their units are cut."""
+    d = Drafter([ctx + n], 2, hd, BF16, seed=15)
+    q = d.rows(n, 8)
+    entries = [(0, ctx, 0, n)]
+    clean = call(d, q, entries)
+    bad = q.clone()
+    bad[n - 1, 5] = float("nan")
+    got = call(d, bad, entries)
+    assert got[n - 1, 5].isnan().all()
+    got[n - 1, 5] = clean[n - 1, 5]
+    assert torch.equal(got, clean)
+    if n > 1:  # the last token's key: its own row sees it
+        pos = ctx + n - 1
+        d.data[int(d.pool.tables[0, pos // PAGE]), 1, 0, pos % PAGE] = float("nan")
+        got = call(d, q, entries)
+        assert got[n - 1, 4:].isnan().all()
+        got[n - 1, 4:] = clean[n - 1, 4:]
+        assert torch.equal(got, clean)
+
+
 # ------------------------------------------------------------ stv_kv_write --
 
 @pytest.mark.parametrize("hkv,hd,dtype", [(4, 256, FP16), (1, 64, BF16), (3, 128, BF16)])
