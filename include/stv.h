@@ -753,7 +753,9 @@ typedef struct {
  * (STV_DEV_BAD_PAGE); a row without keys is zero.  An entry whose rows are not
  * within [0, n_rows) in ascending order, or are more than max_new, is left
  * out (STV_DEV_BAD_ROW), as is one whose sequence is not in the pool or whose
- * ctx is negative or past 2^30 (STV_DEV_BAD_SEQ).
+ * ctx is negative or past 2^30 (STV_DEV_BAD_SEQ).  Entries share no rows: where
+ * they do, o is any of the answers there, or nothing is written and
+ * STV_DEV_BAD_ROW set.  A sequence may be in the list twice.
  */
 int stv_paged_attn_workspace_bytes(const stv_shape* shape, int max_new, size_t* bytes);
 int stv_paged_attn(const stv_shape* shape, const stv_attn_spec* spec, const stv_layer_cache* layer,

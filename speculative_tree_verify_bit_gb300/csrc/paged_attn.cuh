@@ -187,7 +187,7 @@ __device__ __forceinline__ RunStart run_of(const AttnParams& p, int* scratch) {
   // units of the entries before
   const int per = (p.n + kThreads - 1) / kThreads;
   const int e0 = min(tid * per, p.n), e1 = min(e0 + per, p.n);
-  int mine = 0;
+  long long mine = 0;
   for (int e = e0; e < e1; ++e) {
     const int nu = (entry_of(p, e).L + p.tokens_per - 1) / p.tokens_per;
     scratch[e] = nu;
@@ -195,7 +195,9 @@ __device__ __forceinline__ RunStart run_of(const AttnParams& p, int* scratch) {
   }
   long long all;
   int at = (int)cta_scan<kThreads>(mine, &all);
-  const int n_units = (int)all;
+  // (more units than rows: entries share rows, and their sum may be anything)
+  const int n_units = all > p.n_rows ? 0 : (int)all;
+  if (all > p.n_rows && tid == 0) report(p.status, STV_DEV_BAD_ROW);
   for (int e = e0; e < e1; ++e) {
     const int nu = scratch[e];
     scratch[e] = at;

@@ -317,6 +317,78 @@ def test_nan_goes_where_it_is_seen(gpu, n, ctx, hd):
         assert torch.equal(got, clean)
 
 
+def test_entries_that_share_rows(gpu):
+    """More tiles of rows than there are rows: nothing is written."""
+    d = Drafter([300] * 60, 1, 64, BF16, seed=16)
+    q = d.rows(8, 128)
+    shape = stv.make_row_shape(128, 1, 64, BF16)
+    ws = torch.empty(stv.stv_paged_attn_workspace_bytes(shape, 8), dtype=torch.uint8, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    o = torch.full_like(q, 7.0)
+    stv.stv_paged_attn(shape, stv.make_attn(), d.layer, d.pool, None, dev([200] * 60), dev([0, 8] * 30 + [0]), 8, q, o, ws,
+                       status)
+    assert status.item() == stv.STV_DEV_BAD_ROW and (o == 7.0).all()
+
+
+@pytest.mark.parametrize("max_new", [2, 40])
+def test_a_sequence_twice_in_the_list(gpu, max_new):
+    d = Drafter([700, 90], 2, 128, BF16, seed=17)
+    q = d.rows(6, 8)
+    q[4:] = q[:2]
+    entries = [(0, 698, 0, 2), (1, 88, 2, 2), (0, 698, 4, 2)]
+    o = call(d, q, entries, max_new=max_new)
+    check(d, q, entries, o)
+
+
+@pytest.mark.parametrize("max_new", [1, 20])
+def test_the_most_entries(gpu, max_new):
+    """4,096 entries, most without rows, on the two kernels; one more is refused."""
+    rng = np.random.default_rng(18)
+    lens = [(int(c), int(k)) for c, k in zip(rng.integers(0, 30, 4096), rng.random(4096) < 0.2)]
+    lens[4095] = (2500, 1)
+    entries, n = ragged(lens)
+    d = Drafter([c + k if k else 0 for c, k in lens], 1, 64, FP16, seed=18)
+    q = d.rows(n, 2)
+    check(d, q, entries, call(d, q, entries, max_new=max_new))
+
+
+@pytest.mark.parametrize("n", [1, 20])
+def test_windows_and_first_tokens_without_end(gpu, n):
+    """The largest window sees what no window does; so do the most first tokens."""
+    d = Drafter([900 + n], 2, 64, FP16, seed=19)
+    q = d.rows(n, 8)
+    entries = [(0, 900, 0, n)]
+    want = call(d, q, entries)
+    most = (1 << 31) - 1
+    assert torch.equal(call(d, q, entries, window=most), want)
+    assert torch.equal(call(d, q, entries, window=most, sinks=most), want)
+    check(d, q, entries, call(d, q, entries, window=3, sinks=most), window=3, sinks=most)
+
+
+@pytest.mark.parametrize("n", [1, 40])
+def test_two_calls_at_once(gpu, n):
+    """Two streams, a workspace each."""
+    lens = [(6000, n), (50, n)]
+    entries, rows = ragged(lens)
+    d = Drafter([c + n for c, _ in lens], 2, 128, BF16, seed=20)
+    qs = [d.rows(rows, 8) for _ in range(2)]
+    want = [call(d, q, entries) for q in qs]
+    shape, spec = stv.make_row_shape(8, 2, 128, BF16), stv.make_attn()
+    ws = [torch.empty(stv.stv_paged_attn_workspace_bytes(shape, n), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    ctx, start = dev([c for c, _ in lens]), dev([0, n, 2 * n])
+    outs = [torch.full_like(q, 7.0) for q in qs]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(10):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                stv.stv_paged_attn(shape, spec, d.layer, d.pool, None, ctx, start, n, qs[i], outs[i], ws[i])
+    for s in streams:
+        torch.cuda.current_stream().wait_stream(s)
+    assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
 # ------------------------------------------------------------ stv_kv_write --
 
 @pytest.mark.parametrize("hkv,hd,dtype", [(4, 256, FP16), (1, 64, BF16), (3, 128, BF16)])
