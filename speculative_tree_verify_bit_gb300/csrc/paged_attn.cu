@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, Small<HD>::kCtasPerSm)
               o[n][i + 1] *= corr;
             }
           }
-          const float ref = m[half] == -INFINITY ? 0.f : m[half];
+          const float ref = (m[half] == -INFINITY ? 0.f : m[half]) - kLift<T>;
           // The sum takes P as the product takes it, rounded to the cache's type.
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
@@ -596,7 +596,7 @@ int make_q_map(const stv_rows* q, const RowShape& sh, int n_rows, int tokens, CU
   return encode(map, sh.bf16, 4, q->data, dims, strides, box);
 }
 
-// Whether the bytes of a view and of another (or of a range) can meet, by their extents.
+// Whether the bytes of two views can meet, by their extents.
 struct Extent {
   uintptr_t a, b;
 };
@@ -651,8 +651,7 @@ extern "C" int stv_paged_attn(const stv_shape* shape, const stv_attn_spec* spec,
     const int64_t c = n_rows > 1 ? (d % st + st) % st : d;
     if (n_rows == 1 || st != o->row_stride || c < wide || c + wide_o > st) return STV_ERR_INVALID_ARG;
   }
-  const Extent cache = {(uintptr_t)layer->pool, (uintptr_t)layer->pool + (uintptr_t)layer->page_bytes * layer->n_pages};
-  if (meet(cache, extent_of(o, sh.hd, n_rows))) return STV_ERR_INVALID_ARG;
+  if (rows_meet_pool(o, sh.hd, n_rows, layer)) return STV_ERR_INVALID_ARG;
   AttnPlan a;
   if ((rc = plan_attn(sh, max_new, &a))) return rc;
   if (ws_bytes < a.bytes) return STV_ERR_WORKSPACE_TOO_SMALL;

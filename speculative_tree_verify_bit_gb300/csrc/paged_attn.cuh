@@ -21,6 +21,8 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 
+#include <type_traits>
+
 #include "stv_device.cuh"
 #include "tc_util.cuh"
 
@@ -352,6 +354,12 @@ __device__ __forceinline__ void tma_box(void* dst, const CUtensorMap* map, int r
       "l"(map), "r"(0), "r"(row), "r"(block), "r"(su32(bar))
       : "memory");
 }
+
+// P = 2^(s - m + kLift): in fp16, whose values end at 2^16 and 2^-24, it may be up
+// to 2^15 (the maximum is up to 2^8 behind), so that what a long flat tail adds is
+// kept down to 2^-31 of the largest; O and the sum carry the same factor.
+template <typename T>
+constexpr float kLift = std::is_same<T, __half>::value ? 7.f : 0.f;
 
 template <typename T>
 struct Pack;

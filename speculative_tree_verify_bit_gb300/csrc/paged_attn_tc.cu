@@ -585,9 +585,9 @@ __global__ void __launch_bounds__(Tiles<HD, NQ>::kThreads, 1)
             }
           }
         }
-        // P = 2^(S c - m_ref), rounded to the cache's type, packed in key pairs into
+        // P = 2^(S c - m_ref + kLift), rounded to the cache's type, packed in key pairs into
         // S's columns; the row's sum takes it before the rounding.
-        const float mref = m_ref == -INFINITY ? 0.f : m_ref;
+        const float mref = (m_ref == -INFINITY ? 0.f : m_ref) - kLift<T>;
         const float2 c2 = make_float2(c, c), nm2 = make_float2(-mref, -mref);
         float2 sum4[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll

@@ -389,6 +389,28 @@ def test_two_calls_at_once(gpu, n):
     assert all(torch.equal(a, b) for a, b in zip(outs, want))
 
 
+@pytest.mark.parametrize("n", [1, 20])
+@pytest.mark.parametrize("dtype", [FP16, BF16], ids=str)
+def test_a_long_flat_tail_counts(gpu, n, dtype):
+    """One key far ahead of 100,000 equal ones, each 2^-26 of it: together 1.5e-3."""
+    length = 100000
+    d = Drafter([length], 1, 64, dtype, seed=21, fill=0.0)
+    for e in range(-(-length // PAGE)):
+        page = int(d.pool.tables[0, e])
+        d.data[page, 0, 0] = 0
+        d.data[page, 0, 1] = 1.0
+    d.data[int(d.pool.tables[0, 0]), 0, 0, 7] = 1.0
+    d.data[int(d.pool.tables[0, 0]), 0, 1, 7] = 0.0
+    q = torch.ones((n, 2, 64), dtype=dtype, device="cuda")
+    got = call(d, q, [(0, length - n, 0, n)], scale=26 * np.log(2.0) / 64).double()
+    tail = (length - n + torch.arange(1, n + 1, device="cuda").double() - 1) * 2.0 ** -26
+    want = (tail / (1 + tail))[:, None, None]
+    # P (2^-26 and 1) is exact in both types, the result rounded; 26 ln 2 log2(e) / 64 in fp32, and fp32 sums
+    # of up to 100,000 equal numbers
+    tol = want * (torch.finfo(dtype).eps / 2 + 26 * 2.0 ** -22 + length * 2.0 ** -24)
+    assert ((got - want).abs() <= tol).all()
+
+
 # ------------------------------------------------------------ stv_kv_write --
 
 @pytest.mark.parametrize("hkv,hd,dtype", [(4, 256, FP16), (1, 64, BF16), (3, 128, BF16)])
