@@ -707,7 +707,7 @@ int stv_page_extend(const stv_page_pool* pool, const int32_t* seqs, int n, const
  *
  * stv_kv_write puts row r of k and v, hkv heads each, into slot slots[r].
  *  k, v:  views of n_rows rows (heads = hkv), of the cache's type; any strides
- *         (k and v may lie inside the rows of one projection).
+ *         (k and v may lie inside the rows of one projection, not in the pool).
  *  slots: device int32 [n_rows], distinct; -1: the row is left out; any other
  *         slot outside the pool is left out and reported (STV_DEV_BAD_PAGE).
  */
@@ -789,8 +789,8 @@ int stv_paged_attn(const stv_shape* shape, const stv_attn_spec* spec, const stv_
  *  n_commit, path, out_ids: as stv_tree_accept writes them; stv_kv_commit takes
  *            them.
  * R and its sums are 64-bit integers in units of 2^-60, so the result does not
- * depend on the order of threads; u Z S(x) < R(x) is decided in 64 bits.  Z S(y)
- * is off by less than 2^-46 of itself from the second rejection at a node on.
+ * depend on the order of threads.  u Z S(x) < R(x) is decided exactly where
+ * nothing was rejected before, later with Z S(y) off by less than 2^-45 of itself.
  * A sequence with a bad tree gets n_commit 0 and -1 (STV_DEV_BAD_TREE); so does
  * one whose walk reads a probability outside [0, 1] or NaN, a u outside
  * [0, 1), or a row that adds up to nothing or to 4 or more (STV_DEV_BAD_SAMPLE).

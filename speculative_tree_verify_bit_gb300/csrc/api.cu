@@ -59,6 +59,12 @@ int check_row_layer(const stv_layer_cache* l, const RowShape& sh) {
   return STV_OK;
 }
 
+bool rows_meet_pool(const stv_rows* v, int head_dim, int n_rows, const stv_layer_cache* l) {
+  const uintptr_t a = (uintptr_t)v->data, p = (uintptr_t)l->pool;
+  const uintptr_t b = a + 2 * ((n_rows - 1) * v->row_stride + (v->heads - 1) * v->head_stride + head_dim);
+  return a < p + (uintptr_t)l->page_bytes * l->n_pages && p < b;
+}
+
 bool rows_view_ok(const stv_rows* v, int head_dim, int n_rows) {
   if (!v->data || v->heads < 1 || v->heads > 1 << 17 || v->head_stride < head_dim) return false;
   // an extent of at most 2^50 bytes, so that no offset overflows

@@ -83,6 +83,7 @@ extern "C" int stv_kv_write(const stv_shape* shape, const stv_layer_cache* layer
   for (int t = 0; t < 2; ++t) {
     const stv_rows* x = in[t];
     if (!rows_view_ok(x, sh.hd, n_rows) || x->heads != sh.hkv || (uintptr_t)x->data % 2) return STV_ERR_INVALID_ARG;
+    if (rows_meet_pool(x, sh.hd, n_rows, layer)) return STV_ERR_INVALID_ARG;
     wide = wide && (uintptr_t)x->data % 16 == 0 && (x->heads == 1 || x->head_stride % 8 == 0) &&
            (n_rows == 1 || x->row_stride % 8 == 0);
     p.in[t] = static_cast<const uint8_t*>(x->data);

@@ -267,6 +267,8 @@ int check_row_shape(const stv_shape* sh, RowShape* out);
 int check_row_layer(const stv_layer_cache* l, const RowShape& sh);
 // A view of rows of heads whose extents fit (api.cu).
 bool rows_view_ok(const stv_rows* v, int head_dim, int n_rows);
+// Whether the bytes of such a view meet those of a cache's pool.
+bool rows_meet_pool(const stv_rows* v, int head_dim, int n_rows, const stv_layer_cache* l);
 int device_sm_count(int* n);
 int make_plan(const ShapeInfo& sh, const stv_seq* seqs, int n_seqs, int sm_count, Plan* plan, bool balance);
 WsLayout ws_layout(const ShapeInfo& sh, int n_seqs, const Plan& plan);

@@ -91,6 +91,8 @@ def test_extend_refusals(lib, kw, rc):
     (dict(k=rows(head=64)), BAD), (dict(v=rows(row=256)), BAD), (dict(k=rows(row=1 << 46), n=1 << 20), BAD),
     (dict(l=layer(shape(), pool=0)), BAD), (dict(l=layer(shape(), pool=D + 8)), BAD), (dict(l=layer(shape(), n_pages=0)), BAD),
     (dict(l=layer(shape(), page_bytes=4096)), SHAPE), (dict(l=layer(shape(), n_pages=1 << 20)), SHAPE),
+    (dict(k=rows(D + (1 << 40) + 4096)), BAD), (dict(v=rows(D + (1 << 40) + 8 * 4 * 1024 * 128 - 2)), BAD),
+    (dict(k=rows(D + (1 << 40) - 8192 - 1024 + 2)), BAD),
 ])
 def test_write_refusals(lib, kw, rc):
     s = shape()
