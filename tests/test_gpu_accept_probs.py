@@ -44,7 +44,8 @@ def call(parent, ids, p, q, u, distinct=False, status=None):
 @pytest.mark.parametrize("dtype", DTYPES, ids=str)
 @pytest.mark.parametrize("n,t,vocab,pad,shift,shape", [
     (3, 1, 1, 0, 0, "chain"), (5, 8, 17, 0, 0, "tree"), (4, 32, 1000, 3, 1, "star"), (6, 16, 4097, 0, 0, "tree"),
-    (2, 32, 33000, 8, 0, "chain"), (1, 9, 131071, 1, 3, "tree"), (40, 12, 9001, 0, 0, "star")])
+    (2, 32, 33000, 8, 0, "chain"), (1, 9, 131071, 1, 3, "tree"), (40, 12, 9001, 0, 0, "star"),
+    (1, 7, 524288, 0, 0, "star")])
 def test_rows_of_every_kind(gpu, n, t, vocab, pad, shift, shape, dtype, drafts):
     rng = np.random.default_rng(t + vocab)
     p = rows(rng, n * t, vocab, dtype, vocab + pad, 2.0, shift)
