@@ -515,8 +515,9 @@ __global__ void __launch_bounds__(kThreads, kDrafts == kCertain ? 2 : 1) accept_
         x.bad |= __shfl_xor_sync(0xffffffffu, x.bad, o);
       }
       uint64_t more = 0;
-      if (kDrafts == kDistinct && st.n_gone) {
-        if (lane < st.n_gone) more = gone_adds(lane);
+      const int n_gone = kDrafts == kDistinct ? st.n_gone : 0;
+      if (n_gone) {
+        if (lane < n_gone) more = gone_adds(lane);
 #pragma unroll
         for (int o = 16; o; o >>= 1) more += __shfl_xor_sync(0xffffffffu, more, o);
       }
@@ -527,6 +528,7 @@ __global__ void __launch_bounds__(kThreads, kDrafts == kCertain ? 2 : 1) accept_
             ((kDrafts == kCertain || !pending) && left == 0))
           bad_bits = STV_DEV_BAD_SAMPLE;
       }
+      __syncwarp();  // lane 0 goes on to the walk, which changes what the others have just read of st
     }
     // (thread 0's next decisions are behind this loop's first barrier; it alone reads what it wrote)
   }
