@@ -687,7 +687,8 @@ int stv_page_copy(const stv_shape* shape, const stv_layer_cache* layers, int n_l
  *  seqs: device int32 [n], distinct, or NULL: entry i is sequence i.
  *  n_new: device int32 [n], >= 0.   ctx: device int32 [max_seqs].
  *  max_rows: 0 .. 2^26 (else STV_ERR_SHAPE_UNSUPPORTED).
- * All or nothing: where anything is wrong (STV_DEV_BAD_SEQ; STV_DEV_NO_PAGES;
+ * All or nothing: where anything is wrong (STV_DEV_BAD_SEQ, also where ctx + L
+ * is past the table or past 2^31 - 1; STV_DEV_NO_PAGES;
  * STV_DEV_BAD_ROW: a negative n_new, or more rows than max_rows) the books stay
  * as they were, row_start is 0 and the maps are -1, so that the calls after it
  * find no rows.  A row on a table entry outside the pool gets slot -1

@@ -277,8 +277,9 @@ __global__ void __launch_bounds__(kBookThreads) page_extend_kernel(const __grid_
       continue;
     }
     const int have = pool.counts[s], c = p.ctx[s];
-    const int64_t need = ((int64_t)c + more + kPageTok - 1) / kPageTok;
-    if (have < 0 || c < 0 || have > pool.table_stride || need > pool.table_stride)
+    // (positions are 32-bit; a table whose pages are named again may be long enough for more)
+    const int64_t end = (int64_t)c + more, need = (end + kPageTok - 1) / kPageTok;
+    if (have < 0 || c < 0 || have > pool.table_stride || need > pool.table_stride || end > 0x7fffffff)
       bad |= STV_DEV_BAD_SEQ;
     else if (need > have)
       off[i] = (int)min(need - have, (int64_t)pool.n_pages + 1);
