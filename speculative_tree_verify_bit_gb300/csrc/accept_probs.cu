@@ -87,10 +87,10 @@ struct Parts {
   int h, l, s;
 };
 __device__ __forceinline__ Parts parts_of(float x) {
-  const float t = x + 2.f, r = x - (t - 2.f);          // r exact, at most 2^-23
-  const float t2 = fmaf(r, 4194304.f, 3.f);            // 2^22 r
-  const float r2 = fmaf(t2 - 3.f, -2.384185791015625e-7f, r);  // exact, at most 2^-45
-  const float t3 = fmaf(r2, 274877906944.f, 3.f);      // 2^38 r2
+  const float t = __fadd_rn(x, 2.f), r = __fsub_rn(x, __fsub_rn(t, 2.f));          // r exact, at most 2^-23
+  const float t2 = __fmaf_rn(r, 4194304.f, 3.f);                                   // 2^22 r
+  const float r2 = __fmaf_rn(__fsub_rn(t2, 3.f), -2.384185791015625e-7f, r);       // exact, at most 2^-45
+  const float t3 = __fmaf_rn(r2, 274877906944.f, 3.f);                             // 2^38 r2
   return {__float_as_int(t) - 0x40000000, __float_as_int(t2) - 0x40400000, __float_as_int(t3) - 0x40400000};
 }
 __device__ __forceinline__ uint64_t whole(const Parts& x) {
@@ -99,25 +99,28 @@ __device__ __forceinline__ uint64_t whole(const Parts& x) {
 __device__ __forceinline__ uint64_t fixed(float x) { return whole(parts_of(x)); }
 // The same of a number of at most 2^-22, without h.
 __device__ __forceinline__ Parts small_parts_of(float x) {
-  const float t2 = fmaf(x, 4194304.f, 3.f), r2 = fmaf(t2 - 3.f, -2.384185791015625e-7f, x);
-  const float t3 = fmaf(r2, 274877906944.f, 3.f);
+  const float t2 = __fmaf_rn(x, 4194304.f, 3.f);
+  const float r2 = __fmaf_rn(__fsub_rn(t2, 3.f), -2.384185791015625e-7f, x);
+  const float t3 = __fmaf_rn(r2, 274877906944.f, 3.f);
   return {0, __float_as_int(t2) - 0x40400000, __float_as_int(t3) - 0x40400000};
 }
 
 // a += max(p - F q, 0).  F q = x + w with w at most 2^-23 x; where p >= x, p - x = d + e
 // exactly; d + e - w has the sign of (p - x) - w, since d is exact where w matters.
+// (Each operation here is rounded by itself, and as add_above2 rounds it: the last
+// token is looked for among the same numbers as a pass has added up, so the running
+// sums end where the mass does.)
 template <bool kOneF>
 __device__ __forceinline__ void add_above(Parts& a, float p, float q, float2 f) {
-  const float x = kOneF ? q : q * f.x;
-  const float d = p - x;
-  float e = (p - d) - x, sign = d;
+  const float x = kOneF ? q : __fmul_rn(q, f.x);
+  const float d = __fsub_rn(p, x);
+  float e = __fsub_rn(__fsub_rn(p, d), x), w = 0.f;
   if constexpr (!kOneF) {
-    const float w = fmaf(q, f.y, fmaf(q, f.x, -x));
-    e -= w;
-    sign = d - w;
+    w = __fmaf_rn(q, f.y, __fmaf_rn(q, f.x, -x));
+    e = __fsub_rn(e, w);
   }
   const Parts y = parts_of(d), z = small_parts_of(e);
-  if (sign > 0.f) {
+  if (d > w) {
     a.h += y.h;
     a.l += y.l + z.l;
     a.s += y.s + z.s;
@@ -132,10 +135,11 @@ __device__ __forceinline__ uint64_t rest_of(float p, float q, float2 f) {
 }
 // The walk's own arithmetic, one thread's, in pairs of floats (x + y, y at most
 // half a place of x): about 2^-46, at a few cycles an operation where an fp64 one
-// takes a hundred.
+// takes a hundred.  A product that goes on into a sum has to be rounded first, which
+// the compiler is free not to do with * and +.
 __device__ __forceinline__ float2 pair_sum(float a, float b) {  // |a| >= |b|
-  const float s = a + b;
-  return make_float2(s, b - (s - a));
+  const float s = __fadd_rn(a, b);
+  return make_float2(s, __fsub_rn(b, __fsub_rn(s, a)));
 }
 __device__ __forceinline__ float2 pair_of(uint64_t x) {  // of x units
   if (x == 0) return make_float2(0.f, 0.f);
@@ -143,21 +147,21 @@ __device__ __forceinline__ float2 pair_of(uint64_t x) {  // of x units
   x <<= s;
   const uint32_t top = (uint32_t)(x >> 40), rest = (uint32_t)(x >> 8);  // 24 bits, the next 32
   const float unit = __int_as_float((127 - 36 + 16 - s) << 23);       // 2^(64 - 24 - 60 - s)
-  return pair_sum((float)top * unit, (float)rest * 2.3283064365386963e-10f * unit);
+  return pair_sum(__fmul_rn((float)top, unit), __fmul_rn(__fmul_rn((float)rest, 2.3283064365386963e-10f), unit));
 }
 __device__ __forceinline__ float2 operator*(float2 a, float2 b) {
-  const float x = a.x * b.x;
-  return pair_sum(x, fmaf(a.x, b.x, -x) + fmaf(a.x, b.y, a.y * b.x));
+  const float x = __fmul_rn(a.x, b.x);
+  return pair_sum(x, __fadd_rn(__fmaf_rn(a.x, b.x, -x), __fmaf_rn(a.x, b.y, __fmul_rn(a.y, b.x))));
 }
 __device__ __forceinline__ float2 operator/(float2 a, float2 b) {  // b > 0
-  const float r = 1.f / b.x, q = a.x * r;
+  const float r = 1.f / b.x, q = __fmul_rn(a.x, r);
   const float2 back = b * make_float2(q, 0.f);
-  return pair_sum(q, ((a.x - back.x) + (a.y - back.y)) * r);
+  return pair_sum(q, __fmul_rn(__fadd_rn(__fsub_rn(a.x, back.x), __fsub_rn(a.y, back.y)), r));
 }
 __device__ __forceinline__ float2 operator+(float2 a, float2 b) {  // both at least 0
   const bool swap = b.x > a.x;
   const float2 s = pair_sum(swap ? b.x : a.x, swap ? a.x : b.x);
-  return pair_sum(s.x, s.y + (a.y + b.y));
+  return pair_sum(s.x, __fadd_rn(s.y, __fadd_rn(a.y, b.y)));
 }
 __device__ __forceinline__ bool operator<(float2 a, float2 b) { return a.x < b.x || (a.x == b.x && a.y < b.y); }
 
