@@ -290,8 +290,8 @@ __global__ void __launch_bounds__(kThreads, kDrafts == kCertain ? 2 : 1) accept_
     const uint32_t with = __match_any_sync(0xffffffffu, there ? pa : -1);
     if (there && lane == __ffs(with) - 1) kids[pa] = with;
     const uint32_t good = __ballot_sync(0xffffffffu, is_prob(px) && is_prob(qx) && u >= 0.f && u < 1.f);
-    // u q < p, exactly: two 24-bit numbers, and one
-    const uint32_t take = __ballot_sync(0xffffffffu, make_float2(u, 0.f) * make_float2(qx, 0.f) < make_float2(px, 0.f));
+    // u q < p, exactly, however small: two 24-bit numbers make one of 48
+    const uint32_t take = __ballot_sync(0xffffffffu, (double)u * (double)qx < (double)px);
     if (tid == 0) {
       bad_bits = any ? STV_DEV_BAD_TREE : 0;
       st.f = make_float2(0.f, 0.f);

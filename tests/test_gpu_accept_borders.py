@@ -202,3 +202,25 @@ def test_last_tokens_close_to_the_border(gpu, vocab, n, drafts):
         u[s, 0] = near[ok[int(np.argmin(off[ok]))]]
     check(np.tile([-1, 0, 0, 0], (n, 1)), ids, p, None if drafts == "certain" else q, u, drafts == "distinct",
           nearest=2.0 ** -41)
+
+
+def test_first_children_of_tiny_shares(gpu):
+    """u q where its low half, or all of it, lies below fp32's smallest number."""
+    rng = np.random.default_rng(2)
+    n, vocab = 3000, 4
+    tiny = np.float32(2.0 ** -149)
+    share = np.float32(2.0 ** -rng.uniform(80, 146, n))
+    share[::7] = np.float32(tiny * rng.integers(1, 9, len(share[::7])))
+    u = np.float32(rng.random(n) * 0.999 + 0.0005)
+    prod = u.astype(np.float64) * share.astype(np.float64)
+    near = np.float32(prod)
+    other = np.where(near > prod, np.nextafter(near, np.float32(0)), np.nextafter(near, np.float32(1)))
+    p_x = np.where(rng.random(n) < 0.5, near, other).astype(np.float32)
+    p, q = np.zeros((2 * n, vocab), np.float32), np.full((2 * n, vocab), 0.1, np.float32)
+    p[:, 0] = 0.5
+    p[::2, 3], q[::2, 3] = p_x, share
+    uu = np.stack([np.full(n, 0.25, np.float32), u], 1)
+    nc, path, out = call(np.tile([-1, 0], (n, 1)), np.tile([0, 3], (n, 1)), p, q, uu)
+    want = np.array([Fraction(float(a)) * Fraction(float(b)) < Fraction(float(c)) for a, b, c in zip(u, share, p_x)])
+    assert 0.3 < want.mean() < 0.7
+    assert (nc == 1 + want).all(), (int((nc != 1 + want).sum()), np.nonzero(nc != 1 + want)[0][:10])
