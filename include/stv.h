@@ -765,6 +765,20 @@ int stv_paged_attn(const stv_shape* shape, const stv_attn_spec* spec, const stv_
                    void* workspace, size_t ws_bytes, int32_t* dev_status, stv_stream_t stream);
 
 /*
+ * Failure-path test of stv_paged_attn (see stv_verify_attn_timeout_test).  Same
+ * arguments and checks, but the kernel's producer issues none of its copies of K
+ * and V, so every wait on them gives up after its bound (about 1.3 s), the kernel
+ * stops every role, waits for anything it issued, frees its tensor memory, ORs
+ * STV_DEV_TIMEOUT into *dev_status and returns.  The entries' rows of o are then
+ * invalid; the CUDA context stays usable.
+ */
+int stv_paged_attn_timeout_test(const stv_shape* shape, const stv_attn_spec* spec, const stv_layer_cache* layer,
+                                const stv_page_pool* pool, const int32_t* seqs, int n, const int32_t* ctx,
+                                const int32_t* row_start, int max_new, const stv_rows* q, const stv_rows* o,
+                                int n_rows, void* workspace, size_t ws_bytes, int32_t* dev_status,
+                                stv_stream_t stream);
+
+/*
  * Verification of drafted tokens against the target's probabilities (the
  * sampled counterpart of stv_tree_accept; what is committed is distributed as
  * the target's own sampling).  At a node with target row p and draft row q,

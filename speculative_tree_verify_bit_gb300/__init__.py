@@ -58,7 +58,7 @@ EXPORTS = (
     "stv_prefill_attn_timeout_test", "stv_append_verify_combine", "stv_rope", "stv_sample",
     "stv_page_workspace_bytes", "stv_page_reserve", "stv_page_fork", "stv_page_free", "stv_page_compact",
     "stv_page_copy", "stv_page_extend", "stv_kv_write", "stv_paged_attn_workspace_bytes", "stv_paged_attn",
-    "stv_tree_accept_probs",
+    "stv_tree_accept_probs", "stv_paged_attn_timeout_test",
 )
 
 
@@ -176,6 +176,8 @@ def load() -> ctypes.CDLL:
         lib.stv_paged_attn_workspace_bytes.argtypes = [P, I, P]
         lib.stv_paged_attn.restype = I
         lib.stv_paged_attn.argtypes = [P, P, P, P, P, I, P, P, I, P, P, I, P, ctypes.c_size_t, P, P]
+        lib.stv_paged_attn_timeout_test.restype = I
+        lib.stv_paged_attn_timeout_test.argtypes = lib.stv_paged_attn.argtypes
         lib.stv_tree_accept_probs.restype = I
         lib.stv_tree_accept_probs.argtypes = [P, P, P, I64, P, I64, I, I, I, P, I, I, P, P, P, P, P]
         _lib = lib
@@ -859,19 +861,32 @@ def stv_paged_attn(shape, spec: stv_attn_spec, layer: RowCache, pool: PagePool, 
     seqs[i] (None: sequence i) with the rows row_start[i] .. row_start[i + 1] - 1
     (int32 [n + 1]; None: one row each) at positions ctx[s] and on; no entry has
     more than max_new rows (include/stv.h)."""
+    _paged_attn("stv_paged_attn", shape, spec, layer, pool, seqs, ctx, row_start, max_new, q, o, workspace, dev_status,
+                stream)
+
+
+def stv_paged_attn_timeout_test(shape, spec: stv_attn_spec, layer: RowCache, pool: PagePool, seqs, ctx, row_start,
+                                max_new: int, q, o, workspace, dev_status=None, stream=None):
+    """stv_paged_attn with the kernel's copies withheld: every wait runs out
+    and the kernel reports STV_DEV_TIMEOUT (failure-path test)."""
+    _paged_attn("stv_paged_attn_timeout_test", shape, spec, layer, pool, seqs, ctx, row_start, max_new, q, o, workspace,
+                dev_status, stream)
+
+
+def _paged_attn(fn, shape, spec, layer, pool, seqs, ctx, row_start, max_new, q, o, workspace, dev_status, stream):
     i32 = _t().int32
     dev = pool._on_current()
     lc, dt = _row_cache(shape, layer, dev)
     n_rows, hd = q.shape[0], shape.head_dim
     n = row_start.numel() - 1 if row_start is not None else seqs.numel() if seqs is not None else n_rows
-    rc = load().stv_paged_attn(
+    rc = getattr(load(), fn)(
         ctypes.byref(shape), ctypes.byref(spec), lc, pool._ref, _raw(seqs, i32, dev, "seqs", n), n,
         _raw(ctx, i32, dev, "ctx", pool._c.max_seqs), _raw(row_start, i32, dev, "row_start"), int(max_new),
         _rows(q, n_rows, hd, dt, dev, "q"), _rows(o, n_rows, hd, dt, dev, "o"), n_rows,
         _raw(workspace, None, dev, "workspace"), workspace.nbytes, _raw(dev_status, i32, dev, "dev_status"),
         _raw_stream(stream, dev))
     if rc:
-        raise StvError("stv_paged_attn", rc)
+        raise StvError(fn, rc)
 
 
 def stv_tree_accept_probs(parent, draft_ids, p, q, u, n_commit, path, out_ids, distinct: bool = False,

@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(kThreads, Small<HD>::kCtasPerSm)
     RunWalk run(p, start);
     JoinRecord rec = {0, 0, 0, 0};
     PageWalk pages;
-    int g = 0, n_units = 0;
+    int g = 0, n_units = 0, issued = 0;
     bool ok = true;
     for (; ok && run.any; run.next(), ++n_units) {
       const int rows = run.x.ntok * p.G, row0 = run.en.row0 + run.at.u * p.tokens_per;
@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(kThreads, Small<HD>::kCtasPerSm)
       if (slot == 2 * (int)blockIdx.x + 1) rec = {row0, rows, run.at.h, run.last_cta()};
       for (int t = run.t0; ok && t < run.t1; ++t, ++g) {
         const int st = g % kStages;
-        if (!(ok = waitw<false>(&sh.empty[st], ((g / kStages) & 1) ^ 1, abort_flag))) break;
+        if (!(ok = !p.withhold && waitw<false>(&sh.empty[st], ((g / kStages) & 1) ^ 1, abort_flag))) break;
         const int key0 = tile_key(p, run.x, t);
         const int row = pages.row(p, run.en, run.at.h, key0);
         if (lane == 0) {
@@ -147,6 +147,7 @@ __global__ void __launch_bounds__(kThreads, Small<HD>::kCtasPerSm)
             tma_box(dst + K::kTileBytes, &p.map_k, row + kPageTok, 0, &sh.full[st]);
           }
         }
+        issued = g + 1;
         __syncwarp();
         if (t == run.t0) {
           // The unit's Q: 16 rows, row r of token r / G, 16-byte pieces swizzled
@@ -178,7 +179,7 @@ __global__ void __launch_bounds__(kThreads, Small<HD>::kCtasPerSm)
         }
       }
     }
-    int oldest = max(0, g - kStages);
+    int oldest = max(0, issued - kStages);
     if (ok) {
       const int st = g % kStages;
       if (waitw<false>(&sh.empty[st], ((g / kStages) & 1) ^ 1, abort_flag)) {
@@ -186,14 +187,14 @@ __global__ void __launch_bounds__(kThreads, Small<HD>::kCtasPerSm)
           sh.info[st].flags = kStop;
           mbar_arrive(&sh.full[st]);
         }
-        oldest = max(0, g - kStages + 1);  // the stage was free: its copy has landed
+        oldest = max(0, issued - kStages + 1);  // the stage was free: its copy has landed
       }
     }
     if (lane == 0) {
       p.rec[blockIdx.x] = rec;
       // No copy may still be landing when the CTA exits.
       volatile int never = 0;
-      for (int j = oldest; j < g; ++j) wait1<false>(&sh.full[j % kStages], (j / kStages) & 1, &never);
+      for (int j = oldest; j < issued; ++j) wait1<false>(&sh.full[j % kStages], (j / kStages) & 1, &never);
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else {
@@ -626,10 +627,10 @@ extern "C" int stv_paged_attn_workspace_bytes(const stv_shape* shape, int max_ne
   return STV_OK;
 }
 
-extern "C" int stv_paged_attn(const stv_shape* shape, const stv_attn_spec* spec, const stv_layer_cache* layer,
-                              const stv_page_pool* pool, const int32_t* seqs, int n, const int32_t* ctx,
-                              const int32_t* row_start, int max_new, const stv_rows* q, const stv_rows* o, int n_rows,
-                              void* workspace, size_t ws_bytes, int32_t* dev_status, stv_stream_t stream) {
+static int paged_attn(const stv_shape* shape, const stv_attn_spec* spec, const stv_layer_cache* layer,
+                      const stv_page_pool* pool, const int32_t* seqs, int n, const int32_t* ctx,
+                      const int32_t* row_start, int max_new, const stv_rows* q, const stv_rows* o, int n_rows,
+                      void* workspace, size_t ws_bytes, int32_t* dev_status, stv_stream_t stream, bool withhold) {
   RowShape sh;
   int rc = check_row_shape(shape, &sh);
   if (rc || (rc = check_row_layer(layer, sh))) return rc;
@@ -705,10 +706,29 @@ extern "C" int stv_paged_attn(const stv_shape* shape, const stv_attn_spec* spec,
   p.ml = reinterpret_cast<float2*>(ws + a.ml_at);
   p.part = reinterpret_cast<float*>(ws + a.part_at);
   p.part_rows = a.part_rows;
+  p.withhold = withhold;
   p.status = dev_status;
   cudaStream_t st = (cudaStream_t)stream;
   cudaError_t e = a.small ? launch_attn_small(p, sh.hd, sh.bf16, a.grid, st)
                           : launch_attn_tiles(p, sh.hd, sh.bf16, a.q_tiles, a.grid, st);
   if (e == cudaSuccess) e = launch_attn_join(p, sh.hd, sh.bf16, a.small, a.grid, st);
   return e == cudaSuccess ? STV_OK : STV_ERR_CUDA;
+}
+
+extern "C" int stv_paged_attn(const stv_shape* shape, const stv_attn_spec* spec, const stv_layer_cache* layer,
+                              const stv_page_pool* pool, const int32_t* seqs, int n, const int32_t* ctx,
+                              const int32_t* row_start, int max_new, const stv_rows* q, const stv_rows* o, int n_rows,
+                              void* workspace, size_t ws_bytes, int32_t* dev_status, stv_stream_t stream) {
+  return paged_attn(shape, spec, layer, pool, seqs, n, ctx, row_start, max_new, q, o, n_rows, workspace, ws_bytes,
+                    dev_status, stream, false);
+}
+
+extern "C" int stv_paged_attn_timeout_test(const stv_shape* shape, const stv_attn_spec* spec,
+                                           const stv_layer_cache* layer, const stv_page_pool* pool,
+                                           const int32_t* seqs, int n, const int32_t* ctx, const int32_t* row_start,
+                                           int max_new, const stv_rows* q, const stv_rows* o, int n_rows,
+                                           void* workspace, size_t ws_bytes, int32_t* dev_status,
+                                           stv_stream_t stream) {
+  return paged_attn(shape, spec, layer, pool, seqs, n, ctx, row_start, max_new, q, o, n_rows, workspace, ws_bytes,
+                    dev_status, stream, true);
 }

@@ -69,6 +69,9 @@ struct AttnParams {
   float2* ml;        // [2 * CTAs][part_rows]
   JoinRecord* rec;   // [CTAs]
   int part_rows;
+  // Failure-path test (stv_paged_attn_timeout_test): the producer stops before its
+  // first copy, so that every wait for one runs out.
+  bool withhold;
   int32_t* status;
 };
 

@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(Tiles<HD, NQ>::kThreads, 1)
       auto issue = [&](int row, bool v) {
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
-          if (!ok || !(ok = wait1<false>(&sh.empty[st], ph, abort_flag))) return;
+          if (!ok || !(ok = !p.withhold && wait1<false>(&sh.empty[st], ph, abort_flag))) return;
           uint8_t* dst = ring + st * kPiece;
           if (row < 0) {
             mbar_arrive(&sh.full[st]);
@@ -361,6 +361,7 @@ __global__ void __launch_bounds__(Tiles<HD, NQ>::kThreads, 1)
     // K-major tiles [hd / 64][128 rows][128 bytes], row r of token r / G.  Rows
     // past a row tile's keep what they held: a row's sums are its own.
     const int tile_tokens = p.tokens_per / NQ, tile_rows = tile_tokens * p.G;
+    int asked = 0;  // units whose Q has been asked for
     for (int n = 0;; ++n) {
       UnitInfo u;
       if (!unit_at(n, &u) || u.t1 == u.t0) break;
@@ -388,7 +389,11 @@ __global__ void __launch_bounds__(Tiles<HD, NQ>::kThreads, 1)
         fence_async_smem();
         mbar_arrive(&sh.q_full);
       }
+      asked = n + 1;
     }
+    // (the MMA warp has seen it land, unless the CTA aborted)
+    volatile int never = 0;
+    if (asked) wait1<false>(&sh.q_full, (asked - 1) & 1, &never);
   }
   } else {
     if (NQ == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftmaxRegs));
