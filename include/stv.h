@@ -739,8 +739,9 @@ typedef struct {
  *             all SMs and mma.sync does the products; past that, tiles of 128 rows
  *             on the tensor cores of tcgen05, split in the same way.
  *  q, o:      views of n_rows rows (heads = hq), of the cache's type; no
- *             element of o in q or in the cache; rows from row_start[n] on
- *             are left as they were.
+ *             element of o in q (o may be other columns of q's rows, or of
+ *             its heads), its extent not in the cache; rows from
+ *             row_start[n] on are left as they were.
  *  workspace: device, 16-byte aligned, at least
  *             stv_paged_attn_workspace_bytes(...) bytes; need not be cleared.
  *             Calls that overlap on the GPU need one each.

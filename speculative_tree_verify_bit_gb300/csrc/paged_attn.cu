@@ -597,16 +597,6 @@ int make_q_map(const stv_rows* q, const RowShape& sh, int n_rows, int tokens, CU
   return encode(map, sh.bf16, 4, q->data, dims, strides, box);
 }
 
-// Whether the bytes of two views can meet, by their extents.
-struct Extent {
-  uintptr_t a, b;
-};
-Extent extent_of(const stv_rows* v, int hd, int n_rows) {
-  const uintptr_t a = (uintptr_t)v->data;
-  return {a, a + 2 * ((n_rows - 1) * v->row_stride + (v->heads - 1) * v->head_stride + hd)};
-}
-bool meet(const Extent& x, const Extent& y) { return x.a < y.b && y.a < x.b; }
-
 }  // namespace
 
 cudaError_t launch_attn_small(const AttnParams& p, int hd, bool bf16, int grid, cudaStream_t s) {
@@ -645,13 +635,8 @@ static int paged_attn(const stv_shape* shape, const stv_attn_spec* spec, const s
   if (!ctx || !workspace || (uintptr_t)workspace % 16) return STV_ERR_INVALID_ARG;
   for (const stv_rows* v : {q, o})
     if (!rows_view_ok(v, sh.hd, n_rows) || v->heads != sh.hq || (uintptr_t)v->data % 2) return STV_ERR_INVALID_ARG;
-  // o's columns may lie beside q's in the same rows
-  if (meet(extent_of(q, sh.hd, n_rows), extent_of(o, sh.hd, n_rows))) {
-    const int64_t d = ((const uint8_t*)o->data - (const uint8_t*)q->data) / 2, st = q->row_stride;
-    const int64_t wide = (sh.hq - 1) * q->head_stride + sh.hd, wide_o = (sh.hq - 1) * o->head_stride + sh.hd;
-    const int64_t c = n_rows > 1 ? (d % st + st) % st : d;
-    if (n_rows == 1 || st != o->row_stride || c < wide || c + wide_o > st) return STV_ERR_INVALID_ARG;
-  }
+  // o's columns may lie beside q's in the same rows, or in the same heads
+  if (views_may_meet(q, o, sh.hd, n_rows, 2)) return STV_ERR_INVALID_ARG;
   if (rows_meet_pool(o, sh.hd, n_rows, layer)) return STV_ERR_INVALID_ARG;
   AttnPlan a;
   if ((rc = plan_attn(sh, max_new, &a))) return rc;

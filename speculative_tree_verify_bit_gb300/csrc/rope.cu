@@ -230,36 +230,6 @@ bool rows_ok(const stv_rows* v, int head_dim, int n_rows) {
   return n_rows <= 1 || v->row_stride >= (v->heads - 1) * v->head_stride + head_dim;
 }
 
-// Whether elements of a row of a and of one of b that starts d bytes after it
-// can meet: their extents (wa, wb) do, and they are not different columns of
-// heads with one stride.
-bool rows_may_meet(const stv_rows* a, const stv_rows* b, int64_t d, int64_t wa, int64_t wb, int head_dim, int64_t es) {
-  if (d >= wa || d + wb <= 0) return false;
-  if (a->heads == 1 && b->heads == 1) return true;
-  if (a->heads > 1 && b->heads > 1 && a->head_stride != b->head_stride) return true;
-  const int64_t st = (a->heads > 1 ? a : b)->head_stride * es, hw = head_dim * es;
-  const int64_t c = (d % st + st) % st;  // column of b's heads against a's
-  return !(c >= hw && c + hw <= st);
-}
-
-// Whether elements of two views can meet: their extents do, and they are not
-// different columns of rows with one stride, or in those of heads with one.
-bool may_meet(const stv_rows* a, const stv_rows* b, int head_dim, int n_rows, int64_t es) {
-  const int64_t wa = ((a->heads - 1) * a->head_stride + head_dim) * es;
-  const int64_t wb = ((b->heads - 1) * b->head_stride + head_dim) * es;
-  const uintptr_t a0 = (uintptr_t)a->data, b0 = (uintptr_t)b->data;
-  const uintptr_t a1 = a0 + (n_rows - 1) * a->row_stride * es + wa;
-  const uintptr_t b1 = b0 + (n_rows - 1) * b->row_stride * es + wb;
-  if (a1 <= b0 || b1 <= a0) return false;
-  const int64_t apart = (int64_t)(b0 - a0);
-  if (n_rows == 1) return rows_may_meet(a, b, apart, wa, wb, head_dim, es);
-  if (a->row_stride != b->row_stride) return true;
-  // a row is no longer than the stride, so of b's rows only the first at or
-  // after one of a's and the one before it can reach that
-  const int64_t st = a->row_stride * es, d = (apart % st + st) % st;
-  return rows_may_meet(a, b, d, wa, wb, head_dim, es) || rows_may_meet(a, b, d - st, wa, wb, head_dim, es);
-}
-
 bool same_view(const stv_rows* a, const stv_rows* b, int n_rows) {
   return a->data == b->data && (a->head_stride == b->head_stride || a->heads == 1) &&
          (a->row_stride == b->row_stride || n_rows == 1);
@@ -321,9 +291,9 @@ extern "C" int stv_rope(const stv_rope_spec* spec, int dtype, int head_dim, cons
   for (int t = 0; t < 2; ++t)
     for (int u = 0; u < 2; ++u) {
       if (out[t] && in[u] && !(t == u && same_view(in[u], out[t], n_rows)) &&
-          may_meet(out[t], in[u], head_dim, n_rows, es))
+          views_may_meet(out[t], in[u], head_dim, n_rows, es))
         return STV_ERR_INVALID_ARG;
-      if (t < u && out[t] && out[u] && may_meet(out[t], out[u], head_dim, n_rows, es)) return STV_ERR_INVALID_ARG;
+      if (t < u && out[t] && out[u] && views_may_meet(out[t], out[u], head_dim, n_rows, es)) return STV_ERR_INVALID_ARG;
     }
 
   memcpy(p.turn, turns_of(spec->theta, spec->rotary_dim), (size_t)half * sizeof(uint64_t));

@@ -267,6 +267,8 @@ int check_row_shape(const stv_shape* sh, RowShape* out);
 int check_row_layer(const stv_layer_cache* l, const RowShape& sh);
 // A view of rows of heads whose extents fit (api.cu).
 bool rows_view_ok(const stv_rows* v, int head_dim, int n_rows);
+// Whether elements of two such views, of es bytes, can meet.
+bool views_may_meet(const stv_rows* a, const stv_rows* b, int head_dim, int n_rows, int64_t es);
 // Whether the bytes of such a view meet those of a cache's pool.
 bool rows_meet_pool(const stv_rows* v, int head_dim, int n_rows, const stv_layer_cache* l);
 int device_sm_count(int* n);
