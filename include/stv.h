@@ -722,7 +722,7 @@ typedef struct {
   int32_t window; /* 0: no window; else >= 1: the row itself and the window - 1 before it */
   int32_t sinks;  /* >= 0: the first tokens that stay visible outside the window */
   int32_t causal; /* 1, or 0: a block whose rows see one another (a block drafter) */
-  float scale;    /* of q . k, finite and > 0; 0 for head_dim^-1/2 */
+  float scale;    /* of q . k, > 0 and times log2(e) finite; 0 for head_dim^-1/2 */
 } stv_attn_spec;
 
 /*

@@ -627,7 +627,8 @@ static int paged_attn(const stv_shape* shape, const stv_attn_spec* spec, const s
   if (!spec || !pool || !pool->tables || !pool->counts || !q || !o) return STV_ERR_INVALID_ARG;
   if (spec->window < 0 || spec->sinks < 0 || (spec->causal != 0 && spec->causal != 1)) return STV_ERR_INVALID_ARG;
   const float scale = spec->scale == 0.f ? 1.f / sqrtf((float)sh.hd) : spec->scale;
-  if (!(scale > 0.f) || isinf(scale)) return STV_ERR_INVALID_ARG;
+  const float scale2 = scale * 1.4426950408889634f;  // infinite times a score of 0 would be NaN
+  if (!(scale > 0.f) || isinf(scale2)) return STV_ERR_INVALID_ARG;
   if (pool->max_seqs < 1 || pool->table_stride < 1 || n < 0 || n_rows < 0 || max_new < 1) return STV_ERR_INVALID_ARG;
   if (n > kMaxEntries || n_rows > 1 << 29) return STV_ERR_SHAPE_UNSUPPORTED;
   if (!row_start && n_rows < n) return STV_ERR_INVALID_ARG;
@@ -685,7 +686,7 @@ static int paged_attn(const stv_shape* shape, const stv_attn_spec* spec, const s
   p.window = spec->window;
   p.sinks = spec->window ? spec->sinks : 0;
   p.causal = spec->causal;
-  p.scale2 = scale * 1.4426950408889634f;
+  p.scale2 = scale2;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.rec = reinterpret_cast<JoinRecord*>(ws);
   p.ml = reinterpret_cast<float2*>(ws + a.ml_at);

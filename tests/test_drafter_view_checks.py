@@ -1,4 +1,4 @@
-"""Which views of q and o stv_paged_attn takes: checked on the host, so no
+"""Which views of q and o, and which scales, stv_paged_attn takes: checked on the host, so no
 GPU is needed, nor used where there is one: the workspace is too small."""
 import pytest
 
@@ -27,4 +27,11 @@ ROW = 2 * HQ * HD
 ])
 def test_o_beside_q(lib, q, o, n_rows, fits):  # noqa: F811
     rc = call_attn(lib, q=q, o=o, n_rows=n_rows, n=1, s=shape(hd=HD), ws_bytes=0)
+    assert rc == BAD if not fits else rc in (SMALL, stv.STV_ERR_CUDA), rc
+
+
+@pytest.mark.parametrize("scale,fits", [(1e-45, True), (1.0, True), (2.3e38, True), (2.4e38, False), (3.4e38, False)])
+def test_scales(lib, scale, fits):  # noqa: F811
+    """The kernels multiply by scale log2(e), which has to be finite."""
+    rc = call_attn(lib, spec=stv.make_attn(scale=scale), ws_bytes=0)
     assert rc == BAD if not fits else rc in (SMALL, stv.STV_ERR_CUDA), rc
