@@ -681,7 +681,8 @@ int stv_page_copy(const stv_shape* shape, const stv_layer_cache* layers, int n_l
  *              row_start[i] <= r < row_start[i + 1].
  *   row_pos:   device int32 [max_rows] or NULL: ctx[s] + r - row_start[i].
  *              (row_seq and row_pos as stv_kv_append_pack takes them, its
- *              seqs being the list's.)
+ *              seqs being the list's; rows of -1 it leaves out and reports,
+ *              STV_DEV_BAD_ROW.)
  *   slots:     device int32 [max_rows] or NULL: page * 256 + row_pos % 256.
  * Entries from row_start[n] on are -1.  ctx is not changed.
  *  seqs: device int32 [n], distinct, or NULL: entry i is sequence i.
@@ -746,11 +747,16 @@ typedef struct {
  *             stv_paged_attn_workspace_bytes(...) bytes; need not be cleared.
  *             Calls that overlap on the GPU need one each.
  * Scores and softmax are formed in fp32, P is rounded to the cache's type for
- * P . V (sums in fp32), o rounded once.  The split depends on the lengths
- * alone and partials are joined in order: the result is the same every time.
+ * P . V (sums in fp32), o rounded once.  The softmax's sum takes P as rounded in
+ * the kernel of up to 16 rows and before the rounding in the other, which may be
+ * off by half a step of the type more where one key has most of the weight.  The
+ * split depends on the lengths alone and partials are joined in order: the result
+ * is the same every time.
  * Keys that no row of a tile sees are not read, or have no effect whatever
  * they hold: pages that lie outside window and first tokens may have been
- * given up (their table entries are not looked at).  Keys of a page past
+ * given up (their table entries are not looked at).  A key that some rows of a
+ * tile see and others do not counts 0 times V for the others, which is NaN
+ * where V is not finite.  Keys of a page past
  * counts[s], or on a table entry outside the pool, are left out
  * (STV_DEV_BAD_PAGE); a row without keys is zero.  An entry whose rows are not
  * within [0, n_rows) in ascending order, or are more than max_new, is left

@@ -25,10 +25,11 @@
 //
 // Bounds: the launch, two dependent loads, a pass, two cluster barriers and the
 // second reading, one after the other, for few sequences (one chain over 248,320
-// fp32 tokens 7.1 us; 8 trees of 16 nodes in bf16 36 us, at most six rejections at a
+// fp32 tokens 7.1 us; 8 trees of 16 nodes in bf16 37 us, at most six rejections at a
 // node, 12,000 cycles each: the pass 6,000, barriers 2,000, the walk's own steps
-// 3,500); HBM and instruction issue for many (64 chains without draft rows 17.5 us,
-// 64 MB).
+// 3,500).  For many, that chain and the bytes one after the other, since all clusters
+// run in step (64 chains without draft rows 17.6 us; their 64 MB take 9.4 at the copy
+// bandwidth, and DRAM is busy 36 % of the time).
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <math.h>

@@ -666,8 +666,11 @@ static int paged_attn(const stv_shape* shape, const stv_attn_spec* spec, const s
     if (p.q_wide && make_q_map(q, sh, n_rows, kMaxRows / sh.G, &p.map_q)) p.q_wide = false;
   }
   p.tile_bits = a.small ? 6 : 7;
-  // Measured: 64 ragged single tokens of 128 channels take 82, 78, 69 and 66 us at 0, 1,
-  // 2 and 4; prompts 4 % and 18 % more at 2 and 1 than at 3, as much at 5.
+  // Measured: 64 ragged single tokens of 128 channels take 86, 75, 72 and 74 us at 0, 2,
+  // 4 and 8; of 256 channels 92, 86, 83 and 83 at 0, 1, 2 and 4; of 64 (8 KV heads) 93, 74,
+  // 76 and 81 at 0, 4, 8 and 16.  A windowed prompt of 256 channels takes 4 % and 18 % more
+  // at 2 and 1 than at 3, as much at 5; 8,192 tokens of 64 channels 374, 371, 370 and 378 us
+  // at 1, 2, 3 and 5.
   p.unit_cost = a.small ? 512 / sh.hd : 3;
   p.tables = pool->tables;
   p.counts = pool->counts;

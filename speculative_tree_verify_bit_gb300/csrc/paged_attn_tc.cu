@@ -591,7 +591,9 @@ __global__ void __launch_bounds__(Tiles<HD, NQ>::kThreads, 1)
           }
         }
         // P = 2^(S c - m_ref + kLift), rounded to the cache's type, packed in key pairs into
-        // S's columns; the row's sum takes it before the rounding.
+        // S's columns.  The row's sum takes it before the rounding: as rounded, where a
+        // large key's own rounding cancels, an 8,192-token prompt of 128 channels takes 381
+        // us for 342 and one of 256 through a window 388 for 329.
         const float mref = (m_ref == -INFINITY ? 0.f : m_ref) - kLift<T>;
         const float2 c2 = make_float2(c, c), nm2 = make_float2(-mref, -mref);
         float2 sum4[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
