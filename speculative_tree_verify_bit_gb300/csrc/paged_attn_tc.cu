@@ -24,8 +24,10 @@
 //
 // Measured (2,070 MHz maximum): an 8,192-token prompt of 24 / 4 heads of 128 takes
 // 342 us, 1,206 TFLOP/s (0.63 of the measured bf16 peak); 32,768 tokens of heads of
-// 256 through a window of 2,048, 1,380 us, 1,167 TFLOP/s (0.60); the tensor pipe
-// is busy 55 % of the time.  Heads of 256: a step takes 2,500 cycles where its MMAs
+// 256 through a window of 2,048, 1,330 us, 1,210 TFLOP/s (0.63), and 1,430 to 1,475 in a
+// long row of calls, where the power limit takes the clock to 1,850 to 1,950 MHz; 2,048
+// tokens over 100,000 cached ones 1,750 us with heads of 128 (0.75), 4,090 of 256 (0.64),
+// 1,897 of 64 (0.46).  The tensor pipe is busy 55 % of the time.  Heads of 256: a step takes 2,500 cycles where its MMAs
 // take 2,304 (K and V cross shared memory once per 128 rows, 57 bytes a cycle and
 // SM), and a unit's end 8,000 more: two or three masked tiles and O on its way out.
 // Heads of 128: a row tile's turn is its softmax (1,700 cycles, two row tiles' on
